@@ -2,7 +2,8 @@
 
 Every step runs in the HIP kernels behind the C ABI declared in
 ``include/qknorm_rope.h`` (fused QK-norm + RoPE), ``include/fuse_scale_shift.h``
-(AdaLN modulation) and ``include/group_norm_silu.h`` (group norm + SiLU);
+(AdaLN modulation), ``include/group_norm_silu.h`` (group norm + SiLU) and
+``include/dit_attention.h`` (attention and its backward pass);
 this module turns torch
 tensors into device pointers, sizes and enum codes and raises on a non-zero
 status.  There is no fallback: if the library is missing, loading fails
@@ -34,7 +35,9 @@ TENSORS = {"fused": QKR_TENSORS_FUSED, "pair": QKR_TENSORS_PAIR, "one": QKR_TENS
 EXPORTS = ("qknorm_rope_fused", "qknorm_rope_strerror", "qknorm_rope_version",
            "qknorm_rope_kernel_info", "dit_fuse_scale_shift",
            "dit_group_norm_silu_workspace_size", "dit_group_norm_silu_schedule",
-           "dit_group_norm_silu", "dit_group_norm_silu_noalloc")
+           "dit_group_norm_silu", "dit_group_norm_silu_noalloc",
+           "dit_attention_workspace_size", "dit_attention_backward_workspace_size",
+           "dit_attention", "dit_attention_backward")
 MOD_DTYPES = {"bf16": QKR_BF16, "fp16": QKR_FP16, "fp32": QKR_FP32}
 
 
@@ -52,6 +55,19 @@ class KernelInfo(ctypes.Structure):
                 ("tokens_per_block", ctypes.c_int32), ("heads_in_flight", ctypes.c_int32),
                 ("die_runs", ctypes.c_int32), ("dynamic_lds_bytes", ctypes.c_int32),
                 ("workgroups_per_cu", ctypes.c_int32)]
+
+
+class AttnTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class AttnArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("q_tokens", ctypes.c_int64),
+                ("kv_tokens", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("kv_lengths", ctypes.c_void_p)]
 
 
 _lib = None
@@ -97,6 +113,14 @@ def load_library(path: str = LIB_PATH):
     lib.dit_group_norm_silu_noalloc.argtypes = [vp, vp, i64, i32, i64, i32, vp, vp, i32, f32,
                                                 i32, vp]
     lib.dit_group_norm_silu_noalloc.restype = ctypes.c_int
+    args, tensor = ctypes.POINTER(AttnArgs), ctypes.POINTER(AttnTensor)
+    for name in ("dit_attention_workspace_size", "dit_attention_backward_workspace_size"):
+        getattr(lib, name).argtypes = [args]
+        getattr(lib, name).restype = i64
+    lib.dit_attention.argtypes = [args, *[tensor] * 4, vp, vp, i64, vp]
+    lib.dit_attention.restype = ctypes.c_int
+    lib.dit_attention_backward.argtypes = [args, *[tensor] * 5, vp, *[tensor] * 3, vp, i64, vp]
+    lib.dit_attention_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -414,3 +438,152 @@ def group_norm_silu(x, gamma, beta, groups: int, *, out=None, eps: float = 1e-6,
                                          _x_code(x), _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return out
+
+
+def _attn_tensor(t) -> AttnTensor:
+    b, n, h, _ = t.stride()
+    return AttnTensor(t.data_ptr(), b, n, h)
+
+
+def _attn_view(t, name: str):
+    """[tokens, heads, head_dim] counts as one sample."""
+    if t.dim() == 3:
+        t = t.unsqueeze(0)
+    if t.dim() != 4:
+        raise ValueError("%s must be [batch, tokens, heads, head_dim]" % name)
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    return t
+
+
+def _attn_args(q, k, v, causal, kv_lengths, scale) -> AttnArgs:
+    torch = _torch()
+    batch, q_tokens, heads, head_dim = q.shape
+    if k.shape != v.shape or k.shape[0] != batch or k.shape[3] != head_dim:
+        raise ValueError("k and v must be [%d, kv_tokens, kv_heads, %d]" % (batch, head_dim))
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have one dtype")
+    kv_heads = k.shape[2]
+    if kv_heads < 1 or heads % kv_heads:
+        raise ValueError("the number of query heads must be a multiple of k's and v's")
+    if kv_lengths is not None and (kv_lengths.dtype != torch.int32 or kv_lengths.shape != (batch,)):
+        raise ValueError("kv_lengths must be int32 [batch]")
+    if scale is None:
+        scale = head_dim ** -0.5
+    return AttnArgs(batch, q_tokens, k.shape[1], heads, kv_heads, head_dim, 1 if causal else 0,
+                    _x_code(q), scale, _ptr(kv_lengths) or None)
+
+
+def _lse_shape(q):
+    return (*q.shape[:-3], q.shape[-2], q.shape[-3])
+
+
+def _check_lse(lse, q):
+    if tuple(lse.shape) != _lse_shape(q) or lse.dtype != _torch().float32:
+        raise ValueError("lse must be float32 [batch, heads, tokens]")
+
+
+def _attn_workspace(size_of, args, workspace, device):
+    """(workspace, its bytes), allocated here if the call needs one and has none."""
+    if workspace is None:
+        need = int(size_of(ctypes.byref(args)))
+        if need < 0:
+            raise QkrError(need, strerror(need))
+        if need > 0:
+            workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def attention_workspace_size(batch: int, q_tokens: int, kv_tokens: int, heads: int, kv_heads: int,
+                             head_dim: int, *, causal: bool = False, dtype: int = QKR_BF16,
+                             backward: bool = False) -> int:
+    """Workspace bytes of an attention call, or of its backward pass (negative:
+    a QKR_ERR_* code for bad sizes)."""
+    lib = load_library()
+    args = AttnArgs(batch, q_tokens, kv_tokens, heads, kv_heads, head_dim, 1 if causal else 0, dtype,
+                    1.0, None)
+    size_of = lib.dit_attention_backward_workspace_size if backward else lib.dit_attention_workspace_size
+    return int(size_of(ctypes.byref(args)))
+
+
+def attention(q, k, v, *, causal: bool = False, kv_lengths=None, scale: float | None = None,
+              out=None, lse=None, workspace=None, stream=None):
+    """Attention (see ``include/dit_attention.h``); returns ``(out, lse)``.
+
+    ``q``: [batch, tokens, heads, head_dim], ``k``/``v``: [batch, kv_tokens,
+    kv_heads, head_dim] of bfloat16 or float16 (or without the batch dimension
+    for one sample); any strides that are multiples of 8 with the last
+    dimension contiguous, so the slices of a fused QKV buffer serve as they
+    are.  ``heads`` is a multiple of ``kv_heads``; consecutive query heads
+    share a key head.  ``kv_lengths``: int32 [batch], the keys in use of each
+    sample.  ``causal``: the last query sees the last key of kv_tokens, the
+    one before it one key fewer.  ``scale`` defaults to head_dim ** -0.5.
+    ``out`` (like q, same rules for strides) and ``lse`` (float32 [batch,
+    heads, tokens], the log of each row's sum of exponentials, which the
+    backward pass takes) default to new tensors.  ``workspace``: a device
+    tensor of at least ``attention_workspace_size`` bytes; allocated here on
+    the launch stream when None and one is needed.
+    """
+    torch = _torch()
+    lib = load_library()
+    q4, k4, v4 = _attn_view(q, "q"), _attn_view(k, "k"), _attn_view(v, "v")
+    args = _attn_args(q4, k4, v4, causal, kv_lengths, scale)
+    with _launch_stream_context(q, stream):
+        workspace, ws_bytes = _attn_workspace(lib.dit_attention_workspace_size, args, workspace,
+                                              q.device)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(_lse_shape(q), dtype=torch.float32, device=q.device)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must match q in shape and dtype")
+    _check_lse(lse, q)
+    ctx, stream_ptr = _call_context(q, (k, v, out, lse, kv_lengths, workspace), stream)
+    with ctx:
+        status = lib.dit_attention(
+            ctypes.byref(args), *[ctypes.byref(_attn_tensor(t)) for t in (q4, k4, v4,
+                                                                        _attn_view(out, "out"))],
+            _ptr(lse) or None, _ptr(workspace) or None, ws_bytes, stream_ptr or None)
+    _check(status)
+    return out, lse
+
+
+def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, kv_lengths=None,
+                       scale: float | None = None, dq=None, dk=None, dv=None, workspace=None,
+                       stream=None):
+    """Backward pass of ``attention``; returns ``(dq, dk, dv)``.
+
+    ``dout`` is the gradient of ``out``; ``q``, ``k``, ``v``, ``out``, ``lse``
+    and the masks are the forward call's.  ``dq``, ``dk`` and ``dv`` are
+    written (not added to) and default to new contiguous tensors; they may be
+    the slices of one fused gradient buffer.  Tensors follow the forward
+    call's rules; a dout without its own memory for every token (an expanded
+    one) has to be made contiguous first.
+    """
+    torch = _torch()
+    lib = load_library()
+    q4, k4, v4 = _attn_view(q, "q"), _attn_view(k, "k"), _attn_view(v, "v")
+    args = _attn_args(q4, k4, v4, causal, kv_lengths, scale)
+    with _launch_stream_context(q, stream):
+        workspace, ws_bytes = _attn_workspace(lib.dit_attention_backward_workspace_size, args,
+                                              workspace, q.device)
+        dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if t is None else t
+                      for t, x in ((dq, q), (dk, k), (dv, v)))
+    for name, t, like in (("dout", dout, q), ("out", out, q), ("dq", dq, q), ("dk", dk, k),
+                          ("dv", dv, v)):
+        if t.shape != like.shape or t.dtype != like.dtype:
+            raise ValueError("%s must match %s in shape and dtype"
+                             % (name, {"dk": "k", "dv": "v"}.get(name, "q")))
+    _check_lse(lse, q)
+    ctx, stream_ptr = _call_context(q, (dout, k, v, out, lse, dq, dk, dv, kv_lengths, workspace),
+                                    stream)
+    with ctx:
+        t = [ctypes.byref(_attn_tensor(_attn_view(x, name)))
+             for x, name in ((dout, "dout"), (q4, "q"), (k4, "k"), (v4, "v"), (out, "out"),
+                             (dq, "dq"), (dk, "dk"), (dv, "dv"))]
+        status = lib.dit_attention_backward(ctypes.byref(args), *t[:5], _ptr(lse) or None, *t[5:],
+                                            _ptr(workspace) or None, ws_bytes, stream_ptr or None)
+    _check(status)
+    return dq, dk, dv

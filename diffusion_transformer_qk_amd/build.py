@@ -1,5 +1,6 @@
 """Compile the HIP library ``libqknorm_rope.so`` for gfx950 with hipcc (and,
-beside it, bench.py's data-movement probe ``bench_floor.so``).
+beside it, ``libdit_attention.so``, which holds the matrix-core kernels and
+which it depends on, and bench.py's data-movement probe ``bench_floor.so``).
 
 Usage:  python -m diffusion_transformer_qk_amd.build [--save-temps DIR]
 """
@@ -17,6 +18,13 @@ SRCS = [os.path.join(PKG, "csrc", "qknorm_rope.hip"),
         os.path.join(PKG, "csrc", "group_norm_silu.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqknorm_rope.so")
+# The attention kernels: a library of their own, because every kernel of
+# libqknorm_rope.so is memory-bound work without matrix instructions and the
+# tests hold its whole code to that.  libqknorm_rope.so names it as a
+# dependency beside itself, so one library is still all that a caller links.
+ATTN_SRCS = [os.path.join(PKG, "csrc", "attention_forward.hip"),
+             os.path.join(PKG, "csrc", "attention_backward.hip")]
+ATTN_LIB = os.path.join(PKG, "libdit_attention.so")
 # bench.py's data-movement probe: its own library, outside libqknorm_rope.so
 FLOOR_SRC = os.path.join(ROOT, "bench_floor.hip")
 FLOOR_LIB = os.path.join(ROOT, "bench_floor.so")
@@ -52,16 +60,21 @@ def build(save_temps: str | None = None) -> str:
     whole build runs as one hipcc call that keeps its ISA/IR there.
     """
     tmp = LIB + ".tmp%d" % os.getpid()
+    attn_tmp = ATTN_LIB + ".tmp%d" % os.getpid()
+    needs_attn = ["-L", PKG, "-Wl,--no-as-needed", "-ldit_attention", "-Wl,-rpath,$ORIGIN"]
+    attn_name = "-Wl,-soname," + os.path.basename(ATTN_LIB)
     if save_temps:
         os.makedirs(save_temps, exist_ok=True)
-        cmd = [hipcc(), "--save-temps", *HIPCC_FLAGS, "-I", INCLUDE, *SRCS, "-o", tmp]
-        subprocess.run(cmd, check=True, cwd=save_temps)
-        os.replace(tmp, LIB)
+        for srcs, out, lib, link in ((ATTN_SRCS, attn_tmp, ATTN_LIB, [attn_name]),
+                                     (SRCS, tmp, LIB, needs_attn)):
+            cmd = [hipcc(), "--save-temps", *HIPCC_FLAGS, "-I", INCLUDE, *srcs, *link, "-o", out]
+            subprocess.run(cmd, check=True, cwd=save_temps)
+            os.replace(out, lib)
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
     objs, procs = [], []
-    for src in SRCS:
+    for src in SRCS + ATTN_SRCS:
         obj = os.path.join(OBJ_DIR, os.path.basename(src) + ".o")
         objs.append(obj)
         procs.append((src, subprocess.Popen([hipcc(), *compile_flags, "-I", INCLUDE, "-c", src,
@@ -73,8 +86,10 @@ def build(save_temps: str | None = None) -> str:
     failed = [src for src, proc in procs if proc.wait() != 0]
     if failed:
         raise RuntimeError("hipcc failed on " + ", ".join(failed))
-    subprocess.run([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", *objs, "-o", tmp],
-                   check=True)
+    link = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC"]
+    subprocess.run([*link, *objs[len(SRCS):], attn_name, "-o", attn_tmp], check=True)
+    os.replace(attn_tmp, ATTN_LIB)
+    subprocess.run([*link, *objs[:len(SRCS)], *needs_attn, "-o", tmp], check=True)
     os.replace(tmp, LIB)
     os.replace(floor_tmp, FLOOR_LIB)
     return LIB

@@ -1,0 +1,576 @@
+// attention_backward.hip -- attention backward for gfx950 (see dit_attention.h).
+//
+// Three kernels on one stream:
+//   rows: lse (in base 2) and delta = dout . out of every query, and for fp16
+//         the norms that bound dout . v;
+//   dkv:  a wave owns 32 keys, keeps their k, v, dk and dv in registers and
+//         walks the queries: S = Q K^T and dP = dO V^T come out with queries
+//         down the registers, so packed P and dS are the B operands of
+//         dV^T = dO^T P and dK^T = Q^T dS as they stand;
+//   dq:   a wave owns 32 query rows and walks the keys, with S^T = K Q^T,
+//         dP^T = V dO^T and dQ^T = K^T dS^T.
+// The scores are computed twice (7 products instead of 5), because the other
+// way, one walk that adds to dQ from every key block, needs fp32 atomic
+// additions: their order changes the result from run to run, and their
+// traffic is Sk / (keys of a workgroup) times the size of dQ in fp32.
+//
+// fp16: p = exp(s - lse) is about 1 / keys, and ds that times the gradient's
+// size; both would sink into fp16's subnormals.  p is computed times 2^15
+// (p <= 1), and dp - delta, which the norms of dout and v bound, is brought
+// below 1 by a power of two (of a query in dq; of a whole key head in dkv,
+// where queries are summed); the sums are scaled back in fp32.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "attention_common.h"
+#include "attention_host.h"
+#include "dit_attention.h"
+
+namespace {
+
+using namespace qkr_attn;
+
+struct BwdParams {
+    const uint16_t *dout, *q, *k, *v, *out;
+    const float* lse;
+    uint16_t *dq, *dk, *dv;
+    const int32_t* kv_lengths;
+    int64_t do_bs, do_ts, do_hs, q_bs, q_ts, q_hs, k_bs, k_ts, k_hs, v_bs, v_ts, v_hs;
+    int64_t o_bs, o_ts, o_hs, dq_bs, dq_ts, dq_hs, dk_bs, dk_ts, dk_hs, dv_bs, dv_ts, dv_hs;
+    int64_t batch;
+    int32_t q_tokens, kv_tokens, heads, kv_heads, group, rows;
+    int32_t row_blocks, key_blocks;
+    float scale, c;                           // c = scale * log2(e)
+    float* stats;                             // [batch][heads][q_tokens][lse2, delta]
+    uint32_t* norms;                          // [batch][kv_heads][|dout|, |v|]: largest row norms (fp16)
+};
+
+template <bool F16>
+constexpr float p_shift() { return F16 ? 15.0f : 0.0f; }
+
+// Exponent e of a bound on |dp|: |dp - delta| * 2^(-e - 1) <= 1.
+__device__ __forceinline__ int bound_exponent(float bound)
+{
+    // a bound that is 0, infinite or NaN scales nothing
+    if (!(bound > 0.0f && bound <= 0x1.fffffep127f))
+        return -1;
+    return __builtin_amdgcn_frexp_expf(bound);
+}
+
+__global__ __launch_bounds__(256) void clear_norms_kernel(uint32_t* norms, int64_t n)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n)
+        norms[i] = 0;
+}
+
+// D / 8 lanes a row of (sample, head, query); a workgroup covers 256 / (D / 8)
+// queries of one head.  fp16: also the largest |dout| row of the key head
+// (norms are not negative, so their bits compare as integers, and a maximum
+// does not depend on the order of the atomics).
+template <int D, bool F16>
+__global__ __launch_bounds__(256)
+void row_stats_kernel(const BwdParams p)
+{
+    constexpr int L = D / 8, R = 256 / L;
+    const int64_t blocks = (p.q_tokens + R - 1) / R;
+    const int64_t bh = blockIdx.x / blocks;
+    const int64_t b = bh / p.heads;
+    const int h = bh % p.heads;
+    const int qi = (int)(blockIdx.x % blocks) * R + threadIdx.x / L;
+    const int d0 = threadIdx.x % L * 8;
+    float dot = 0.0f, sq = 0.0f;
+    if (qi < p.q_tokens) {
+        float x[8], y[8];
+        unpack8<F16>(load16<false>(p.dout + b * p.do_bs + qi * p.do_ts + h * p.do_hs + d0), x);
+        unpack8<F16>(load16<false>(p.out + b * p.o_bs + qi * p.o_ts + h * p.o_hs + d0), y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dot = __builtin_fmaf(x[i], y[i], dot);
+            if (F16)
+                sq = __builtin_fmaf(x[i], x[i], sq);
+        }
+    }
+#pragma unroll
+    for (int w = 1; w < L; w *= 2) {
+        dot += __shfl_xor(dot, w);
+        if (F16)
+            sq += __shfl_xor(sq, w);
+    }
+    if (qi < p.q_tokens && threadIdx.x % L == 0) {
+        const float lse = p.lse[bh * p.q_tokens + qi];
+        // a query without keys: exp2(s - inf) is 0 for every score
+        const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+        reinterpret_cast<f32x2*>(p.stats)[bh * p.q_tokens + qi] = f32x2{lse2, dot};
+    }
+    if constexpr (F16) {
+        const float top = wave_max(sq);
+        if (threadIdx.x % 64 == 0)
+            atomicMax(p.norms + (b * p.kv_heads + h / p.group) * 2, __float_as_uint(sqrtf(top)));
+    }
+}
+
+// fp16: the largest row norm of each sample's and key head's values in use.
+template <int D>
+__global__ __launch_bounds__(256)
+void value_norms_kernel(const BwdParams p)
+{
+    constexpr int L = D / 8, R = 256 / L;
+    const int64_t blocks = (p.kv_tokens + R - 1) / R;
+    const int64_t bh = blockIdx.x / blocks;
+    const int64_t b = bh / p.kv_heads;
+    const int j = (int)(blockIdx.x % blocks) * R + threadIdx.x / L;
+    int len = p.kv_tokens;
+    if (p.kv_lengths && p.kv_lengths[b] < len)
+        len = p.kv_lengths[b];
+    float sq = 0.0f;
+    if (j < len) {
+        float x[8];
+        unpack8<true>(load16<false>(p.v + b * p.v_bs + j * p.v_ts + (bh % p.kv_heads) * p.v_hs +
+                                    threadIdx.x % L * 8), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sq = __builtin_fmaf(x[i], x[i], sq);
+    }
+#pragma unroll
+    for (int w = 1; w < L; w *= 2)
+        sq += __shfl_xor(sq, w);
+    const float top = wave_max(sq);
+    if (threadIdx.x % 64 == 0)
+        atomicMax(p.norms + bh * 2 + 1, __float_as_uint(sqrtf(top)));
+}
+
+// ---------------------------------------------------------------- dk and dv
+
+// DS waves share a block of 32 keys: each computes its scores and keeps
+// 1 / DS of the columns of its dk and dv (head_dim 256, whose 256 accumulators
+// and 128 registers of k and v would not fit beside the products' operands).
+// The queries are taken 32 at a time.
+template <int D, bool F16, bool CAUSAL, int NW, int DS>
+__global__ __launch_bounds__(NW * 64, 1)
+void attention_dkv_kernel(const BwdParams p)
+{
+    constexpr int BK = NW / DS * 32, BQ = 32, DB = D / 32 / DS;
+    constexpr int kTile = BQ * D * 2;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile + 2 * BQ * 8];
+    const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+
+    const int64_t block = logical_block<-1>(blockIdx.x, gridDim.x);
+    const int kb = block % p.key_blocks;
+    const int64_t bh = block / p.key_blocks;
+    const int64_t b = bh / p.kv_heads;
+    const int hk = bh % p.kv_heads;
+    int len = p.kv_tokens;
+    if (p.kv_lengths) {
+        const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
+        len = given < 0 ? 0 : given < len ? given : len;
+    }
+    const int shift = p.kv_tokens - p.q_tokens;
+    const int k0 = kb * BK + wave / DS * 32;              // the wave's first key
+    const int key = k0 + n;                               // this lane's
+    const int db0 = DS == 1 ? 0 : wave % DS * DB;         // the wave's first column block
+    // the first query that sees one of the workgroup's keys, in whole tiles
+    int first = 0;
+    if (CAUSAL) {
+        const int i = kb * BK - shift;
+        first = i > 0 ? i / BQ : 0;
+    }
+    const int tiles = (p.q_tokens + BQ - 1) / BQ;
+    const int per = tiles > first ? tiles - first : 0;    // tiles of one query head
+    const int total = kb * BK < len ? per * p.group : 0;
+
+    u32x4 kf[D / 16], vf[D / 16];
+    {
+        const uint16_t* kr = p.k + b * p.k_bs + (int64_t)key * p.k_ts + hk * p.k_hs + 8 * g;
+        const uint16_t* vr = p.v + b * p.v_bs + (int64_t)key * p.v_ts + hk * p.v_hs + 8 * g;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            kf[kk] = key < len ? load16<false>(kr + 16 * kk) : u32x4{0, 0, 0, 0};
+            vf[kk] = key < len ? load16<false>(vr + 16 * kk) : u32x4{0, 0, 0, 0};
+        }
+    }
+    float down = 1.0f;            // brings dp - delta below 1
+    int e = 0;
+    if constexpr (F16) {
+        e = bound_exponent(__uint_as_float(p.norms[bh * 2]) * __uint_as_float(p.norms[bh * 2 + 1])) + 1;
+        down = __builtin_amdgcn_ldexpf(1.0f, -e);
+    }
+    f32x16 dk[DB], dv[DB];
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+        dk[i] = dv[i] = f32x16{};
+
+    Stager<D, BQ, NW> qs, dos;
+    qs.init(wave, lane, p.q_ts);
+    dos.init(wave, lane, p.do_ts);
+    const uint32_t lds0 = lds_address(lds);
+    const uint32_t at_row = row_offset<D>(lane), at_tr = tr_offset<D>(lane);
+
+    // tile t: query tile first + t % per of the group's head t / per
+    const auto stage = [&](int t, int buf) {
+        const int h = hk * p.group + t / per;
+        const int q0 = (first + t % per) * BQ;
+        const int left = p.q_tokens - q0;
+        const uint32_t to = lds0 + buf * 2 * kTile;
+        qs.load(p.q + b * p.q_bs + (int64_t)q0 * p.q_ts + h * p.q_hs, p.q_ts, left, to, wave);
+        dos.load(p.dout + b * p.do_bs + (int64_t)q0 * p.do_ts + h * p.do_hs, p.do_ts, left, to + kTile,
+                 wave);
+        if (wave == 0) {          // lse2 and delta: zero past the last query, as are its rows
+            const int rows = left < BQ ? left : BQ;
+            const uint64_t a = reinterpret_cast<uint64_t>(
+                p.stats + ((b * p.heads + h) * p.q_tokens + q0) * 2);
+            const u32x4 rsrc = {scalar((uint32_t)a), scalar((uint32_t)(a >> 32) & 0xffffu),
+                                scalar(rows * 8), kRawBuffer};
+            dma4(rsrc, lane * 4, lds0 + 4 * kTile + buf * BQ * 8);
+        }
+    };
+
+    if (total > 0)
+        stage(0, 0);
+    for (int t = 0; t < total; ++t) {
+        const int buf = t & 1;
+        wait_staged();
+        __syncthreads();
+        if (t + 1 < total)
+            stage(t + 1, buf ^ 1);
+        const char* qt = lds + buf * 2 * kTile;
+        const char* dot = qt + kTile;
+        const float* st = reinterpret_cast<const float*>(lds + 4 * kTile + buf * BQ * 8);
+        const int q0 = (first + t % per) * BQ;
+        if (k0 >= len || (CAUSAL && k0 > q0 + BQ - 1 + shift))
+            continue;             // no query of the tile sees a key of the wave
+
+        f32x16 s{}, dp{};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+            s = mfma<F16>(row_fragment<D>(qt, at_row, 0, kk), kf[kk], s);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+            dp = mfma<F16>(row_fragment<D>(dot, at_row, 0, kk), vf[kk], dp);
+        const bool diagonal = CAUSAL && k0 + 31 > q0 + shift;
+#pragma unroll
+        for (int i4 = 0; i4 < 4; ++i4) {
+            const f32x4 a = *reinterpret_cast<const f32x4*>(st + 2 * (8 * i4 + 4 * g));
+            const f32x4 c = *reinterpret_cast<const f32x4*>(st + 2 * (8 * i4 + 4 * g) + 4);
+            const float lse2[4] = {a[0], a[2], c[0], c[2]};
+            const float delta[4] = {a[1], a[3], c[1], c[3]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = 4 * i4 + i;
+                float pr = __builtin_amdgcn_exp2f(
+                    __builtin_fmaf(s[at], p.c, p_shift<F16>() - lse2[i]));
+                if (diagonal && key > q0 + 8 * i4 + 4 * g + i + shift)
+                    pr = 0.0f;
+                s[at] = pr;
+                dp[at] = F16 ? pr * ((dp[at] - delta[i]) * down) : pr * (dp[at] - delta[i]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const u32x4 pf = pack_b<F16>(s, k), sf = pack_b<F16>(dp, k);
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+                dv[i] = mfma<F16>(tr_fragment<D>(dot, at_tr, 0, k, db0 + i), pf, dv[i]);
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+                dk[i] = mfma<F16>(tr_fragment<D>(qt, at_tr, 0, k, db0 + i), sf, dk[i]);
+        }
+    }
+
+    const bool valid = key < p.kv_tokens;
+    const int at = valid ? key : p.kv_tokens - 1;
+    uint16_t* kr = p.dk + b * p.dk_bs + (int64_t)at * p.dk_ts + hk * p.dk_hs + 32 * db0;
+    uint16_t* vr = p.dv + b * p.dv_bs + (int64_t)at * p.dv_ts + hk * p.dv_hs + 32 * db0;
+    const float fv = F16 ? 0x1p-15f : 1.0f;
+    const float fk = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
+#pragma unroll
+    for (int i = 0; i < DB; ++i) {
+        if (key >= len)           // the scores of a padding key are no scores
+            dk[i] = dv[i] = f32x16{};
+        store_column<F16>(kr + 32 * i, dk[i], fk, g, valid);
+        store_column<F16>(vr + 32 * i, dv[i], fv, g, valid);
+    }
+}
+
+// ---------------------------------------------------------------- dq
+
+template <int D, bool F16, bool CAUSAL, int NW, int BN>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2)
+void attention_dq_kernel(const BwdParams p)
+{
+    constexpr int BM = NW * 32, KB = BN / 32, DB = D / 32;
+    constexpr int kTile = BN * D * 2;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];
+    const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+
+    const int64_t block = logical_block<-1>(blockIdx.x, gridDim.x);
+    const int mb_raw = block % p.row_blocks;
+    const int64_t bh = block / p.row_blocks;
+    const int64_t b = bh / p.kv_heads;
+    const int hk = bh % p.kv_heads;
+    const int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;
+    int len = p.kv_tokens;
+    if (p.kv_lengths) {
+        const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
+        len = given < 0 ? 0 : given < len ? given : len;
+    }
+    const int r0 = mb * BM + wave * 32;
+    const int r = r0 + n < p.rows ? r0 + n : p.rows - 1;
+    const int qi = r / p.group, head = hk * p.group + r % p.group;
+    const int shift = p.kv_tokens - p.q_tokens;
+    int end = len;
+    if (CAUSAL) {
+        const int last = (mb * BM + BM < p.rows ? mb * BM + BM : p.rows) - 1;
+        const int sees = last / p.group + shift + 1;
+        end = sees < end ? (sees < 0 ? 0 : sees) : end;
+    }
+    const int tiles = (end + BN - 1) / BN;
+    int open = len;
+    if (CAUSAL) {
+        const int s = (r0 < p.rows ? r0 : p.rows - 1) / p.group + shift + 1;
+        open = s < open ? s : open;
+    }
+
+    u32x4 qf[D / 16], df[D / 16];
+    {
+        const uint16_t* qr = p.q + b * p.q_bs + qi * p.q_ts + head * p.q_hs + 8 * g;
+        const uint16_t* dr = p.dout + b * p.do_bs + qi * p.do_ts + head * p.do_hs + 8 * g;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            qf[kk] = load16<false>(qr + 16 * kk);
+            df[kk] = load16<false>(dr + 16 * kk);
+        }
+    }
+    const f32x2 st = reinterpret_cast<const f32x2*>(p.stats)[(b * p.heads + head) * p.q_tokens + qi];
+    const float lse2 = st.x - p_shift<F16>(), delta = st.y;
+    float down = 1.0f;
+    int e = 0;
+    if constexpr (F16) {
+        float sq = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            float x[8];
+            unpack8<true>(df[kk], x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sq = __builtin_fmaf(x[i], x[i], sq);
+        }
+        e = bound_exponent(sqrtf(half_sum(sq)) * __uint_as_float(p.norms[bh * 2 + 1])) + 1;
+        down = __builtin_amdgcn_ldexpf(1.0f, -e);
+    }
+    f32x16 dq[DB];
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+        dq[i] = f32x16{};
+
+    Stager<D, BN, NW> ks, vs;
+    ks.init(wave, lane, p.k_ts);
+    vs.init(wave, lane, p.v_ts);
+    const uint16_t* kbase = p.k + b * p.k_bs + hk * p.k_hs;
+    const uint16_t* vbase = p.v + b * p.v_bs + hk * p.v_hs;
+    const uint32_t lds0 = lds_address(lds);
+    const uint32_t at_row = row_offset<D>(lane), at_tr = tr_offset<D>(lane);
+
+    if (tiles > 0) {
+        ks.load(kbase, p.k_ts, len, lds0, wave);
+        vs.load(vbase, p.v_ts, len, lds0 + kTile, wave);
+    }
+    for (int t = 0; t < tiles; ++t) {
+        const int buf = t & 1;
+        wait_staged();
+        __syncthreads();
+        if (t + 1 < tiles) {
+            const int64_t next = (int64_t)(t + 1) * BN;
+            const uint32_t to = lds0 + (buf ^ 1) * 2 * kTile;
+            ks.load(kbase + next * p.k_ts, p.k_ts, len - (int)next, to, wave);
+            vs.load(vbase + next * p.v_ts, p.v_ts, len - (int)next, to + kTile, wave);
+        }
+        const char* kt = lds + buf * 2 * kTile;
+        const char* vt = kt + kTile;
+        const int sees = CAUSAL ? (qi + shift + 1 < len ? qi + shift + 1 : len) : len;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            f32x16 s{}, dp{};
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                s = mfma<F16>(row_fragment<D>(kt, at_row, j, kk), qf[kk], s);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                dp = mfma<F16>(row_fragment<D>(vt, at_row, j, kk), df[kk], dp);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c, -lse2));
+                s[i] = F16 ? pr * ((dp[i] - delta) * down) : pr * (dp[i] - delta);
+            }
+            if (t * BN + BN > open) {      // hidden keys: their scores are no scores
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (t * BN + j * 32 + 8 * (i / 4) + 4 * g + i % 4 >= sees)
+                        s[i] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const u32x4 sf = pack_b<F16>(s, k);
+#pragma unroll
+                for (int i = 0; i < DB; ++i)
+                    dq[i] = mfma<F16>(tr_fragment<D>(kt, at_tr, j, k, i), sf, dq[i]);
+            }
+        }
+    }
+
+    const bool valid = r0 + n < p.rows;
+    uint16_t* row = p.dq + b * p.dq_bs + qi * p.dq_ts + head * p.dq_hs;
+    const float f = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+        store_column<F16>(row + 32 * i, dq[i], f, g, valid);
+}
+
+// ---------------------------------------------------------------- launches
+
+template <int D>
+constexpr int waves_per_key_block() { return D == 256 ? 2 : 1; }
+
+constexpr int kWaves = 4;
+
+template <int D, bool F16, bool CAUSAL>
+hipError_t launch(BwdParams p, hipStream_t st)
+{
+    constexpr int DS = waves_per_key_block<D>(), BK = 32 * kWaves / DS;
+    constexpr int R = 256 / (D / 8);
+    p.row_blocks = (p.rows + 32 * kWaves - 1) / (32 * kWaves);
+    p.key_blocks = (p.kv_tokens + BK - 1) / BK;
+    const int64_t pairs = p.batch * p.kv_heads;
+    void* argv[] = {&p};
+    const auto go = [&](const void* fn, int64_t blocks) {
+        return blocks ? hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), argv, 0, st) : hipSuccess;
+    };
+    hipError_t err = hipSuccess;
+    if (F16) {
+        int64_t count = pairs * 2;
+        void* cargs[] = {&p.norms, &count};
+        err = hipLaunchKernel(reinterpret_cast<const void*>(clear_norms_kernel),
+                              dim3((unsigned)((count + 255) / 256)), dim3(256), cargs, 0, st);
+        if (err == hipSuccess)
+            err = go(reinterpret_cast<const void*>(value_norms_kernel<D>), pairs * ((p.kv_tokens + R - 1) / R));
+    }
+    if (err == hipSuccess)
+        err = go(reinterpret_cast<const void*>(row_stats_kernel<D, F16>),
+                 p.batch * p.heads * ((p.q_tokens + R - 1) / R));
+    if (err == hipSuccess)
+        err = go(reinterpret_cast<const void*>(attention_dkv_kernel<D, F16, CAUSAL, kWaves, DS>),
+                 pairs * p.key_blocks);
+    if (err == hipSuccess)
+        err = go(reinterpret_cast<const void*>(attention_dq_kernel<D, F16, CAUSAL, kWaves, 64>),
+                 pairs * p.row_blocks);
+    return err;
+}
+
+template <int D>
+hipError_t launch(const BwdParams& p, bool f16, bool causal, hipStream_t st)
+{
+    if (f16)
+        return causal ? launch<D, true, true>(p, st) : launch<D, true, false>(p, st);
+    return causal ? launch<D, false, true>(p, st) : launch<D, false, false>(p, st);
+}
+
+}  // namespace
+
+extern "C" int64_t dit_attention_backward_workspace_size(const dit_attn_args* args)
+{
+    const int rc = qkr_attn_host::check_args(args);
+    if (rc != QKR_OK)
+        return rc;
+    return args->batch * args->heads * args->q_tokens * 8 + args->batch * args->kv_heads * 8;
+}
+
+extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_tensor* dout,
+                                      const dit_attn_tensor* q, const dit_attn_tensor* k,
+                                      const dit_attn_tensor* v, const dit_attn_tensor* out,
+                                      const float* lse, const dit_attn_tensor* dq,
+                                      const dit_attn_tensor* dk, const dit_attn_tensor* dv,
+                                      void* workspace, int64_t workspace_bytes, void* stream)
+{
+    using namespace qkr_attn_host;
+    int rc = check_args(args);
+    if (rc != QKR_OK)
+        return rc;
+    const dit_attn_args& a = *args;
+    if (a.batch == 0 || (a.q_tokens == 0 && a.kv_tokens == 0))
+        return QKR_OK;
+    const Extent eq = {a.q_tokens, a.heads}, ekv = {a.kv_tokens, a.kv_heads};
+    const struct { const dit_attn_tensor* t; Extent e; } all[] = {
+        {dout, eq}, {q, eq}, {k, ekv}, {v, ekv}, {out, eq}, {dq, eq}, {dk, ekv}, {dv, ekv}};
+    for (int i = 0; i < 8; ++i)
+        if ((rc = check_tensor(a, all[i].t, all[i].e, i >= 5)))
+            return rc;
+    if (a.q_tokens && !lse)
+        return QKR_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u || reinterpret_cast<uintptr_t>(a.kv_lengths) & 3u)
+        return QKR_ERR_ALIGN;
+    const int64_t need = dit_attention_backward_workspace_size(args);
+    if (!workspace || workspace_bytes < need)
+        return QKR_ERR_WORKSPACE;
+    if (!qkr_host::aligned16(workspace))
+        return QKR_ERR_ALIGN;
+    const Range lse_r = {lse, (uint64_t)a.batch * a.heads * a.q_tokens * 4};
+    const Range ws_r = {workspace, (uint64_t)need};
+    const Range len_r = {a.kv_lengths, a.kv_lengths ? (uint64_t)a.batch * 4 : 0};
+    if (meet(ws_r, lse_r) || meet(ws_r, len_r))
+        return QKR_ERR_ARG;
+    for (int i = 0; i < 8; ++i) {
+        const bool there = all[i].e.tokens != 0;
+        const Range x = there ? range(a, all[i].t, all[i].e) : Range{nullptr, 0};
+        if (meet(x, ws_r))
+            return QKR_ERR_ARG;
+        if (i < 5)
+            continue;
+        if (meet(x, lse_r) || meet(x, len_r))
+            return QKR_ERR_ARG;
+        for (int j = 0; j < i; ++j)
+            if (may_meet(a, all[i].t, all[i].e, all[j].t, all[j].e))
+                return QKR_ERR_ARG;
+    }
+
+    BwdParams p = {};
+    const auto set = [](const dit_attn_tensor* t, auto*& at, int64_t& bs, int64_t& ts, int64_t& hs) {
+        using P = typename std::remove_reference<decltype(at)>::type;
+        if (t) {
+            at = static_cast<P>(t->data);
+            bs = t->batch_stride, ts = t->token_stride, hs = t->head_stride;
+        }
+    };
+    set(dout, p.dout, p.do_bs, p.do_ts, p.do_hs);
+    set(q, p.q, p.q_bs, p.q_ts, p.q_hs);
+    set(k, p.k, p.k_bs, p.k_ts, p.k_hs);
+    set(v, p.v, p.v_bs, p.v_ts, p.v_hs);
+    set(out, p.out, p.o_bs, p.o_ts, p.o_hs);
+    set(dq, p.dq, p.dq_bs, p.dq_ts, p.dq_hs);
+    set(dk, p.dk, p.dk_bs, p.dk_ts, p.dk_hs);
+    set(dv, p.dv, p.dv_bs, p.dv_ts, p.dv_hs);
+    p.lse = lse;
+    p.kv_lengths = a.kv_lengths;
+    p.batch = a.batch;
+    p.q_tokens = (int32_t)a.q_tokens;
+    p.kv_tokens = (int32_t)a.kv_tokens;
+    p.heads = a.heads;
+    p.kv_heads = a.kv_heads;
+    p.group = a.heads / a.kv_heads;
+    p.rows = (int32_t)(a.q_tokens * p.group);
+    p.scale = a.scale;
+    p.c = a.scale * kLog2e;
+    p.stats = static_cast<float*>(workspace);
+    p.norms = reinterpret_cast<uint32_t*>(p.stats + a.batch * a.heads * a.q_tokens * 2);
+    const bool f16 = a.dtype == QKR_FP16, causal = a.causal != 0;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const hipError_t err = a.head_dim == 64    ? launch<64>(p, f16, causal, st)
+                           : a.head_dim == 128 ? launch<128>(p, f16, causal, st)
+                                               : launch<256>(p, f16, causal, st);
+    return err == hipSuccess ? QKR_OK : QKR_ERR_HIP;
+}

@@ -1,0 +1,357 @@
+// attention_forward.hip -- attention forward for gfx950 (see dit_attention.h).
+//
+// One wave holds 32 query rows as the B operand of S^T = K Q^T: its lane n has
+// row n (twice, for the two halves of the wave), so the running maximum m and
+// sum l of a row are plain registers and need one cross-lane step a tile.  The
+// scores of a tile come out of the product with keys down the registers, which
+// is the layout in which the packed probabilities are the B operand of
+// O^T = V^T P^T (attention_common.h); P never goes through LDS.
+//
+// Query heads that share a key head are taken as rows of one sequence (row r
+// is query r / G, head r % G of the group), so their K and V are staged once.
+//
+// K and V tiles are staged straight into a double buffer in LDS; the loads of
+// tile t+1 run while tile t is computed.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "attention_common.h"
+#include "attention_host.h"
+#include "dit_attention.h"
+
+namespace {
+
+using namespace qkr_attn;
+
+struct FwdParams {
+    const uint16_t *q, *k, *v;
+    uint16_t* out;
+    float* lse;
+    const int32_t* kv_lengths;
+    int64_t q_bs, q_ts, q_hs, k_bs, k_ts, k_hs, v_bs, v_ts, v_hs, o_bs, o_ts, o_hs;
+    int32_t q_tokens, kv_tokens, kv_heads, group, rows;    // rows = q_tokens * group
+    int32_t row_blocks;
+    int32_t splits, tiles_per_split;
+    float c;                                  // scale * log2(e)
+    float* part_o;                            // [splits][batch * kv_heads * rows][D]
+    float* part_lse;                          // [splits][batch * kv_heads * rows], base 2
+};
+
+// exp2 of the scores is taken relative to 2^-kShift of the row's maximum, so
+// that fp16 probabilities down to 2^-21 of the largest are normal numbers; a
+// maximum is kept until the scores pass it by kSlack, so p <= 2^(kShift + kSlack).
+template <bool F16>
+constexpr float p_shift() { return F16 ? 7.0f : 0.0f; }
+constexpr float kSlack = 8.0f;
+
+template <int D, bool F16, bool CAUSAL, int NW, int BN>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2)
+void attention_forward_kernel(const FwdParams p)
+{
+    constexpr int BM = NW * 32, KB = BN / 32, DB = D / 32;
+    constexpr int kTile = BN * D * 2;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];   // [buffer][K, V]
+    const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+
+    int64_t block = logical_block<-1>(blockIdx.x, gridDim.x);
+    const int mb_raw = block % p.row_blocks;
+    block /= p.row_blocks;
+    const int split = block % p.splits;
+    const int64_t bh = block / p.splits;                 // sample, key head
+    const int64_t b = bh / p.kv_heads;
+    const int hk = bh % p.kv_heads;
+    const int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;   // the longest first
+
+    int len = p.kv_tokens;
+    if (p.kv_lengths) {
+        const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
+        len = given < 0 ? 0 : given < len ? given : len;
+    }
+    const int r0 = mb * BM + wave * 32;
+    const int r = r0 + n < p.rows ? r0 + n : p.rows - 1;          // this lane's row
+    const int qi = r / p.group, head = hk * p.group + r % p.group;
+    const int shift = p.kv_tokens - p.q_tokens;                   // causal: sees keys <= qi + shift
+    int end = len;                                                // keys of the workgroup
+    if (CAUSAL) {
+        const int last = (mb * BM + BM < p.rows ? mb * BM + BM : p.rows) - 1;
+        const int sees = last / p.group + shift + 1;
+        end = sees < end ? (sees < 0 ? 0 : sees) : end;
+    }
+    const int tiles = (end + BN - 1) / BN;
+    const int t0 = split * p.tiles_per_split;
+    const int t1 = tiles < t0 + p.tiles_per_split ? tiles : t0 + p.tiles_per_split;
+    // keys below this are seen by every row of the wave
+    int open = len;
+    if (CAUSAL) {
+        const int s = (r0 < p.rows ? r0 : p.rows - 1) / p.group + shift + 1;
+        open = s < open ? s : open;
+    }
+
+    u32x4 qf[D / 16];
+    {
+        const uint16_t* row = p.q + b * p.q_bs + qi * p.q_ts + head * p.q_hs + 8 * g;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+            qf[kk] = load16<false>(row + 16 * kk);
+    }
+    f32x16 o[DB];
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+        o[i] = f32x16{};
+    float m = -INFINITY, l = 0.0f;         // m in units of log2 (scores times c)
+
+    Stager<D, BN, NW> ks, vs;
+    ks.init(wave, lane, p.k_ts);
+    vs.init(wave, lane, p.v_ts);
+    const uint16_t* kbase = p.k + b * p.k_bs + hk * p.k_hs;
+    const uint16_t* vbase = p.v + b * p.v_bs + hk * p.v_hs;
+    const uint32_t lds0 = lds_address(lds);
+    const uint32_t at_row = row_offset<D>(lane), at_tr = tr_offset<D>(lane);
+
+    if (t0 < t1) {
+        ks.load(kbase + (int64_t)t0 * BN * p.k_ts, p.k_ts, len - t0 * BN, lds0, wave);
+        vs.load(vbase + (int64_t)t0 * BN * p.v_ts, p.v_ts, len - t0 * BN, lds0 + kTile, wave);
+    }
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1;
+        wait_staged();
+        __syncthreads();       // tile t is there, and the other buffer is free
+        if (t + 1 < t1) {
+            const int64_t next = (int64_t)(t + 1) * BN;
+            const uint32_t to = lds0 + (buf ^ 1) * 2 * kTile;
+            ks.load(kbase + next * p.k_ts, p.k_ts, len - (int)next, to, wave);
+            vs.load(vbase + next * p.v_ts, p.v_ts, len - (int)next, to + kTile, wave);
+        }
+        const char* kt = lds + buf * 2 * kTile;
+        const char* vt = kt + kTile;
+
+        f32x16 s[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            s[j] = f32x16{};
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                s[j] = mfma<F16>(row_fragment<D>(kt, at_row, j, kk), qf[kk], s[j]);
+        }
+        if (t * BN + BN > open) {          // some key of the tile is hidden from some row
+            const int sees = CAUSAL ? (qi + shift + 1 < len ? qi + shift + 1 : len) : len;
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (t * BN + j * 32 + 8 * (i / 4) + 4 * g + i % 4 >= sees)
+                        s[j][i] = -INFINITY;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = fmaxf(top, s[j][i]);
+        top = half_max(top) * p.c;
+        if (__any(top > m + kSlack)) {
+            const float m_new = fmaxf(m, top);
+            const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - m_new);
+            m = m_new;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+                o[i] *= f;
+        }
+        // rows that have seen no key yet: every score is -inf, and p is 0
+        const float base = (m == -INFINITY ? 0.0f : m) - p_shift<F16>();
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], p.c, -base));
+                sum += s[j][i];
+            }
+        l += sum;
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const u32x4 pf = pack_b<F16>(s[j], k);
+#pragma unroll
+                for (int i = 0; i < DB; ++i)
+                    o[i] = mfma<F16>(tr_fragment<D>(vt, at_tr, j, k, i), pf, o[i]);
+            }
+    }
+
+    l = half_sum(l);
+    const bool valid = r0 + n < p.rows;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float lse2 = l == 0.0f ? -INFINITY : m - p_shift<F16>() + __builtin_amdgcn_logf(l);
+    if (p.splits == 1) {
+        uint16_t* row = p.out + b * p.o_bs + qi * p.o_ts + head * p.o_hs;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+            store_column<F16>(row + 32 * i, o[i], inv, g, valid);
+        if (valid && g == 0)
+            p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + qi] = lse2 * kLn2;
+    } else {
+        const int64_t at = (split * ((int64_t)gridDim.x / p.splits / p.row_blocks) + bh) * p.rows + r;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+            store_column_f32(p.part_o + at * D + 32 * i, o[i], inv, g, valid);
+        if (valid && g == 0)
+            p.part_lse[at] = lse2;
+    }
+}
+
+// Joins the splits of a row: out = sum_k 2^(lse_k - lse) out_k.  A wave a row.
+template <int D, bool F16>
+__global__ __launch_bounds__(256)
+void attention_join_kernel(const FwdParams p, int64_t total)
+{
+    const int lane = threadIdx.x % 64;
+    const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (at >= total)
+        return;
+    float top = -INFINITY;
+    for (int k = lane; k < p.splits; k += 64)
+        top = fmaxf(top, p.part_lse[k * total + at]);
+    top = wave_max(top);
+    const float base = top == -INFINITY ? 0.0f : top;
+    constexpr int E = D / 64;
+    float o[E] = {}, l = 0.0f;
+    for (int k = 0; k < p.splits; ++k) {
+        const float w = __builtin_amdgcn_exp2f(p.part_lse[k * total + at] - base);
+        l += w;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] = __builtin_fmaf(w, p.part_o[(k * total + at) * D + lane * E + e], o[e]);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t bh = at / p.rows, b = bh / p.kv_heads;
+    const int r = at % p.rows, qi = r / p.group;
+    const int head = (int)(bh % p.kv_heads) * p.group + r % p.group;
+    uint16_t* row = p.out + b * p.o_bs + qi * p.o_ts + head * p.o_hs + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        row[e] = (uint16_t)pack2<F16>(o[e] * inv, 0.0f);
+    if (lane == 0)
+        p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + qi] =
+            l == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+struct Shape {
+    int waves, tile;
+    int64_t row_blocks, splits, tiles_per_split;
+};
+
+Shape shape_of(const dit_attn_args& a)
+{
+    Shape s;
+    const int64_t rows = a.q_tokens * (a.heads / a.kv_heads);
+    s.waves = 4;
+    s.tile = 64;
+    s.row_blocks = (rows + 32 * s.waves - 1) / (32 * s.waves);
+    s.splits = 1;
+    s.tiles_per_split = (a.kv_tokens + s.tile - 1) / s.tile;
+    if (s.tiles_per_split < 1)
+        s.tiles_per_split = 1;
+    return s;
+}
+
+using Fn = void (*)(FwdParams);
+
+template <int D>
+Fn select(bool f16, bool causal)
+{
+    if (f16)
+        return causal ? attention_forward_kernel<D, true, true, 4, 64>
+                      : attention_forward_kernel<D, true, false, 4, 64>;
+    return causal ? attention_forward_kernel<D, false, true, 4, 64>
+                  : attention_forward_kernel<D, false, false, 4, 64>;
+}
+
+}  // namespace
+
+extern "C" int64_t dit_attention_workspace_size(const dit_attn_args* args)
+{
+    const int rc = qkr_attn_host::check_args(args);
+    if (rc != QKR_OK)
+        return rc;
+    const Shape s = shape_of(*args);
+    if (s.splits == 1)
+        return 0;
+    return s.splits * args->batch * args->heads * args->q_tokens * (args->head_dim + 1) * 4;
+}
+
+extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q,
+                             const dit_attn_tensor* k, const dit_attn_tensor* v,
+                             const dit_attn_tensor* out, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream)
+{
+    using namespace qkr_attn_host;
+    int rc = check_args(args);
+    if (rc != QKR_OK)
+        return rc;
+    const dit_attn_args& a = *args;
+    if (a.batch == 0 || a.q_tokens == 0)
+        return QKR_OK;
+    const Extent eq = {a.q_tokens, a.heads}, ekv = {a.kv_tokens, a.kv_heads};
+    if ((rc = check_tensor(a, q, eq, false)) || (rc = check_tensor(a, k, ekv, false)) ||
+        (rc = check_tensor(a, v, ekv, false)) || (rc = check_tensor(a, out, eq, true)))
+        return rc;
+    const uint64_t lse_bytes = (uint64_t)a.batch * a.heads * a.q_tokens * 4;
+    if (!lse)
+        return QKR_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u || reinterpret_cast<uintptr_t>(a.kv_lengths) & 3u)
+        return QKR_ERR_ALIGN;
+    const int64_t need = dit_attention_workspace_size(args);
+    if (need && (!workspace || workspace_bytes < need))
+        return QKR_ERR_WORKSPACE;
+    if (!qkr_host::aligned16(workspace))
+        return QKR_ERR_ALIGN;
+    const Range lse_r = {lse, lse_bytes}, ws_r = {workspace, (uint64_t)need};
+    const Range len_r = {a.kv_lengths, a.kv_lengths ? (uint64_t)a.batch * 4 : 0};
+    const Range in[] = {range(a, q, eq), range(a, k, ekv), range(a, v, ekv), len_r};
+    const Range o = range(a, out, eq);
+    for (const Range& x : in)
+        if (meet(x, lse_r) || meet(x, ws_r))
+            return QKR_ERR_ARG;
+    if (meet(o, lse_r) || meet(o, ws_r) || meet(lse_r, ws_r) || meet(o, len_r) ||
+        may_meet(a, out, eq, q, eq) || may_meet(a, out, eq, k, ekv) || may_meet(a, out, eq, v, ekv))
+        return QKR_ERR_ARG;
+
+    const Shape s = shape_of(a);
+    FwdParams p;
+    p.q = static_cast<const uint16_t*>(q->data);
+    p.k = static_cast<const uint16_t*>(k->data);
+    p.v = static_cast<const uint16_t*>(v->data);
+    p.out = static_cast<uint16_t*>(out->data);
+    p.lse = lse;
+    p.kv_lengths = a.kv_lengths;
+    p.q_bs = q->batch_stride, p.q_ts = q->token_stride, p.q_hs = q->head_stride;
+    p.k_bs = k->batch_stride, p.k_ts = k->token_stride, p.k_hs = k->head_stride;
+    p.v_bs = v->batch_stride, p.v_ts = v->token_stride, p.v_hs = v->head_stride;
+    p.o_bs = out->batch_stride, p.o_ts = out->token_stride, p.o_hs = out->head_stride;
+    p.q_tokens = (int32_t)a.q_tokens;
+    p.kv_tokens = (int32_t)a.kv_tokens;
+    p.kv_heads = a.kv_heads;
+    p.group = a.heads / a.kv_heads;
+    p.rows = (int32_t)(a.q_tokens * p.group);
+    p.row_blocks = (int32_t)s.row_blocks;
+    p.splits = (int32_t)s.splits;
+    p.tiles_per_split = (int32_t)s.tiles_per_split;
+    p.c = a.scale * kLog2e;
+    const int64_t total = a.batch * a.kv_heads * (int64_t)p.rows;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = p.part_o ? p.part_o + s.splits * total * a.head_dim : nullptr;
+    const bool f16 = a.dtype == QKR_FP16, causal = a.causal != 0;
+    Fn fn = a.head_dim == 64 ? select<64>(f16, causal)
+            : a.head_dim == 128 ? select<128>(f16, causal) : select<256>(f16, causal);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    void* argv[] = {&p};
+    hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(fn),
+                                     dim3((unsigned)(a.batch * a.kv_heads * s.splits * s.row_blocks)),
+                                     dim3(s.waves * 64), argv, 0, st);
+    return err == hipSuccess ? QKR_OK : QKR_ERR_HIP;
+}

@@ -1,0 +1,131 @@
+// attention_host.h -- argument checks shared by the attention entry points.
+// Internal header.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#include "dit_attention.h"
+#include "host_common.h"
+
+namespace qkr_attn_host {
+
+struct Extent {
+    int64_t tokens;
+    int32_t heads;
+};
+
+struct Range {
+    const void* at;
+    uint64_t bytes;
+};
+
+// Workgroups of one launch, and rows of one sample's head group, stay below
+// these (a launch holds fewer than 2^32 work-items; row numbers are 32-bit).
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
+
+inline int check_args(const dit_attn_args* a)
+{
+    if (!a)
+        return QKR_ERR_NULL;
+    if (a->dtype < QKR_BF16 || a->dtype > QKR_FP32 || (a->causal != 0 && a->causal != 1) ||
+        !isfinite(a->scale) || !(a->scale > 0.0f))
+        return QKR_ERR_ARG;
+    if (a->dtype == QKR_FP32 || (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256))
+        return QKR_ERR_UNSUPPORTED;
+    if (a->batch < 0 || a->q_tokens < 0 || a->kv_tokens < 0 || a->q_tokens >= QKR_MAX_TOKENS ||
+        a->kv_tokens >= QKR_MAX_TOKENS || a->batch >= QKR_MAX_TOKENS || a->kv_heads < 1 ||
+        a->heads < a->kv_heads || a->heads > QKR_MAX_HEADS || a->heads % a->kv_heads)
+        return QKR_ERR_SHAPE;
+    // rows are dealt to workgroups in blocks of 32 or more
+    const int64_t group = a->heads / a->kv_heads;
+    if (a->q_tokens * group >= kMaxRows)
+        return QKR_ERR_SHAPE;
+    const int64_t pairs = a->batch * a->kv_heads;
+    const int64_t long_side = a->q_tokens * group > a->kv_tokens ? a->q_tokens * group : a->kv_tokens;
+    if (pairs >= kMaxBlocks || pairs * (long_side / 32 + 1) >= kMaxBlocks)
+        return QKR_ERR_SHAPE;
+    return QKR_OK;
+}
+
+// Elements from the first to one past the last of a tensor.
+inline uint64_t span(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e)
+{
+    if (e.tokens == 0)
+        return 0;
+    return (uint64_t)(a.batch - 1) * t->batch_stride + (uint64_t)(e.tokens - 1) * t->token_stride +
+           (uint64_t)(e.heads - 1) * t->head_stride + a.head_dim;
+}
+
+inline Range range(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e)
+{
+    return Range{t->data, span(a, t, e) * 2};
+}
+
+inline bool meet(const Range& x, const Range& y) { return qkr_host::overlaps(x.at, x.bytes, y.at, y.bytes); }
+
+// Whether two elements of the tensor share memory, or may: each dimension,
+// smallest stride first, has to step past all that the smaller ones cover.
+inline bool overlaps_itself(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e)
+{
+    struct { int64_t n, s; } dim[3] = {{a.batch, t->batch_stride}, {e.tokens, t->token_stride},
+                                       {e.heads, t->head_stride}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (dim[j].s > dim[j + 1].s) {
+                const auto x = dim[j];
+                dim[j] = dim[j + 1];
+                dim[j + 1] = x;
+            }
+    int64_t covered = a.head_dim;
+    for (const auto& d : dim)
+        if (d.n > 1) {
+            if (d.s < covered)
+                return true;
+            covered += (d.n - 1) * d.s;
+        }
+    return false;
+}
+
+inline int check_tensor(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e, bool written)
+{
+    if (e.tokens == 0)
+        return QKR_OK;
+    if (!t || !t->data)
+        return QKR_ERR_NULL;
+    if (!qkr_host::aligned16(t->data) || t->batch_stride % 8 || t->token_stride % 8 ||
+        t->head_stride % 8)
+        return QKR_ERR_ALIGN;
+    constexpr int64_t kMax = (int64_t)1 << 44;     // spans stay far inside 64 bits
+    if (t->batch_stride < 0 || t->token_stride < 0 || t->head_stride < 0 || t->batch_stride > kMax ||
+        t->head_stride > kMax || t->token_stride > DIT_ATTN_MAX_TOKEN_STRIDE ||
+        (e.tokens > 1 && t->token_stride < a.head_dim))
+        return QKR_ERR_SHAPE;
+    return written && overlaps_itself(a, t, e) ? QKR_ERR_ARG : QKR_OK;
+}
+
+// Whether two tensors may share an element.  Ranges that do not meet settle
+// it; tensors that interleave are told apart where they are slices of one
+// buffer: rows of the same token stride whose columns do not meet, at batch
+// strides that are whole rows.
+inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor* x, const Extent& ex,
+                     const dit_attn_tensor* y, const Extent& ey)
+{
+    if (ex.tokens == 0 || ey.tokens == 0 || !meet(range(a, x, ex), range(a, y, ey)))
+        return false;
+    const int64_t ts = x->token_stride;
+    if (ts != y->token_stride || ts == 0)
+        return true;
+    if (a.batch > 1 && (x->batch_stride % ts || y->batch_stride % ts))
+        return true;
+    const int64_t wx = (ex.heads - 1) * x->head_stride + a.head_dim;
+    const int64_t wy = (ey.heads - 1) * y->head_stride + a.head_dim;
+    const intptr_t bytes = reinterpret_cast<intptr_t>(y->data) - reinterpret_cast<intptr_t>(x->data);
+    int64_t ahead = bytes / 2 % ts;                 // y's columns begin here in x's rows
+    if (ahead < 0)
+        ahead += ts;
+    return !(wx <= ahead && ahead + wy <= ts);
+}
+
+}  // namespace qkr_attn_host
