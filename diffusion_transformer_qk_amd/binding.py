@@ -2,8 +2,10 @@
 
 Every step runs in the HIP kernels behind the C ABI declared in
 ``include/qknorm_rope.h`` (fused QK-norm + RoPE), ``include/fuse_scale_shift.h``
-(AdaLN modulation), ``include/group_norm_silu.h`` (group norm + SiLU) and
-``include/dit_attention.h`` (attention and its backward pass);
+(AdaLN modulation), ``include/group_norm_silu.h`` (group norm + SiLU),
+``include/dit_attention.h`` (attention and its backward pass),
+``include/layer_norm.h`` (layer norm and its backward pass) and
+``include/qknorm_rope_backward.h``;
 this module turns torch
 tensors into device pointers, sizes and enum codes and raises on a non-zero
 status.  There is no fallback: if the library is missing, loading fails
@@ -30,6 +32,7 @@ QKR_ROPE_INTERLEAVED, QKR_ROPE_ROTATE_HALF = 0, 1
 QKR_TENSORS_FUSED, QKR_TENSORS_PAIR, QKR_TENSORS_ONE = 0, 1, 2
 
 LAYOUTS = {"shared": QKR_COS_SHARED, "per_head": QKR_COS_PER_HEAD}
+DIT_LN_WEIGHT, DIT_LN_ONE_PLUS = 0, 1
 STYLES = {"interleaved": QKR_ROPE_INTERLEAVED, "rotate_half": QKR_ROPE_ROTATE_HALF}
 TENSORS = {"fused": QKR_TENSORS_FUSED, "pair": QKR_TENSORS_PAIR, "one": QKR_TENSORS_ONE}
 EXPORTS = ("qknorm_rope_fused", "qknorm_rope_strerror", "qknorm_rope_version",
@@ -37,7 +40,9 @@ EXPORTS = ("qknorm_rope_fused", "qknorm_rope_strerror", "qknorm_rope_version",
            "dit_group_norm_silu_workspace_size", "dit_group_norm_silu_schedule",
            "dit_group_norm_silu", "dit_group_norm_silu_noalloc",
            "dit_attention_workspace_size", "dit_attention_backward_workspace_size",
-           "dit_attention", "dit_attention_backward")
+           "dit_attention", "dit_attention_backward", "dit_layer_norm",
+           "dit_layer_norm_backward_workspace_size", "dit_layer_norm_backward",
+           "qknorm_rope_backward_workspace_size", "qknorm_rope_backward")
 MOD_DTYPES = {"bf16": QKR_BF16, "fp16": QKR_FP16, "fp32": QKR_FP32}
 
 
@@ -55,6 +60,10 @@ class KernelInfo(ctypes.Structure):
                 ("tokens_per_block", ctypes.c_int32), ("heads_in_flight", ctypes.c_int32),
                 ("die_runs", ctypes.c_int32), ("dynamic_lds_bytes", ctypes.c_int32),
                 ("workgroups_per_cu", ctypes.c_int32)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("x", ctypes.c_void_p), ("out", ctypes.c_void_p)]
 
 
 class AttnTensor(ctypes.Structure):
@@ -121,6 +130,19 @@ def load_library(path: str = LIB_PATH):
     lib.dit_attention.restype = ctypes.c_int
     lib.dit_attention_backward.argtypes = [args, *[tensor] * 5, vp, *[tensor] * 3, vp, i64, vp]
     lib.dit_attention_backward.restype = ctypes.c_int
+    lib.dit_layer_norm.argtypes = [vp, vp, i64, i32, vp, vp, i32, f32, i32, vp]
+    lib.dit_layer_norm.restype = ctypes.c_int
+    lib.dit_layer_norm_backward_workspace_size.argtypes = [i64, i32, i64]
+    lib.dit_layer_norm_backward_workspace_size.restype = i64
+    lib.dit_layer_norm_backward.argtypes = [vp, vp, vp, i64, i32, i64, vp, i32, i32, vp, vp, f32,
+                                            i32, vp, i64, vp]
+    lib.dit_layer_norm_backward.restype = ctypes.c_int
+    grad = ctypes.POINTER(GradTensor)
+    lib.qknorm_rope_backward_workspace_size.argtypes = [i64, i32]
+    lib.qknorm_rope_backward_workspace_size.restype = i64
+    lib.qknorm_rope_backward.argtypes = [grad, grad, grad, i64, i32, i32, vp, vp, vp, vp, f32, vp, vp,
+                                         i32, i32, i32, i32, vp, i64, vp]
+    lib.qknorm_rope_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -587,3 +609,224 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, kv_leng
                                             _ptr(workspace) or None, ws_bytes, stream_ptr or None)
     _check(status)
     return dq, dk, dv
+
+
+def layer_norm(x, weight=None, bias=None, *, out=None, eps: float = 1e-6, stream=None):
+    """Layer norm over the last dimension (see ``include/layer_norm.h``); returns ``out``.
+
+    ``x``: [..., hidden] bfloat16/float16; ``weight``/``bias``: [hidden] of one
+    of bfloat16, float16 or float32, either may be None.  ``out`` defaults to
+    a new tensor like x; pass ``out=x`` to normalise in place.
+    """
+    torch = _torch()
+    hidden = x.shape[-1]
+    rows = x.numel() // hidden if x.numel() else 0
+    for p in (weight, bias):
+        if p is not None and p.shape != (hidden,):
+            raise ValueError("weight and bias must be [%d]" % hidden)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    one = weight if weight is not None else bias
+    if out is None:
+        with _launch_stream_context(x, stream):
+            out = torch.empty_like(x)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must match x in shape and dtype")
+    ctx, stream_ptr = _call_context(x, (out, weight, bias), stream)
+    with ctx:
+        status = load_library().dit_layer_norm(
+            _ptr(x) or None, _ptr(out) or None, rows, hidden, _ptr(weight) or None,
+            _ptr(bias) or None, QKR_FP32 if one is None else _mod_code(one), float(eps), _x_code(x),
+            stream_ptr or None)
+    _check(status)
+    return out
+
+
+def layer_norm_backward_workspace_size(rows: int, hidden: int, rows_per_batch: int | None = None) -> int:
+    """Workspace bytes of ``layer_norm_backward`` (or, with rows_per_batch, of
+    ``fuse_scale_shift_backward``); negative: a QKR_ERR_* code."""
+    return int(load_library().dit_layer_norm_backward_workspace_size(
+        rows, hidden, max(1, rows) if rows_per_batch is None else rows_per_batch))
+
+
+def _norm_backward(dy, x, weight, form, rows_per_batch, params_shape, out, eps, workspace, stream):
+    torch = _torch()
+    lib = load_library()
+    hidden = x.shape[-1]
+    rows = x.numel() // hidden if x.numel() else 0
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must match x in shape and dtype")
+    dweight = dbias = None
+    with _launch_stream_context(x, stream):
+        if params_shape is not None:
+            make = torch.empty if rows else torch.zeros     # without rows the sums are empty
+            dweight, dbias = (make(params_shape, dtype=torch.float32, device=x.device)
+                              for _ in range(2))
+            if workspace is None:
+                need = int(lib.dit_layer_norm_backward_workspace_size(rows, hidden, rows_per_batch))
+                if need < 0:
+                    raise QkrError(need, strerror(need))
+                if need > 0:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        if out is None:
+            out = torch.empty_like(x)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must match x in shape and dtype")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ctx, stream_ptr = _call_context(x, (dy, out, weight, workspace), stream)
+    with ctx:
+        status = lib.dit_layer_norm_backward(
+            _ptr(dy) or None, _ptr(x) or None, _ptr(out) or None, rows, hidden, rows_per_batch,
+            _ptr(weight) or None, form, QKR_FP32 if weight is None else _mod_code(weight),
+            _ptr(dweight) or None, _ptr(dbias) or None, float(eps), _x_code(x),
+            _ptr(workspace) or None, ws_bytes, stream_ptr or None)
+    _check(status)
+    return out, dweight, dbias
+
+
+def layer_norm_backward(dy, x, weight=None, *, out=None, eps: float = 1e-6, workspace=None,
+                        stream=None):
+    """Backward pass of ``layer_norm``; returns ``(dx, dweight, dbias)``.
+
+    ``dy``: the gradient of its output, ``x``: its input.  ``dweight`` and
+    ``dbias`` are float32 [hidden], and None where ``weight`` is None.
+    ``out`` receives dx (a new tensor by default); ``out=dy`` works in place.
+    ``workspace``: at least ``layer_norm_backward_workspace_size`` bytes;
+    allocated here on the launch stream when None and needed.
+    """
+    hidden = x.shape[-1]
+    if weight is not None and weight.shape != (hidden,):
+        raise ValueError("weight must be [%d]" % hidden)
+    rows = x.numel() // hidden if x.numel() else 0
+    return _norm_backward(dy, x, weight, DIT_LN_WEIGHT, max(1, rows),
+                          None if weight is None else (hidden,), out, eps, workspace, stream)
+
+
+def fuse_scale_shift_backward(dy, x, scale, *, out=None, eps: float = 1e-6,
+                              rows_per_batch: int | None = None, workspace=None, stream=None):
+    """Backward pass of ``fuse_scale_shift``; returns ``(dx, dscale, dshift)``.
+
+    ``dy``: the gradient of its output; ``x``, ``scale`` and
+    ``rows_per_batch``: the forward call's.  ``dscale`` and ``dshift`` are
+    float32 in scale's shape, each row summed over the rows of x that use it
+    (zero where none does).  ``out`` and ``workspace``: as in
+    ``layer_norm_backward``.
+    """
+    hidden = x.shape[-1]
+    rows = x.numel() // hidden if x.numel() else 0
+    if scale.shape[-1] != hidden:
+        raise ValueError("scale's last dimension must equal hidden")
+    batches = scale.numel() // hidden
+    if rows_per_batch is None:
+        if batches < 1 or rows % batches:
+            raise ValueError("rows do not split evenly over the modulation batches")
+        rows_per_batch = max(1, rows // batches)
+    used = -(-rows // rows_per_batch) if rows_per_batch > 0 else 0
+    if used > batches:
+        raise ValueError("scale holds fewer batches than the rows need")
+    dx, dscale, dshift = _norm_backward(dy, x, scale, DIT_LN_ONE_PLUS, rows_per_batch, scale.shape,
+                                        out, eps, workspace, stream)
+    if 0 < used < batches:
+        with _launch_stream_context(x, stream):
+            for t in (dscale, dshift):
+                t.view(batches, hidden)[used:].zero_()
+    return dx, dscale, dshift
+
+
+def qknorm_rope_backward_workspace_size(tokens: int, head_dim: int) -> int:
+    """Workspace bytes the call needs (negative: a QKR_ERR_* code for bad sizes)."""
+    return int(load_library().qknorm_rope_backward_workspace_size(tokens, head_dim))
+
+
+def qknorm_rope_backward(dqkv=None, qkv=None, dq=None, dk=None, q=None, k=None, *, q_gamma=None,
+                         k_gamma=None, cos=None, sin=None, eps: float = 1e-6,
+                         heads: int | None = None, head_dim: int | None = None,
+                         cos_layout: str = "shared", style: str = "interleaved", out=None,
+                         dq_out=None, dk_out=None, workspace=None, stream=None):
+    """Backward pass of ``qknorm_rope_fused`` (see ``include/qknorm_rope_backward.h``);
+    returns ``(dq_gamma, dk_gamma)``, float32 [head_dim], and writes dx.
+
+    Fused mode: ``dqkv`` holds the gradients of the pass's output in its Q and
+    K slices, ``qkv`` the pass's input (a copy taken before the pass wrote
+    over it).  dx replaces the Q and K slices of ``dqkv``, or goes to those of
+    ``out``; V slices are neither read nor written.
+    Separate mode: ``dq`` with ``q`` and/or ``dk`` with ``k``, [..., heads,
+    head_dim]; dx replaces dq and dk, or goes to ``dq_out`` and ``dk_out``.
+    The gradient of a weight whose tensor is not given is None.  The other
+    arguments are the forward call's; ``workspace``: at least
+    ``qknorm_rope_backward_workspace_size`` bytes, allocated here on the launch
+    stream when None.
+    """
+    torch = _torch()
+    lib = load_library()
+    if dqkv is not None:
+        if qkv is None or any(t is not None for t in (dq, dk, q, k)):
+            raise ValueError("pass dqkv with qkv, or dq with q and/or dk with k")
+        ref = qkv
+        gam = q_gamma if q_gamma is not None else k_gamma
+        if head_dim is None:
+            if gam is None:
+                raise ValueError("head_dim is needed")
+            head_dim = gam.numel()
+        if heads is None:
+            heads = qkv.shape[-1] // (3 * head_dim)
+        if qkv.shape[-1] != 3 * heads * head_dim:
+            raise ValueError("qkv last dimension must be 3*heads*head_dim")
+        tokens = qkv.numel() // qkv.shape[-1] if qkv.numel() else 0
+        sets = {"qkv": (dqkv, qkv, dqkv if out is None else out)}
+    else:
+        if qkv is not None or (dq is None) != (q is None) or (dk is None) != (k is None) \
+                or (q is None and k is None):
+            raise ValueError("pass dqkv with qkv, or dq with q and/or dk with k")
+        ref = q if q is not None else k
+        if ref.dim() < 2:
+            raise ValueError("q/k must be [..., heads, head_dim]")
+        head_dim = ref.shape[-1] if head_dim is None else head_dim
+        heads = ref.shape[-2] if heads is None else heads
+        if tuple(ref.shape[-2:]) != (heads, head_dim):
+            raise ValueError("q/k must be [..., heads, head_dim] = [..., %d, %d]"
+                             % (heads, head_dim))
+        tokens = ref.numel() // (heads * head_dim) if ref.numel() else 0
+        sets = {}
+        if q is not None:
+            sets["q"] = (dq, q, dq if dq_out is None else dq_out)
+        if k is not None:
+            sets["k"] = (dk, k, dk if dk_out is None else dk_out)
+    flat = [t for s in sets.values() for t in s]
+    if any(t.shape != ref.shape or t.dtype != ref.dtype for t in flat):
+        raise ValueError("gradients, inputs and outputs must have one shape and dtype")
+    if cos_layout not in LAYOUTS:
+        raise ValueError("cos_layout must be one of %s" % sorted(LAYOUTS))
+    if style not in STYLES:
+        raise ValueError("style must be one of %s" % sorted(STYLES))
+    if cos is None or sin is None:
+        raise ValueError("cos and sin are required")
+    if cos.dtype != sin.dtype or cos.shape != sin.shape:
+        raise ValueError("cos and sin must match in shape and dtype")
+    rows = tokens * (heads if cos_layout == "per_head" else 1)
+    if cos.numel() != rows * head_dim:
+        raise ValueError("cos/sin hold %d values, expected %d for the %s layout"
+                         % (cos.numel(), rows * head_dim, cos_layout))
+    for g in (q_gamma, k_gamma):
+        if g is not None and (g.dtype != torch.float32 or g.numel() != head_dim):
+            raise ValueError("gamma must be float32 [head_dim]")
+    with _launch_stream_context(ref, stream):
+        dq_gamma, dk_gamma = (
+            torch.empty(head_dim, dtype=torch.float32, device=ref.device)
+            if dqkv is not None or name in sets else None for name in ("q", "k"))
+        if workspace is None:
+            need = qknorm_rope_backward_workspace_size(tokens, head_dim)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=ref.device)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ctx, stream_ptr = _call_context(ref, (*flat, q_gamma, k_gamma, cos, sin, workspace), stream)
+    with ctx:
+        ptrs = {n: ctypes.byref(GradTensor(*(_ptr(t) or None for t in s))) for n, s in sets.items()}
+        status = lib.qknorm_rope_backward(
+            ptrs.get("qkv"), ptrs.get("q"), ptrs.get("k"), tokens, heads, head_dim,
+            _ptr(q_gamma) or None, _ptr(k_gamma) or None, _ptr(dq_gamma) or None,
+            _ptr(dk_gamma) or None, float(eps), _ptr(cos) or None, _ptr(sin) or None,
+            LAYOUTS[cos_layout], _table_code(cos), STYLES[style], _x_code(ref),
+            _ptr(workspace) or None, ws_bytes, stream_ptr or None)
+    _check(status)
+    return dq_gamma, dk_gamma

@@ -15,7 +15,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", "qknorm_rope.hip"),
         os.path.join(PKG, "csrc", "fuse_scale_shift.hip"),
-        os.path.join(PKG, "csrc", "group_norm_silu.hip")]
+        os.path.join(PKG, "csrc", "group_norm_silu.hip"),
+        os.path.join(PKG, "csrc", "layer_norm.hip"),
+        os.path.join(PKG, "csrc", "qknorm_rope_backward.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqknorm_rope.so")
 # The attention kernels: a library of their own, because every kernel of
