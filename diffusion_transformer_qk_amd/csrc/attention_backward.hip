@@ -151,12 +151,12 @@ void value_norms_kernel(const BwdParams p)
 // and 128 registers of k and v would not fit beside the products' operands).
 // The queries are taken 32 at a time.
 template <int D, bool F16, bool CAUSAL, int NW, int DS>
-__global__ __launch_bounds__(NW * 64, 1)
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2)
 void attention_dkv_kernel(const BwdParams p)
 {
     constexpr int BK = NW / DS * 32, BQ = 32, DB = D / 32 / DS;
     constexpr int kTile = BQ * D * 2;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile + 2 * BQ * 8];
+    __shared__ __attribute__((aligned(4 * kTile))) char lds[4 * kTile + 2 * BQ * 8];
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
@@ -205,87 +205,103 @@ void attention_dkv_kernel(const BwdParams p)
     for (int i = 0; i < DB; ++i)
         dk[i] = dv[i] = f32x16{};
 
-    Stager<D, BQ, NW> qs, dos;
-    qs.init(wave, lane, p.q_ts);
-    dos.init(wave, lane, p.do_ts);
+    // waves 0 and 1 stage the two groups of q's rows, 2 and 3 those of dout's
+    static_assert(NW == 4, "a group of 16 rows a wave");
+    const bool stages_q = wave < 2;
+    const int64_t stage_ts = stages_q ? p.q_ts : p.do_ts;
+    const int64_t stage_hs = stages_q ? p.q_hs : p.do_hs;
+    const uint16_t* stage_base = stages_q ? p.q + b * p.q_bs : p.dout + b * p.do_bs;
+    const Stager<D> rows(lane, stage_ts);
     const uint32_t lds0 = lds_address(lds);
-    const uint32_t at_row = row_offset<D>(lane), at_tr = tr_offset<D>(lane);
+    uint32_t fill = lds0;
+    TileAt at(lds0, lane);
 
-    // tile t: query tile first + t % per of the group's head t / per
-    const auto stage = [&](int t, int buf) {
-        const int h = hk * p.group + t / per;
-        const int q0 = (first + t % per) * BQ;
-        const int left = p.q_tokens - q0;
-        const uint32_t to = lds0 + buf * 2 * kTile;
-        qs.load(p.q + b * p.q_bs + (int64_t)q0 * p.q_ts + h * p.q_hs, p.q_ts, left, to, wave);
-        dos.load(p.dout + b * p.do_bs + (int64_t)q0 * p.do_ts + h * p.do_hs, p.do_ts, left, to + kTile,
-                 wave);
+    // the tiles run through the queries of one head of the group after another;
+    // h and next_q: the next one to be staged
+    int h = hk * p.group, next_q = first * BQ;
+    const auto stage = [&](int buf) {
+        const int left = p.q_tokens - next_q;
+        rows.load(stage_base + (int64_t)next_q * stage_ts + h * stage_hs, stage_ts, left,
+                  fill + (stages_q ? 0 : kTile), wave & 1);
         if (wave == 0) {          // lse2 and delta: zero past the last query, as are its rows
-            const int rows = left < BQ ? left : BQ;
             const uint64_t a = reinterpret_cast<uint64_t>(
-                p.stats + ((b * p.heads + h) * p.q_tokens + q0) * 2);
+                p.stats + ((b * p.heads + h) * p.q_tokens + next_q) * 2);
             const u32x4 rsrc = {scalar((uint32_t)a), scalar((uint32_t)(a >> 32) & 0xffffu),
-                                scalar(rows * 8), kRawBuffer};
+                                scalar((left < BQ ? left : BQ) * 8), kRawBuffer};
             dma4(rsrc, lane * 4, lds0 + 4 * kTile + buf * BQ * 8);
+        }
+        fill ^= 2 * kTile;
+        next_q += BQ;
+        if (next_q >= p.q_tokens) {
+            next_q = first * BQ;
+            ++h;
         }
     };
 
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        settle(kf[kk]);
+        settle(vf[kk]);
+    }
     if (total > 0)
-        stage(0, 0);
+        stage(0);
+    int q0 = first * BQ;
     for (int t = 0; t < total; ++t) {
         const int buf = t & 1;
         wait_staged();
         __syncthreads();
+        const int following = next_q;
         if (t + 1 < total)
-            stage(t + 1, buf ^ 1);
-        const char* qt = lds + buf * 2 * kTile;
-        const char* dot = qt + kTile;
-        const float* st = reinterpret_cast<const float*>(lds + 4 * kTile + buf * BQ * 8);
-        const int q0 = (first + t % per) * BQ;
-        if (k0 >= len || (CAUSAL && k0 > q0 + BQ - 1 + shift))
-            continue;             // no query of the tile sees a key of the wave
+            stage(buf ^ 1);
+        const uint32_t st = lds0 + 4 * kTile + buf * BQ * 8 + 32 * g;
 
         f32x16 s{}, dp{};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-            s = mfma<F16>(row_fragment<D>(qt, at_row, 0, kk), kf[kk], s);
+            s = mfma<F16>(row_fragment(at, 0, kk), kf[kk], s);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-            dp = mfma<F16>(row_fragment<D>(dot, at_row, 0, kk), vf[kk], dp);
-        const bool diagonal = CAUSAL && k0 + 31 > q0 + shift;
+            dp = mfma<F16>(row_fragment(at, kTile, kk), vf[kk], dp);
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(st + 2 * (8 * i4 + 4 * g));
-            const f32x4 c = *reinterpret_cast<const f32x4*>(st + 2 * (8 * i4 + 4 * g) + 4);
+            const f32x4 a = *reinterpret_cast<LdsFloats>(st + 64 * i4);
+            const f32x4 c = *reinterpret_cast<LdsFloats>(st + 64 * i4 + 16);
             const float lse2[4] = {a[0], a[2], c[0], c[2]};
             const float delta[4] = {a[1], a[3], c[1], c[3]};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = 4 * i4 + i;
-                float pr = __builtin_amdgcn_exp2f(
-                    __builtin_fmaf(s[at], p.c, p_shift<F16>() - lse2[i]));
-                if (diagonal && key > q0 + 8 * i4 + 4 * g + i + shift)
-                    pr = 0.0f;
-                s[at] = pr;
-                dp[at] = F16 ? pr * ((dp[at] - delta[i]) * down) : pr * (dp[at] - delta[i]);
+                const int j = 4 * i4 + i;
+                const float pr = __builtin_amdgcn_exp2f(
+                    __builtin_fmaf(s[j], p.c, p_shift<F16>() - lse2[i]));
+                s[j] = pr;
+                dp[j] = F16 ? pr * ((dp[j] - delta[i]) * down) : pr * (dp[j] - delta[i]);
             }
+        }
+        if (CAUSAL && k0 + 31 > q0 + shift) {
+            keep_branch();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (key > q0 + 8 * (i / 4) + 4 * g + i % 4 + shift)
+                    s[i] = dp[i] = 0.0f;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const u32x4 pf = pack_b<F16>(s, k), sf = pack_b<F16>(dp, k);
 #pragma unroll
             for (int i = 0; i < DB; ++i)
-                dv[i] = mfma<F16>(tr_fragment<D>(dot, at_tr, 0, k, db0 + i), pf, dv[i]);
+                dv[i] = mfma<F16>(tr_fragment(at, kTile + db0 * kSlab, k, i), pf, dv[i]);
 #pragma unroll
             for (int i = 0; i < DB; ++i)
-                dk[i] = mfma<F16>(tr_fragment<D>(qt, at_tr, 0, k, db0 + i), sf, dk[i]);
+                dk[i] = mfma<F16>(tr_fragment(at, db0 * kSlab, k, i), sf, dk[i]);
         }
+        q0 = following;
+        at.flip(2 * kTile);
     }
 
     const bool valid = key < p.kv_tokens;
-    const int at = valid ? key : p.kv_tokens - 1;
-    uint16_t* kr = p.dk + b * p.dk_bs + (int64_t)at * p.dk_ts + hk * p.dk_hs + 32 * db0;
-    uint16_t* vr = p.dv + b * p.dv_bs + (int64_t)at * p.dv_ts + hk * p.dv_hs + 32 * db0;
+    const int64_t to = valid ? key : p.kv_tokens - 1;
+    uint16_t* kr = p.dk + b * p.dk_bs + to * p.dk_ts + hk * p.dk_hs + 32 * db0;
+    uint16_t* vr = p.dv + b * p.dv_bs + to * p.dv_ts + hk * p.dv_hs + 32 * db0;
     const float fv = F16 ? 0x1p-15f : 1.0f;
     const float fk = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
 #pragma unroll
@@ -305,7 +321,7 @@ void attention_dq_kernel(const BwdParams p)
 {
     constexpr int BM = NW * 32, KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];
+    __shared__ __attribute__((aligned(4 * kTile))) char lds[4 * kTile];
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
@@ -369,46 +385,50 @@ void attention_dq_kernel(const BwdParams p)
     for (int i = 0; i < DB; ++i)
         dq[i] = f32x16{};
 
-    Stager<D, BN, NW> ks, vs;
-    ks.init(wave, lane, p.k_ts);
-    vs.init(wave, lane, p.v_ts);
+    const Stager<D> ks(lane, p.k_ts), vs(lane, p.v_ts);
     const uint16_t* kbase = p.k + b * p.k_bs + hk * p.k_hs;
     const uint16_t* vbase = p.v + b * p.v_bs + hk * p.v_hs;
-    const uint32_t lds0 = lds_address(lds);
-    const uint32_t at_row = row_offset<D>(lane), at_tr = tr_offset<D>(lane);
-
-    if (tiles > 0) {
-        ks.load(kbase, p.k_ts, len, lds0, wave);
-        vs.load(vbase, p.v_ts, len, lds0 + kTile, wave);
+    uint32_t fill = lds_address(lds);
+    TileAt at(fill, lane);
+    const auto stage = [&](int t) {
+        const int64_t first = (int64_t)t * BN;
+#pragma unroll
+        for (int i = 0; i < BN / 16 / NW; ++i) {
+            ks.load(kbase + first * p.k_ts, p.k_ts, len - (int)first, fill, wave + i * NW);
+            vs.load(vbase + first * p.v_ts, p.v_ts, len - (int)first, fill + kTile, wave + i * NW);
+        }
+        fill ^= 2 * kTile;
+    };
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        settle(qf[kk]);
+        settle(df[kk]);
     }
+
+    if (tiles > 0)
+        stage(0);
     for (int t = 0; t < tiles; ++t) {
-        const int buf = t & 1;
         wait_staged();
         __syncthreads();
-        if (t + 1 < tiles) {
-            const int64_t next = (int64_t)(t + 1) * BN;
-            const uint32_t to = lds0 + (buf ^ 1) * 2 * kTile;
-            ks.load(kbase + next * p.k_ts, p.k_ts, len - (int)next, to, wave);
-            vs.load(vbase + next * p.v_ts, p.v_ts, len - (int)next, to + kTile, wave);
-        }
-        const char* kt = lds + buf * 2 * kTile;
-        const char* vt = kt + kTile;
+        if (t + 1 < tiles)
+            stage(t + 1);
         const int sees = CAUSAL ? (qi + shift + 1 < len ? qi + shift + 1 : len) : len;
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
             f32x16 s{}, dp{};
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-                s = mfma<F16>(row_fragment<D>(kt, at_row, j, kk), qf[kk], s);
+                s = mfma<F16>(row_fragment(at, j * block_bytes<D>(), kk), qf[kk], s);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-                dp = mfma<F16>(row_fragment<D>(vt, at_row, j, kk), df[kk], dp);
+                dp = mfma<F16>(row_fragment(at, kTile + j * block_bytes<D>(), kk), df[kk], dp);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c, -lse2));
                 s[i] = F16 ? pr * ((dp[i] - delta) * down) : pr * (dp[i] - delta);
             }
             if (t * BN + BN > open) {      // hidden keys: their scores are no scores
+                keep_branch();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (t * BN + j * 32 + 8 * (i / 4) + 4 * g + i % 4 >= sees)
@@ -419,9 +439,10 @@ void attention_dq_kernel(const BwdParams p)
                 const u32x4 sf = pack_b<F16>(s, k);
 #pragma unroll
                 for (int i = 0; i < DB; ++i)
-                    dq[i] = mfma<F16>(tr_fragment<D>(kt, at_tr, j, k, i), sf, dq[i]);
+                    dq[i] = mfma<F16>(tr_fragment(at, j * block_bytes<D>(), k, i), sf, dq[i]);
             }
         }
+        at.flip(2 * kTile);
     }
 
     const bool valid = r0 + n < p.rows;

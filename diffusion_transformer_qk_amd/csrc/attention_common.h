@@ -10,11 +10,15 @@
 // as they stand: they hold k = 16s + 8 (j/4) + 4g + j%4 (j = 0..7), and the
 // other operand is read from LDS in that order (tr_fragment below).
 //
-// A tile in LDS is rows of head_dim 16-bit elements, as they lie in memory,
-// with the 16-byte chunks of each row permuted: chunk c of row r is stored at
-// c ^ swizzle(r).  Rows are a multiple of 128 bytes apart, so without it the
-// lanes of a fragment read, which go down the rows, would meet in the same
-// banks.
+// A tile in LDS is laid out in blocks of 32 rows, a block in slabs of 32
+// columns, a slab as its 32 rows of 64 bytes with the 16-byte chunks of row r
+// permuted: chunk c is stored at c ^ ((r / 4) % 4).  So
+//   * an A or B fragment of rows (32 rows, 16 columns: half a slab) touches
+//     every bank evenly, and so does a transposed read (8 rows, one slab);
+//   * a lane's address in a slab takes two values for either kind of read (the
+//     half of the slab; the upper or lower 8 rows): all else is an immediate
+//     offset, and four registers address a whole tile;
+//   * 64 bytes of 16 rows are one load of a wave straight into LDS.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -88,69 +92,123 @@ __device__ __forceinline__ float half_sum(float v)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// swizzle(row): 16 rows map to 16 different chunks (8 for head_dim 64, where
-// two rows share a line of the banks), and the 4 rows of a transposed read to
-// 4 different groups of 4 chunks (2 of 4).
+typedef __attribute__((address_space(3))) const u32x4* LdsVec;
+typedef __attribute__((address_space(3))) const f32x4* LdsFloats;
+typedef __attribute__((address_space(3))) s16x4* LdsQuad;
+
+constexpr int kSlab = 2048;                        // 32 rows of 64 bytes
+
 template <int D>
-__device__ __forceinline__ int swizzle(int row)
+constexpr int block_bytes() { return 64 * D; }     // 32 rows
+
+__device__ __forceinline__ uint32_t lds_address(const void* p)
 {
-    if constexpr (D == 64)
-        return (((row >> 1) & 1) << 2) | (((row >> 2) & 1) << 1) | ((row >> 3) & 1);
-    else
-        return ((row & 3) << 2) | ((row >> 2) & 3);
+    return (uint32_t)reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) const void*)p);
 }
 
-// Rows of a tile are staged straight into LDS, 64 lanes x 16 bytes an
-// instruction, in the order of LDS: the permutation is in the addresses that
-// the lanes read.  Rows from `rows` on read as zero (the buffer's range ends
-// there; this needs a row stride of at least head_dim).
-template <int D, int ROWS, int NW>
-struct Stager {
-    static constexpr int kRowBytes = 2 * D;
-    static constexpr int kRowsPer = 1024 / kRowBytes;              // rows of one instruction
-    static constexpr int kPer = ROWS * kRowBytes / 1024 / NW;      // instructions of one wave
-    static_assert(ROWS * kRowBytes % (1024 * NW) == 0, "whole instructions");
-    uint32_t off[kPer];
+// Byte addresses of this lane's part of a tile.
+struct TileAt {
+    uint32_t row[2];     // fragment of rows: half 0 and 1 of a slab
+    uint32_t tr[2];      // transposed read: rows 0 and 8 of a k step
 
-    __device__ __forceinline__ void init(int wave, int lane, int64_t row_stride)
+    __device__ __forceinline__ TileAt(uint32_t lds, int lane)
     {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int row = (wave * kPer + i) * kRowsPer + lane * 16 / kRowBytes;
-            const int slot = (lane * 16 % kRowBytes) / 16;
-            off[i] = (uint32_t)(row * (int)(row_stride * 2) + ((slot ^ swizzle<D>(row)) << 4));
+        const int n = lane & 31, g = lane >> 5, l = lane & 15;
+        row[0] = lds + n * 64 + ((g ^ ((n >> 2) & 3)) << 4);
+        row[1] = lds + n * 64 + (((2 + g) ^ ((n >> 2) & 3)) << 4);
+        const int r = 4 * g + (l >> 2), chunk = ((lane >> 4) & 1) * 2 + ((l & 3) >> 1);
+        tr[0] = lds + r * 64 + ((chunk ^ g) << 4) + (l & 1) * 8;
+        tr[1] = lds + (r + 8) * 64 + ((chunk ^ g ^ 2) << 4) + (l & 1) * 8;
+    }
+
+    // To the other half of a double buffer whose halves are `bytes` (a power
+    // of two, to which the buffer is aligned) apart.
+    __device__ __forceinline__ void flip(uint32_t bytes)
+    {
+        row[0] ^= bytes;
+        row[1] ^= bytes;
+        tr[0] ^= bytes;
+        tr[1] ^= bytes;
+    }
+};
+
+// The A or B fragment of 32 rows and columns 16 kk .. 16 kk + 15; `off`: the
+// block's offset from the tile address.
+__device__ __forceinline__ u32x4 row_fragment(const TileAt& at, int off, int kk)
+{
+    return *reinterpret_cast<LdsVec>(at.row[kk & 1] + (off + (kk >> 1) * kSlab));
+}
+
+// The fragment whose lane index runs over the 32 columns of slab c and whose k
+// runs over rows 16s .. 16s + 15 of the block, in the order of packed C
+// registers: two transposed reads of 8 rows.
+__device__ __forceinline__ u32x4 tr_fragment(const TileAt& at, int off, int s, int c)
+{
+    const int o = off + c * kSlab + s * 1024;
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        reinterpret_cast<LdsQuad>(at.tr[0] + o)));
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        reinterpret_cast<LdsQuad>(at.tr[1] + o)));
+    return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// Rows of a tile are staged straight into LDS in groups of 16 rows; a wave
+// stages one group (all slabs) or several.  Rows from `rows` on read as zero:
+// the buffer's range ends there (this needs a row stride of at least head_dim).
+template <int D>
+struct Stager {
+    uint32_t off;
+
+    __device__ __forceinline__ Stager(int lane, int64_t row_stride)
+        : off((uint32_t)((lane >> 2) * (int)(row_stride * 2) + (((lane & 3) ^ ((lane >> 4) & 3)) << 4)))
+    {
+    }
+
+    // Group `group` of the tile whose first row is at `base` and which starts
+    // at `lds`; base, row_stride, rows, lds and group are the wave's.
+    __device__ __forceinline__ void load(const uint16_t* base, int64_t row_stride, int rows, uint32_t lds,
+                                         int group) const
+    {
+        const int left = rows - 16 * group;
+        const int n = left < 0 ? 0 : left > 16 ? 16 : left;
+        const int bytes = n ? (n - 1) * (int)(row_stride * 2) + 2 * D : 0;
+        const uint64_t a = reinterpret_cast<uint64_t>(base + 16 * group * row_stride);
+        const u32x4 rsrc = {scalar((uint32_t)a), scalar((uint32_t)(a >> 32) & 0xffffu),
+                            scalar((uint32_t)bytes), kRawBuffer};
+        const uint32_t to = lds + (group >> 1) * block_bytes<D>() + (group & 1) * 1024;
+        dma16<0>(rsrc, off, to);
+        dma16<1>(rsrc, off, to);
+        if constexpr (D > 64) {
+            dma16<2>(rsrc, off, to);
+            dma16<3>(rsrc, off, to);
+        }
+        if constexpr (D > 128) {
+            dma16<4>(rsrc, off, to);
+            dma16<5>(rsrc, off, to);
+            dma16<6>(rsrc, off, to);
+            dma16<7>(rsrc, off, to);
         }
     }
 
-    // `base`: the tile's first row; `lds`: byte address of the tile in LDS.
-    __device__ __forceinline__ void load(const uint16_t* base, int64_t row_stride, int rows, uint32_t lds,
-                                         int wave) const
-    {
-        const int n = rows < 0 ? 0 : rows > ROWS ? ROWS : rows;
-        const int bytes = n ? (n - 1) * (int)(row_stride * 2) + kRowBytes : 0;
-        const uint64_t a = reinterpret_cast<uint64_t>(base);
-        const u32x4 rsrc = {scalar((uint32_t)a), scalar((uint32_t)(a >> 32) & 0xffffu),
-                            scalar((uint32_t)bytes), kRawBuffer};
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            dma16(rsrc, off[i], lds + (wave * kPer + i) * 1024, i == 0);
-    }
-
-    // 64 x 16 bytes from buffer offsets `off` to LDS at `lds` + lane * 16.
+    // 64 x 16 bytes of slab C, from buffer offsets off + 64 C to LDS at `to` +
+    // C * kSlab + lane * 16 (the instruction's offset counts in both).
     // Written in assembly because the compiler, which cannot tell the halves
-    // of a double buffer apart, would wait for these loads before the next
-    // LDS read; wait_staged() waits for them.  The no-ops are the wait states
-    // after a scalar register written by the vector unit (the first load of a
-    // resource) and after m0.
-    static __device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t off, uint32_t lds, bool first)
+    // of a double buffer apart, would wait for these loads before the next LDS
+    // read; wait_staged() waits for them.  The no-ops are the wait states
+    // after a scalar register written by the vector unit (a new resource) and
+    // after m0.
+    template <int C>
+    static __device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t off, uint32_t to)
     {
-        const uint32_t at = scalar(lds);
-        if (first)
+        const uint32_t m0 = scalar(to + C * (kSlab - 64));
+        if constexpr (C == 0)
             __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                             : : "v"(off), "s"(rsrc), "s"(at) : "memory");
+                             : : "v"(off), "s"(rsrc), "s"(m0) : "memory");
         else
-            __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                             : : "v"(off), "s"(rsrc), "s"(at) : "memory");
+            __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\t"
+                             "buffer_load_dwordx4 %0, %1, 0 offen offset:%3 lds"
+                             : : "v"(off), "s"(rsrc), "s"(m0), "i"(64 * C) : "memory");
     }
 };
 
@@ -168,54 +226,14 @@ __device__ __forceinline__ void wait_staged()
     __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-__device__ __forceinline__ uint32_t lds_address(const void* p)
-{
-    return (uint32_t)reinterpret_cast<uintptr_t>(
-        (__attribute__((address_space(3))) const void*)p);
-}
+// Keeps a fragment in registers from here on: without it the compiler, which
+// does not know that the loads above count as well, waits for fragments loaded
+// ahead of a loop again in each of its rounds.
+__device__ __forceinline__ void settle(u32x4& f) { __asm__ volatile("" : "+v"(f)); }
 
-// The A or B fragment of rows n (of a 32-row block) and columns 16 kk + 8g..:
-// `at` is the byte offset of the lane's row start with (g ^ swizzle) applied.
-template <int D>
-__device__ __forceinline__ uint32_t row_offset(int lane)
-{
-    const int n = lane & 31, g = lane >> 5;
-    return n * 2 * D + ((g ^ swizzle<D>(n)) << 4);
-}
-
-template <int D>
-__device__ __forceinline__ u32x4 row_fragment(const char* tile, uint32_t at, int block, int kk)
-{
-    return *reinterpret_cast<const u32x4*>(tile + block * 64 * D + (at ^ (kk << 5)));
-}
-
-// The fragment whose lane index runs over 32 columns (column block db) and
-// whose k runs over the rows of k step s of a 32-row block, in the order of
-// packed C registers: two transposed reads, of rows 16s + 4g .. +3 and 8 more.
-template <int D>
-__device__ __forceinline__ uint32_t tr_offset(int lane)
-{
-    const int l = lane & 15, g = lane >> 5;
-    const int row = 4 * g + (l >> 2);
-    const int chunk = ((lane >> 4) & 1) * 2 + ((l & 3) >> 1);
-    return row * 2 * D + ((chunk ^ swizzle<D>(row)) << 4) + (l & 1) * 8;
-}
-
-__device__ __forceinline__ u32x2 tr_read(const char* p)
-{
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)const_cast<char*>(p)));
-}
-
-template <int D>
-__device__ __forceinline__ u32x4 tr_fragment(const char* tile, uint32_t at, int block, int s, int db)
-{
-    constexpr int kFlip = D == 64 ? 16 : 32;      // swizzle(row + 8) ^ swizzle(row), in bytes
-    const char* t = tile + block * 64 * D + s * 32 * D;
-    const u32x2 a = tr_read(t + (at ^ (db << 6)));
-    const u32x2 b = tr_read(t + 16 * D + (at ^ (db << 6) ^ kFlip));
-    return u32x4{a[0], a[1], b[0], b[1]};
-}
+// In a branch that few tiles take: keeps the compiler from turning it into
+// selects that all of them execute.
+__device__ __forceinline__ void keep_branch() { __asm__ volatile("" ::: "memory"); }
 
 // Column n (this lane's) of a C block, times `f`, as 16-bit elements d0 + 0..31
 // at `row`: the halves of the wave trade groups of 4 so that each lane stores

@@ -52,7 +52,7 @@ void attention_forward_kernel(const FwdParams p)
 {
     constexpr int BM = NW * 32, KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];   // [buffer][K, V]
+    __shared__ __attribute__((aligned(4 * kTile))) char lds[4 * kTile];   // [buffer][K, V]
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
@@ -103,30 +103,31 @@ void attention_forward_kernel(const FwdParams p)
         o[i] = f32x16{};
     float m = -INFINITY, l = 0.0f;         // m in units of log2 (scores times c)
 
-    Stager<D, BN, NW> ks, vs;
-    ks.init(wave, lane, p.k_ts);
-    vs.init(wave, lane, p.v_ts);
+    const Stager<D> ks(lane, p.k_ts), vs(lane, p.v_ts);
     const uint16_t* kbase = p.k + b * p.k_bs + hk * p.k_hs;
     const uint16_t* vbase = p.v + b * p.v_bs + hk * p.v_hs;
-    const uint32_t lds0 = lds_address(lds);
-    const uint32_t at_row = row_offset<D>(lane), at_tr = tr_offset<D>(lane);
+    uint32_t fill = lds_address(lds);
+    TileAt at(fill, lane);
+    const auto stage = [&](int t) {
+        const int64_t first = (int64_t)t * BN;
+#pragma unroll
+        for (int i = 0; i < BN / 16 / NW; ++i) {
+            ks.load(kbase + first * p.k_ts, p.k_ts, len - (int)first, fill, wave + i * NW);
+            vs.load(vbase + first * p.v_ts, p.v_ts, len - (int)first, fill + kTile, wave + i * NW);
+        }
+        fill ^= 2 * kTile;
+    };
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+        settle(qf[kk]);
 
-    if (t0 < t1) {
-        ks.load(kbase + (int64_t)t0 * BN * p.k_ts, p.k_ts, len - t0 * BN, lds0, wave);
-        vs.load(vbase + (int64_t)t0 * BN * p.v_ts, p.v_ts, len - t0 * BN, lds0 + kTile, wave);
-    }
+    if (t0 < t1)
+        stage(t0);
     for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
         wait_staged();
         __syncthreads();       // tile t is there, and the other buffer is free
-        if (t + 1 < t1) {
-            const int64_t next = (int64_t)(t + 1) * BN;
-            const uint32_t to = lds0 + (buf ^ 1) * 2 * kTile;
-            ks.load(kbase + next * p.k_ts, p.k_ts, len - (int)next, to, wave);
-            vs.load(vbase + next * p.v_ts, p.v_ts, len - (int)next, to + kTile, wave);
-        }
-        const char* kt = lds + buf * 2 * kTile;
-        const char* vt = kt + kTile;
+        if (t + 1 < t1)
+            stage(t + 1);
 
         f32x16 s[KB];
 #pragma unroll
@@ -134,9 +135,10 @@ void attention_forward_kernel(const FwdParams p)
             s[j] = f32x16{};
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-                s[j] = mfma<F16>(row_fragment<D>(kt, at_row, j, kk), qf[kk], s[j]);
+                s[j] = mfma<F16>(row_fragment(at, j * block_bytes<D>(), kk), qf[kk], s[j]);
         }
         if (t * BN + BN > open) {          // some key of the tile is hidden from some row
+            keep_branch();
             const int sees = CAUSAL ? (qi + shift + 1 < len ? qi + shift + 1 : len) : len;
 #pragma unroll
             for (int j = 0; j < KB; ++j)
@@ -179,8 +181,9 @@ void attention_forward_kernel(const FwdParams p)
                 const u32x4 pf = pack_b<F16>(s[j], k);
 #pragma unroll
                 for (int i = 0; i < DB; ++i)
-                    o[i] = mfma<F16>(tr_fragment<D>(vt, at_tr, j, k, i), pf, o[i]);
+                    o[i] = mfma<F16>(tr_fragment(at, kTile + j * block_bytes<D>(), k, i), pf, o[i]);
             }
+        at.flip(2 * kTile);
     }
 
     l = half_sum(l);
@@ -195,12 +198,12 @@ void attention_forward_kernel(const FwdParams p)
         if (valid && g == 0)
             p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + qi] = lse2 * kLn2;
     } else {
-        const int64_t at = (split * ((int64_t)gridDim.x / p.splits / p.row_blocks) + bh) * p.rows + r;
+        const int64_t slot = (split * ((int64_t)gridDim.x / p.splits / p.row_blocks) + bh) * p.rows + r;
 #pragma unroll
         for (int i = 0; i < DB; ++i)
-            store_column_f32(p.part_o + at * D + 32 * i, o[i], inv, g, valid);
+            store_column_f32(p.part_o + slot * D + 32 * i, o[i], inv, g, valid);
         if (valid && g == 0)
-            p.part_lse[at] = lse2;
+            p.part_lse[slot] = lse2;
     }
 }
 
