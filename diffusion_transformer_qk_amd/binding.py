@@ -205,6 +205,13 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+def _current_stream(torch, dev) -> int:
+    """The current raw stream of a device.  torch's own raw query saves the
+    1.7 us that building a stream object takes."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _call_context(ref, tensors, stream):
     """(device context, raw hipStream_t) for a call on ``ref``'s device.
 
@@ -217,7 +224,7 @@ def _call_context(ref, tensors, stream):
         if t is not None and t.device != dev:
             raise ValueError("all tensors must be on one device (%s)" % dev)
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream if ref.is_cuda else 0
+        raw = _current_stream(torch, dev) if ref.is_cuda else 0
     elif isinstance(stream, int):
         raw = stream
     else:
@@ -462,40 +469,41 @@ def group_norm_silu(x, gamma, beta, groups: int, *, out=None, eps: float = 1e-6,
     return out
 
 
-def _attn_tensor(t) -> AttnTensor:
-    b, n, h, _ = t.stride()
-    return AttnTensor(t.data_ptr(), b, n, h)
-
-
-def _attn_view(t, name: str):
-    """[tokens, heads, head_dim] counts as one sample."""
-    if t.dim() == 3:
-        t = t.unsqueeze(0)
-    if t.dim() != 4:
+def _attn_tensor(t, name: str) -> AttnTensor:
+    """t [batch, tokens, heads, head_dim], or without the batch of one sample."""
+    strides = t.stride()
+    if len(strides) == 3:
+        strides = (0, *strides)
+    if len(strides) != 4:
         raise ValueError("%s must be [batch, tokens, heads, head_dim]" % name)
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if strides[3] != 1 and t.shape[-1] > 1:
         raise ValueError("%s must be contiguous in its last dimension" % name)
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU")
-    return t
+    return AttnTensor(t.data_ptr(), strides[0], strides[1], strides[2])
 
 
 def _attn_args(q, k, v, causal, kv_lengths, scale) -> AttnArgs:
     torch = _torch()
-    batch, q_tokens, heads, head_dim = q.shape
-    if k.shape != v.shape or k.shape[0] != batch or k.shape[3] != head_dim:
+    shape, kv_shape = q.shape, k.shape
+    if len(shape) == 3:
+        shape = (1, *shape)
+        kv_shape = (1, *kv_shape)
+    if len(shape) != 4 or len(kv_shape) != 4:
+        raise ValueError("q, k and v must be [batch, tokens, heads, head_dim]")
+    batch, q_tokens, heads, head_dim = shape
+    if k.shape != v.shape or kv_shape[0] != batch or kv_shape[3] != head_dim:
         raise ValueError("k and v must be [%d, kv_tokens, kv_heads, %d]" % (batch, head_dim))
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have one dtype")
-    kv_heads = k.shape[2]
+    kv_heads = kv_shape[2]
     if kv_heads < 1 or heads % kv_heads:
         raise ValueError("the number of query heads must be a multiple of k's and v's")
     if kv_lengths is not None and (kv_lengths.dtype != torch.int32 or kv_lengths.shape != (batch,)):
         raise ValueError("kv_lengths must be int32 [batch]")
-    if scale is None:
-        scale = head_dim ** -0.5
-    return AttnArgs(batch, q_tokens, k.shape[1], heads, kv_heads, head_dim, 1 if causal else 0,
-                    _x_code(q), scale, _ptr(kv_lengths) or None)
+    return AttnArgs(batch, q_tokens, kv_shape[1], heads, kv_heads, head_dim, 1 if causal else 0,
+                    _x_code(q), head_dim ** -0.5 if scale is None else scale,
+                    None if kv_lengths is None else _ptr(kv_lengths))
 
 
 def _lse_shape(q):
@@ -550,8 +558,7 @@ def attention(q, k, v, *, causal: bool = False, kv_lengths=None, scale: float | 
     """
     torch = _torch()
     lib = load_library()
-    q4, k4, v4 = _attn_view(q, "q"), _attn_view(k, "k"), _attn_view(v, "v")
-    args = _attn_args(q4, k4, v4, causal, kv_lengths, scale)
+    args = _attn_args(q, k, v, causal, kv_lengths, scale)
     with _launch_stream_context(q, stream):
         workspace, ws_bytes = _attn_workspace(lib.dit_attention_workspace_size, args, workspace,
                                               q.device)
@@ -564,10 +571,9 @@ def attention(q, k, v, *, causal: bool = False, kv_lengths=None, scale: float | 
     _check_lse(lse, q)
     ctx, stream_ptr = _call_context(q, (k, v, out, lse, kv_lengths, workspace), stream)
     with ctx:
-        status = lib.dit_attention(
-            ctypes.byref(args), *[ctypes.byref(_attn_tensor(t)) for t in (q4, k4, v4,
-                                                                        _attn_view(out, "out"))],
-            _ptr(lse) or None, _ptr(workspace) or None, ws_bytes, stream_ptr or None)
+        status = lib.dit_attention(args, _attn_tensor(q, "q"), _attn_tensor(k, "k"),
+                                   _attn_tensor(v, "v"), _attn_tensor(out, "out"), _ptr(lse),
+                                   _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return out, lse
 
@@ -586,13 +592,16 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, kv_leng
     """
     torch = _torch()
     lib = load_library()
-    q4, k4, v4 = _attn_view(q, "q"), _attn_view(k, "k"), _attn_view(v, "v")
-    args = _attn_args(q4, k4, v4, causal, kv_lengths, scale)
+    args = _attn_args(q, k, v, causal, kv_lengths, scale)
     with _launch_stream_context(q, stream):
         workspace, ws_bytes = _attn_workspace(lib.dit_attention_backward_workspace_size, args,
                                               workspace, q.device)
-        dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if t is None else t
-                      for t, x in ((dq, q), (dk, k), (dv, v)))
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        if dv is None:
+            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     for name, t, like in (("dout", dout, q), ("out", out, q), ("dq", dq, q), ("dk", dk, k),
                           ("dv", dv, v)):
         if t.shape != like.shape or t.dtype != like.dtype:
@@ -602,11 +611,10 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, kv_leng
     ctx, stream_ptr = _call_context(q, (dout, k, v, out, lse, dq, dk, dv, kv_lengths, workspace),
                                     stream)
     with ctx:
-        t = [ctypes.byref(_attn_tensor(_attn_view(x, name)))
-             for x, name in ((dout, "dout"), (q4, "q"), (k4, "k"), (v4, "v"), (out, "out"),
-                             (dq, "dq"), (dk, "dk"), (dv, "dv"))]
-        status = lib.dit_attention_backward(ctypes.byref(args), *t[:5], _ptr(lse) or None, *t[5:],
-                                            _ptr(workspace) or None, ws_bytes, stream_ptr or None)
+        status = lib.dit_attention_backward(
+            args, _attn_tensor(dout, "dout"), _attn_tensor(q, "q"), _attn_tensor(k, "k"),
+            _attn_tensor(v, "v"), _attn_tensor(out, "out"), _ptr(lse), _attn_tensor(dq, "dq"),
+            _attn_tensor(dk, "dk"), _attn_tensor(dv, "dv"), _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return dq, dk, dv
 
@@ -635,9 +643,9 @@ def layer_norm(x, weight=None, bias=None, *, out=None, eps: float = 1e-6, stream
     ctx, stream_ptr = _call_context(x, (out, weight, bias), stream)
     with ctx:
         status = load_library().dit_layer_norm(
-            _ptr(x) or None, _ptr(out) or None, rows, hidden, _ptr(weight) or None,
-            _ptr(bias) or None, QKR_FP32 if one is None else _mod_code(one), float(eps), _x_code(x),
-            stream_ptr or None)
+            _ptr(x), _ptr(out), rows, hidden, _ptr(weight),
+            _ptr(bias), QKR_FP32 if one is None else _mod_code(one), float(eps), _x_code(x),
+            stream_ptr)
     _check(status)
     return out
 
@@ -660,8 +668,8 @@ def _norm_backward(dy, x, weight, form, rows_per_batch, params_shape, out, eps, 
     with _launch_stream_context(x, stream):
         if params_shape is not None:
             make = torch.empty if rows else torch.zeros     # without rows the sums are empty
-            dweight, dbias = (make(params_shape, dtype=torch.float32, device=x.device)
-                              for _ in range(2))
+            dweight = make(params_shape, dtype=torch.float32, device=x.device)
+            dbias = make(params_shape, dtype=torch.float32, device=x.device)
             if workspace is None:
                 need = int(lib.dit_layer_norm_backward_workspace_size(rows, hidden, rows_per_batch))
                 if need < 0:
@@ -676,10 +684,10 @@ def _norm_backward(dy, x, weight, form, rows_per_batch, params_shape, out, eps, 
     ctx, stream_ptr = _call_context(x, (dy, out, weight, workspace), stream)
     with ctx:
         status = lib.dit_layer_norm_backward(
-            _ptr(dy) or None, _ptr(x) or None, _ptr(out) or None, rows, hidden, rows_per_batch,
-            _ptr(weight) or None, form, QKR_FP32 if weight is None else _mod_code(weight),
-            _ptr(dweight) or None, _ptr(dbias) or None, float(eps), _x_code(x),
-            _ptr(workspace) or None, ws_bytes, stream_ptr or None)
+            _ptr(dy), _ptr(x), _ptr(out), rows, hidden, rows_per_batch,
+            _ptr(weight), form, QKR_FP32 if weight is None else _mod_code(weight),
+            _ptr(dweight), _ptr(dbias), float(eps), _x_code(x),
+            _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return out, dweight, dbias
 
@@ -773,7 +781,9 @@ def qknorm_rope_backward(dqkv=None, qkv=None, dq=None, dk=None, q=None, k=None, 
         if qkv.shape[-1] != 3 * heads * head_dim:
             raise ValueError("qkv last dimension must be 3*heads*head_dim")
         tokens = qkv.numel() // qkv.shape[-1] if qkv.numel() else 0
-        sets = {"qkv": (dqkv, qkv, dqkv if out is None else out)}
+        tensors = (dqkv, qkv, dqkv if out is None else out)
+        fused = GradTensor(_ptr(dqkv), _ptr(qkv), _ptr(tensors[2]))
+        of_q = of_k = None
     else:
         if qkv is not None or (dq is None) != (q is None) or (dk is None) != (k is None) \
                 or (q is None and k is None):
@@ -787,14 +797,19 @@ def qknorm_rope_backward(dqkv=None, qkv=None, dq=None, dk=None, q=None, k=None, 
             raise ValueError("q/k must be [..., heads, head_dim] = [..., %d, %d]"
                              % (heads, head_dim))
         tokens = ref.numel() // (heads * head_dim) if ref.numel() else 0
-        sets = {}
+        fused = of_q = of_k = None
+        tensors = ()
         if q is not None:
-            sets["q"] = (dq, q, dq if dq_out is None else dq_out)
+            tensors = (dq, q, dq if dq_out is None else dq_out)
+            of_q = GradTensor(*map(_ptr, tensors))
         if k is not None:
-            sets["k"] = (dk, k, dk if dk_out is None else dk_out)
-    flat = [t for s in sets.values() for t in s]
-    if any(t.shape != ref.shape or t.dtype != ref.dtype for t in flat):
-        raise ValueError("gradients, inputs and outputs must have one shape and dtype")
+            more = (dk, k, dk if dk_out is None else dk_out)
+            of_k = GradTensor(*map(_ptr, more))
+            tensors += more
+    shape, dtype = ref.shape, ref.dtype
+    for t in tensors:
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError("gradients, inputs and outputs must have one shape and dtype")
     if cos_layout not in LAYOUTS:
         raise ValueError("cos_layout must be one of %s" % sorted(LAYOUTS))
     if style not in STYLES:
@@ -811,22 +826,21 @@ def qknorm_rope_backward(dqkv=None, qkv=None, dq=None, dk=None, q=None, k=None, 
         if g is not None and (g.dtype != torch.float32 or g.numel() != head_dim):
             raise ValueError("gamma must be float32 [head_dim]")
     with _launch_stream_context(ref, stream):
-        dq_gamma, dk_gamma = (
-            torch.empty(head_dim, dtype=torch.float32, device=ref.device)
-            if dqkv is not None or name in sets else None for name in ("q", "k"))
+        dq_gamma = dk_gamma = None
+        if of_k is None or of_q is not None:
+            dq_gamma = torch.empty(head_dim, dtype=torch.float32, device=ref.device)
+        if of_q is None or of_k is not None:
+            dk_gamma = torch.empty(head_dim, dtype=torch.float32, device=ref.device)
         if workspace is None:
             need = qknorm_rope_backward_workspace_size(tokens, head_dim)
             if need > 0:
                 workspace = torch.empty(need, dtype=torch.uint8, device=ref.device)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    ctx, stream_ptr = _call_context(ref, (*flat, q_gamma, k_gamma, cos, sin, workspace), stream)
+    ctx, stream_ptr = _call_context(ref, (*tensors, q_gamma, k_gamma, cos, sin, workspace), stream)
     with ctx:
-        ptrs = {n: ctypes.byref(GradTensor(*(_ptr(t) or None for t in s))) for n, s in sets.items()}
         status = lib.qknorm_rope_backward(
-            ptrs.get("qkv"), ptrs.get("q"), ptrs.get("k"), tokens, heads, head_dim,
-            _ptr(q_gamma) or None, _ptr(k_gamma) or None, _ptr(dq_gamma) or None,
-            _ptr(dk_gamma) or None, float(eps), _ptr(cos) or None, _ptr(sin) or None,
-            LAYOUTS[cos_layout], _table_code(cos), STYLES[style], _x_code(ref),
-            _ptr(workspace) or None, ws_bytes, stream_ptr or None)
+            fused, of_q, of_k, tokens, heads, head_dim, _ptr(q_gamma), _ptr(k_gamma),
+            _ptr(dq_gamma), _ptr(dk_gamma), float(eps), _ptr(cos), _ptr(sin), LAYOUTS[cos_layout],
+            _table_code(cos), STYLES[style], _x_code(ref), _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return dq_gamma, dk_gamma

@@ -42,11 +42,18 @@ struct BwdParams {
     int64_t do_bs, do_ts, do_hs, q_bs, q_ts, q_hs, k_bs, k_ts, k_hs, v_bs, v_ts, v_hs;
     int64_t o_bs, o_ts, o_hs, dq_bs, dq_ts, dq_hs, dk_bs, dk_ts, dk_hs, dv_bs, dv_ts, dv_hs;
     int64_t batch;
+    uint32_t pairs;                           // batch * kv_heads
     int32_t q_tokens, kv_tokens, heads, kv_heads, group, rows;
     int32_t row_blocks, key_blocks;
+    int32_t row_splits, row_tiles_per_split;  // of the query tiles, in dkv
+    int32_t key_splits, key_tiles_per_split;  // of the key tiles, in dq
+    int32_t stat_blocks, value_blocks;        // runs of a head's rows, of a key head's values
     float scale, c;                           // c = scale * log2(e)
     float* stats;                             // [batch][heads][q_tokens][lse2, delta]
-    uint32_t* norms;                          // [batch][kv_heads][|dout|, |v|]: largest row norms (fp16)
+    float* row_norms;                         // fp16: [batch][heads][stat_blocks] largest |dout|
+    float* value_norms;                       // fp16: [batch][kv_heads][value_blocks] largest |v|
+    float* part_kv;                           // [row_splits][pairs][kv_tokens][dk, dv][D]
+    float* part_q;                            // [key_splits][pairs][rows][D]
 };
 
 template <bool F16>
@@ -61,87 +68,89 @@ __device__ __forceinline__ int bound_exponent(float bound)
     return __builtin_amdgcn_frexp_expf(bound);
 }
 
-__global__ __launch_bounds__(256) void clear_norms_kernel(uint32_t* norms, int64_t n)
-{
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < n)
-        norms[i] = 0;
-}
+// Rows of one workgroup of the kernel below: D / 8 lanes a row, 4 rows each.
+template <int D>
+constexpr int stat_rows() { return 4 * 256 / (D / 8); }
 
-// D / 8 lanes a row of (sample, head, query); a workgroup covers 256 / (D / 8)
-// queries of one head.  fp16: also the largest |dout| row of the key head
-// (norms are not negative, so their bits compare as integers, and a maximum
-// does not depend on the order of the atomics).
+// lse in base 2 and delta of a run of one head's queries.  fp16: also the
+// largest |dout| of the run, and in further workgroups the largest |v| of a run
+// of a key head's values in use.
 template <int D, bool F16>
 __global__ __launch_bounds__(256)
 void row_stats_kernel(const BwdParams p)
 {
     constexpr int L = D / 8, R = 256 / L;
-    const int64_t blocks = (p.q_tokens + R - 1) / R;
-    const int64_t bh = blockIdx.x / blocks;
-    const int64_t b = bh / p.heads;
-    const int h = bh % p.heads;
-    const int qi = (int)(blockIdx.x % blocks) * R + threadIdx.x / L;
-    const int d0 = threadIdx.x % L * 8;
-    float dot = 0.0f, sq = 0.0f;
-    if (qi < p.q_tokens) {
-        float x[8], y[8];
-        unpack8<F16>(load16<false>(p.dout + b * p.do_bs + qi * p.do_ts + h * p.do_hs + d0), x);
-        unpack8<F16>(load16<false>(p.out + b * p.o_bs + qi * p.o_ts + h * p.o_hs + d0), y);
+    __shared__ float tops[4];
+    const int d0 = threadIdx.x % L * 8, row0 = threadIdx.x / L;
+    const int64_t rows = p.batch * p.heads * p.stat_blocks;
+    float top = 0.0f;
+    if (blockIdx.x < rows) {
+        const int64_t bh = blockIdx.x / p.stat_blocks, b = bh / p.heads;
+        const int h = bh % p.heads;
+        const uint16_t* dor = p.dout + b * p.do_bs + h * p.do_hs + d0;
+        const uint16_t* outr = p.out + b * p.o_bs + h * p.o_hs + d0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            dot = __builtin_fmaf(x[i], y[i], dot);
-            if (F16)
-                sq = __builtin_fmaf(x[i], x[i], sq);
+        for (int i = 0; i < 4; ++i) {
+            const int64_t qi = (int64_t)(blockIdx.x % p.stat_blocks) * 4 * R + i * R + row0;
+            const bool there = qi < p.q_tokens;
+            float x[8], y[8];
+            unpack8<F16>(there ? load16<false>(dor + qi * p.do_ts) : u32x4{0, 0, 0, 0}, x);
+            unpack8<F16>(there ? load16<false>(outr + qi * p.o_ts) : u32x4{0, 0, 0, 0}, y);
+            float dot = 0.0f, sq = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dot = __builtin_fmaf(x[j], y[j], dot);
+                if (F16)
+                    sq = __builtin_fmaf(x[j], x[j], sq);
+            }
+#pragma unroll
+            for (int w = 1; w < L; w *= 2) {
+                dot += __shfl_xor(dot, w);
+                if (F16)
+                    sq += __shfl_xor(sq, w);
+            }
+            top = fmaxf(top, sq);
+            if (there && d0 == 0) {
+                const float lse = p.lse[bh * p.q_tokens + qi];
+                // a query without keys: exp2(s - inf) is 0 for every score
+                const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+                reinterpret_cast<f32x2*>(p.stats)[bh * p.q_tokens + qi] = f32x2{lse2, dot};
+            }
+        }
+    } else if constexpr (F16) {
+        const int64_t at = blockIdx.x - rows, bh = at / p.value_blocks, b = bh / p.kv_heads;
+        int len = p.kv_tokens;
+        if (p.kv_lengths && p.kv_lengths[b] < len)
+            len = p.kv_lengths[b];
+        const uint16_t* vr = p.v + b * p.v_bs + bh % p.kv_heads * p.v_hs + d0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t j = at % p.value_blocks * 4 * R + i * R + row0;
+            float x[8], sq = 0.0f;
+            unpack8<true>(j < len ? load16<false>(vr + j * p.v_ts) : u32x4{0, 0, 0, 0}, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sq = __builtin_fmaf(x[k], x[k], sq);
+#pragma unroll
+            for (int w = 1; w < L; w *= 2)
+                sq += __shfl_xor(sq, w);
+            top = fmaxf(top, sq);
         }
     }
-#pragma unroll
-    for (int w = 1; w < L; w *= 2) {
-        dot += __shfl_xor(dot, w);
-        if (F16)
-            sq += __shfl_xor(sq, w);
-    }
-    if (qi < p.q_tokens && threadIdx.x % L == 0) {
-        const float lse = p.lse[bh * p.q_tokens + qi];
-        // a query without keys: exp2(s - inf) is 0 for every score
-        const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
-        reinterpret_cast<f32x2*>(p.stats)[bh * p.q_tokens + qi] = f32x2{lse2, dot};
-    }
     if constexpr (F16) {
-        const float top = wave_max(sq);
-        if (threadIdx.x % 64 == 0)
-            atomicMax(p.norms + (b * p.kv_heads + h / p.group) * 2, __float_as_uint(sqrtf(top)));
+        top = block_max<4>(top, tops);
+        if (threadIdx.x == 0)
+            (blockIdx.x < rows ? p.row_norms : p.value_norms - rows)[blockIdx.x] = sqrtf(top);
     }
 }
 
-// fp16: the largest row norm of each sample's and key head's values in use.
-template <int D>
-__global__ __launch_bounds__(256)
-void value_norms_kernel(const BwdParams p)
+// The largest of n values, by all threads of a workgroup of 4 waves.
+__device__ __forceinline__ float largest(const float* v, int n, float* slot)
 {
-    constexpr int L = D / 8, R = 256 / L;
-    const int64_t blocks = (p.kv_tokens + R - 1) / R;
-    const int64_t bh = blockIdx.x / blocks;
-    const int64_t b = bh / p.kv_heads;
-    const int j = (int)(blockIdx.x % blocks) * R + threadIdx.x / L;
-    int len = p.kv_tokens;
-    if (p.kv_lengths && p.kv_lengths[b] < len)
-        len = p.kv_lengths[b];
-    float sq = 0.0f;
-    if (j < len) {
-        float x[8];
-        unpack8<true>(load16<false>(p.v + b * p.v_bs + j * p.v_ts + (bh % p.kv_heads) * p.v_hs +
-                                    threadIdx.x % L * 8), x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            sq = __builtin_fmaf(x[i], x[i], sq);
-    }
-#pragma unroll
-    for (int w = 1; w < L; w *= 2)
-        sq += __shfl_xor(sq, w);
-    const float top = wave_max(sq);
-    if (threadIdx.x % 64 == 0)
-        atomicMax(p.norms + bh * 2 + 1, __float_as_uint(sqrtf(top)));
+    float top = 0.0f;
+    for (int i = threadIdx.x; i < n; i += 256)
+        top = fmaxf(top, v[i]);
+    return block_max<4>(top, slot);
 }
 
 // ---------------------------------------------------------------- dk and dv
@@ -160,9 +169,9 @@ void attention_dkv_kernel(const BwdParams p)
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const int64_t block = logical_block<-1>(blockIdx.x, gridDim.x);
-    const int kb = block % p.key_blocks;
-    const int64_t bh = block / p.key_blocks;
+    const BlockOf block(blockIdx.x, p.pairs, p.key_blocks * p.row_splits);
+    const int kb = block.part % p.key_blocks, split = block.part / p.key_blocks;
+    const int64_t bh = block.pair;
     const int64_t b = bh / p.kv_heads;
     const int hk = bh % p.kv_heads;
     int len = p.kv_tokens;
@@ -182,7 +191,9 @@ void attention_dkv_kernel(const BwdParams p)
     }
     const int tiles = (p.q_tokens + BQ - 1) / BQ;
     const int per = tiles > first ? tiles - first : 0;    // tiles of one query head
-    const int total = kb * BK < len ? per * p.group : 0;
+    const int all = kb * BK < len ? per * p.group : 0;
+    const int t0 = split * p.row_tiles_per_split;
+    const int total = (all < t0 + p.row_tiles_per_split ? all : t0 + p.row_tiles_per_split) - t0;
 
     u32x4 kf[D / 16], vf[D / 16];
     {
@@ -197,7 +208,10 @@ void attention_dkv_kernel(const BwdParams p)
     float down = 1.0f;            // brings dp - delta below 1
     int e = 0;
     if constexpr (F16) {
-        e = bound_exponent(__uint_as_float(p.norms[bh * 2]) * __uint_as_float(p.norms[bh * 2 + 1])) + 1;
+        __shared__ float tops[8];
+        const int n = p.group * p.stat_blocks;
+        e = bound_exponent(largest(p.row_norms + bh * n, n, tops) *
+                           largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops + 4)) + 1;
         down = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
     f32x16 dk[DB], dv[DB];
@@ -218,7 +232,7 @@ void attention_dkv_kernel(const BwdParams p)
 
     // the tiles run through the queries of one head of the group after another;
     // h and next_q: the next one to be staged
-    int h = hk * p.group, next_q = first * BQ;
+    int h = hk * p.group + (per ? t0 / per : 0), next_q = (first + (per ? t0 % per : 0)) * BQ;
     const auto stage = [&](int buf) {
         const int left = p.q_tokens - next_q;
         rows.load(stage_base + (int64_t)next_q * stage_ts + h * stage_hs, stage_ts, left,
@@ -243,9 +257,9 @@ void attention_dkv_kernel(const BwdParams p)
         settle(kf[kk]);
         settle(vf[kk]);
     }
+    int q0 = next_q;
     if (total > 0)
         stage(0);
-    int q0 = first * BQ;
     for (int t = 0; t < total; ++t) {
         const int buf = t & 1;
         wait_staged();
@@ -300,16 +314,28 @@ void attention_dkv_kernel(const BwdParams p)
 
     const bool valid = key < p.kv_tokens;
     const int64_t to = valid ? key : p.kv_tokens - 1;
-    uint16_t* kr = p.dk + b * p.dk_bs + to * p.dk_ts + hk * p.dk_hs + 32 * db0;
-    uint16_t* vr = p.dv + b * p.dv_bs + to * p.dv_ts + hk * p.dv_hs + 32 * db0;
     const float fv = F16 ? 0x1p-15f : 1.0f;
     const float fk = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
+    if (key >= len) {             // the scores of a padding key are no scores
 #pragma unroll
-    for (int i = 0; i < DB; ++i) {
-        if (key >= len)           // the scores of a padding key are no scores
+        for (int i = 0; i < DB; ++i)
             dk[i] = dv[i] = f32x16{};
-        store_column<F16>(kr + 32 * i, dk[i], fk, g, valid);
-        store_column<F16>(vr + 32 * i, dv[i], fv, g, valid);
+    }
+    if (p.row_splits == 1) {
+        uint16_t* kr = p.dk + b * p.dk_bs + to * p.dk_ts + hk * p.dk_hs + 32 * db0;
+        uint16_t* vr = p.dv + b * p.dv_bs + to * p.dv_ts + hk * p.dv_hs + 32 * db0;
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+            store_column<F16>(kr + 32 * i, dk[i], fk, g, valid);
+            store_column<F16>(vr + 32 * i, dv[i], fv, g, valid);
+        }
+    } else {
+        float* row = p.part_kv + ((split * (int64_t)p.pairs + bh) * p.kv_tokens + to) * 2 * D + 32 * db0;
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+            store_column_f32(row + 32 * i, dk[i], fk, g, valid);
+            store_column_f32(row + D + 32 * i, dv[i], fv, g, valid);
+        }
     }
 }
 
@@ -325,9 +351,9 @@ void attention_dq_kernel(const BwdParams p)
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const int64_t block = logical_block<-1>(blockIdx.x, gridDim.x);
-    const int mb_raw = block % p.row_blocks;
-    const int64_t bh = block / p.row_blocks;
+    const BlockOf block(blockIdx.x, p.pairs, p.row_blocks * p.key_splits);
+    const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
+    const int64_t bh = block.pair;
     const int64_t b = bh / p.kv_heads;
     const int hk = bh % p.kv_heads;
     const int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;
@@ -346,7 +372,9 @@ void attention_dq_kernel(const BwdParams p)
         const int sees = last / p.group + shift + 1;
         end = sees < end ? (sees < 0 ? 0 : sees) : end;
     }
-    const int tiles = (end + BN - 1) / BN;
+    const int all = (end + BN - 1) / BN;
+    const int t0 = split * p.key_tiles_per_split;
+    const int tiles = all < t0 + p.key_tiles_per_split ? all : t0 + p.key_tiles_per_split;
     int open = len;
     if (CAUSAL) {
         const int s = (r0 < p.rows ? r0 : p.rows - 1) / p.group + shift + 1;
@@ -377,7 +405,9 @@ void attention_dq_kernel(const BwdParams p)
             for (int i = 0; i < 8; ++i)
                 sq = __builtin_fmaf(x[i], x[i], sq);
         }
-        e = bound_exponent(sqrtf(half_sum(sq)) * __uint_as_float(p.norms[bh * 2 + 1])) + 1;
+        __shared__ float tops[4];
+        e = bound_exponent(sqrtf(half_sum(sq)) *
+                           largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops)) + 1;
         down = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
     f32x16 dq[DB];
@@ -405,9 +435,9 @@ void attention_dq_kernel(const BwdParams p)
         settle(df[kk]);
     }
 
-    if (tiles > 0)
-        stage(0);
-    for (int t = 0; t < tiles; ++t) {
+    if (t0 < tiles)
+        stage(t0);
+    for (int t = t0; t < tiles; ++t) {
         wait_staged();
         __syncthreads();
         if (t + 1 < tiles)
@@ -446,50 +476,130 @@ void attention_dq_kernel(const BwdParams p)
     }
 
     const bool valid = r0 + n < p.rows;
-    uint16_t* row = p.dq + b * p.dq_bs + qi * p.dq_ts + head * p.dq_hs;
     const float f = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
+    if (p.key_splits == 1) {
+        uint16_t* row = p.dq + b * p.dq_bs + qi * p.dq_ts + head * p.dq_hs;
 #pragma unroll
-    for (int i = 0; i < DB; ++i)
-        store_column<F16>(row + 32 * i, dq[i], f, g, valid);
+        for (int i = 0; i < DB; ++i)
+            store_column<F16>(row + 32 * i, dq[i], f, g, valid);
+    } else {
+        float* row = p.part_q + ((split * (int64_t)p.pairs + bh) * p.rows + r) * D;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+            store_column_f32(row + 32 * i, dq[i], f, g, valid);
+    }
+}
+
+// Adds the splits' dk and dv, or dq, in order: D / 8 threads a row.
+template <int D, bool F16, bool KV>
+__global__ __launch_bounds__(256)
+void attention_sum_kernel(const BwdParams p)
+{
+    constexpr int L = D / 8, R = 256 / L;
+    const int64_t rows = (int64_t)p.pairs * (KV ? 2 * (int64_t)p.kv_tokens : p.rows);
+    const int64_t at = (int64_t)blockIdx.x * R + threadIdx.x / L;
+    if (at >= rows)
+        return;
+    const int d0 = threadIdx.x % L * 8;
+    const float* part = (KV ? p.part_kv : p.part_q) + at * D + d0;
+    const int splits = KV ? p.row_splits : p.key_splits;
+    float s[8] = {};
+#pragma unroll 4
+    for (int i = 0; i < splits; ++i) {
+        float f[8];
+        load_f32x8(part + i * rows * D, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s[j] += f[j];
+    }
+    uint16_t* to;
+    if constexpr (KV) {
+        const int64_t key = at / 2 % p.kv_tokens, bh = at / 2 / p.kv_tokens;
+        const int64_t b = bh / p.kv_heads, h = bh % p.kv_heads;
+        to = at % 2 ? p.dv + b * p.dv_bs + key * p.dv_ts + h * p.dv_hs
+                    : p.dk + b * p.dk_bs + key * p.dk_ts + h * p.dk_hs;
+    } else {
+        const int64_t bh = at / p.rows, b = bh / p.kv_heads;
+        const int r = at % p.rows;
+        to = p.dq + b * p.dq_bs + r / p.group * p.dq_ts + (bh % p.kv_heads * p.group + r % p.group) * p.dq_hs;
+    }
+    store16<false>(to + d0, pack8<F16>(s));
 }
 
 // ---------------------------------------------------------------- launches
 
-template <int D>
-constexpr int waves_per_key_block() { return D == 256 ? 2 : 1; }
-
 constexpr int kWaves = 4;
+
+constexpr int waves_per_key_block(int d) { return d == 256 ? 2 : 1; }
+
+// How a call is cut up, and where its workspace's parts begin (in floats).
+struct Shape {
+    int64_t row_blocks, key_blocks, row_splits, row_tiles_per_split, key_splits, key_tiles_per_split;
+    int64_t stat_blocks, value_blocks;
+    int64_t row_norms, value_norms, part_kv, part_q, floats;
+};
+
+// The splits of `tiles` tiles that let `blocks` workgroups fill a chip that
+// holds `resident`: none if they fill half of it, and runs of at least `least`
+// tiles (about 10 us of work, twice what the launch that adds them costs).
+void cut(int64_t blocks, int64_t resident, int64_t tiles, int64_t least, int64_t& splits, int64_t& each)
+{
+    splits = 1;
+    if (blocks > 0 && 2 * blocks <= resident && tiles >= 2 * least) {
+        splits = resident / blocks;
+        if (splits > tiles / least)
+            splits = tiles / least;
+    }
+    each = (tiles + splits - 1) / splits;
+    if (each < 1)
+        each = 1;
+    splits = tiles ? (tiles + each - 1) / each : 1;
+}
+
+Shape shape_of(const dit_attn_args& a)
+{
+    Shape s;
+    const int64_t group = a.heads / a.kv_heads, rows = a.q_tokens * group;
+    const int64_t pairs = a.batch * a.kv_heads;
+    const int64_t bk = 32 * kWaves / waves_per_key_block(a.head_dim), bm = 32 * kWaves;
+    s.row_blocks = (rows + bm - 1) / bm;
+    s.key_blocks = (a.kv_tokens + bk - 1) / bk;
+    const int64_t resident = a.head_dim == 256 ? 256 : 512;
+    cut(pairs * s.key_blocks, resident, (a.q_tokens + 31) / 32 * group, 16, s.row_splits,
+        s.row_tiles_per_split);
+    cut(pairs * s.row_blocks, resident, (a.kv_tokens + 63) / 64, 8, s.key_splits,
+        s.key_tiles_per_split);
+    const int64_t run = 4 * 256 / (a.head_dim / 8);
+    s.stat_blocks = (a.q_tokens + run - 1) / run;
+    s.value_blocks = (a.kv_tokens + run - 1) / run;
+    const auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
+    s.row_norms = whole(a.batch * a.heads * a.q_tokens * 2);
+    s.value_norms = s.row_norms + whole(a.batch * a.heads * s.stat_blocks);
+    s.part_kv = s.value_norms + whole(pairs * s.value_blocks);
+    s.part_q = s.part_kv + (s.row_splits > 1 ? s.row_splits * pairs * a.kv_tokens * 2 * a.head_dim : 0);
+    s.floats = s.part_q + (s.key_splits > 1 ? s.key_splits * pairs * rows * a.head_dim : 0);
+    return s;
+}
 
 template <int D, bool F16, bool CAUSAL>
 hipError_t launch(BwdParams p, hipStream_t st)
 {
-    constexpr int DS = waves_per_key_block<D>(), BK = 32 * kWaves / DS;
-    constexpr int R = 256 / (D / 8);
-    p.row_blocks = (p.rows + 32 * kWaves - 1) / (32 * kWaves);
-    p.key_blocks = (p.kv_tokens + BK - 1) / BK;
-    const int64_t pairs = p.batch * p.kv_heads;
+    constexpr int DS = waves_per_key_block(D), R = 256 / (D / 8);
+    const int64_t pairs = p.pairs;
     void* argv[] = {&p};
-    const auto go = [&](const void* fn, int64_t blocks) {
-        return blocks ? hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), argv, 0, st) : hipSuccess;
-    };
     hipError_t err = hipSuccess;
-    if (F16) {
-        int64_t count = pairs * 2;
-        void* cargs[] = {&p.norms, &count};
-        err = hipLaunchKernel(reinterpret_cast<const void*>(clear_norms_kernel),
-                              dim3((unsigned)((count + 255) / 256)), dim3(256), cargs, 0, st);
-        if (err == hipSuccess)
-            err = go(reinterpret_cast<const void*>(value_norms_kernel<D>), pairs * ((p.kv_tokens + R - 1) / R));
-    }
-    if (err == hipSuccess)
-        err = go(reinterpret_cast<const void*>(row_stats_kernel<D, F16>),
-                 p.batch * p.heads * ((p.q_tokens + R - 1) / R));
-    if (err == hipSuccess)
-        err = go(reinterpret_cast<const void*>(attention_dkv_kernel<D, F16, CAUSAL, kWaves, DS>),
-                 pairs * p.key_blocks);
-    if (err == hipSuccess)
-        err = go(reinterpret_cast<const void*>(attention_dq_kernel<D, F16, CAUSAL, kWaves, 64>),
-                 pairs * p.row_blocks);
+    const auto go = [&](auto fn, int64_t blocks) {
+        if (err == hipSuccess && blocks)
+            err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)blocks), dim3(256),
+                                  argv, 0, st);
+    };
+    go(row_stats_kernel<D, F16>, p.batch * p.heads * p.stat_blocks + (F16 ? pairs * p.value_blocks : 0));
+    go(attention_dkv_kernel<D, F16, CAUSAL, kWaves, DS>, pairs * p.key_blocks * p.row_splits);
+    go(attention_dq_kernel<D, F16, CAUSAL, kWaves, 64>, pairs * p.row_blocks * p.key_splits);
+    if (p.row_splits > 1)
+        go(attention_sum_kernel<D, F16, true>, (pairs * 2 * p.kv_tokens + R - 1) / R);
+    if (p.key_splits > 1)
+        go(attention_sum_kernel<D, F16, false>, (pairs * p.rows + R - 1) / R);
     return err;
 }
 
@@ -506,9 +616,7 @@ hipError_t launch(const BwdParams& p, bool f16, bool causal, hipStream_t st)
 extern "C" int64_t dit_attention_backward_workspace_size(const dit_attn_args* args)
 {
     const int rc = qkr_attn_host::check_args(args);
-    if (rc != QKR_OK)
-        return rc;
-    return args->batch * args->heads * args->q_tokens * 8 + args->batch * args->kv_heads * 8;
+    return rc != QKR_OK ? rc : shape_of(*args).floats * 4;
 }
 
 extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_tensor* dout,
@@ -536,7 +644,7 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     if (reinterpret_cast<uintptr_t>(lse) & 3u || reinterpret_cast<uintptr_t>(a.kv_lengths) & 3u)
         return QKR_ERR_ALIGN;
     const int64_t need = dit_attention_backward_workspace_size(args);
-    if (!workspace || workspace_bytes < need)
+    if (need && (!workspace || workspace_bytes < need))
         return QKR_ERR_WORKSPACE;
     if (!qkr_host::aligned16(workspace))
         return QKR_ERR_ALIGN;
@@ -578,6 +686,7 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
     p.batch = a.batch;
+    p.pairs = (uint32_t)(a.batch * a.kv_heads);
     p.q_tokens = (int32_t)a.q_tokens;
     p.kv_tokens = (int32_t)a.kv_tokens;
     p.heads = a.heads;
@@ -587,7 +696,19 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     p.scale = a.scale;
     p.c = a.scale * kLog2e;
     p.stats = static_cast<float*>(workspace);
-    p.norms = reinterpret_cast<uint32_t*>(p.stats + a.batch * a.heads * a.q_tokens * 2);
+    const Shape shape = shape_of(a);
+    p.row_blocks = (int32_t)shape.row_blocks;
+    p.key_blocks = (int32_t)shape.key_blocks;
+    p.row_splits = (int32_t)shape.row_splits;
+    p.row_tiles_per_split = (int32_t)shape.row_tiles_per_split;
+    p.key_splits = (int32_t)shape.key_splits;
+    p.key_tiles_per_split = (int32_t)shape.key_tiles_per_split;
+    p.stat_blocks = (int32_t)shape.stat_blocks;
+    p.value_blocks = (int32_t)shape.value_blocks;
+    p.row_norms = p.stats + shape.row_norms;
+    p.value_norms = p.stats + shape.value_norms;
+    p.part_kv = p.stats + shape.part_kv;
+    p.part_q = p.stats + shape.part_q;
     const bool f16 = a.dtype == QKR_FP16, causal = a.causal != 0;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const hipError_t err = a.head_dim == 64    ? launch<64>(p, f16, causal, st)

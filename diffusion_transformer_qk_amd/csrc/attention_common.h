@@ -41,6 +41,32 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kRawBuffer = 0x00020000u;   // raw buffer resource, 32-bit data
 
+// The (pair, part) of hardware block `bid`, for `pairs` (sample, key head) pairs
+// of `parts` blocks each.  The dispatcher deals consecutive blocks to
+// consecutive dies, and the blocks of a pair read the same keys, so a pair
+// stays on one die, with its L2: die d takes pairs d, d + 8, ...  (Neighbouring
+// pairs, which are of one sample and so of one length, go to different dies.)
+// The last pairs % 8 are cut into eighths, one a die.
+struct BlockOf {
+    int64_t pair;
+    int32_t part;
+
+    __device__ __forceinline__ BlockOf(uint32_t bid, uint32_t pairs, uint32_t parts)
+    {
+        const uint32_t whole = pairs / kXcds * kXcds;
+        const uint32_t die = bid % kXcds, local = bid / kXcds;
+        if (bid < whole * parts) {
+            pair = local / parts * kXcds + die;
+            part = local % parts;
+        } else {
+            const uint32_t blocks = (pairs - whole) * parts;
+            const uint32_t at = (uint32_t)logical_block<-1>(bid - whole * parts, blocks);
+            pair = whole + at / parts;
+            part = at % parts;
+        }
+    }
+};
+
 template <bool F16>
 __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
 {
@@ -76,6 +102,19 @@ __device__ __forceinline__ u32x4 pack_b(const f32x16& c, int s)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         w[j] = pack2<F16>(c[8 * s + 2 * j], c[8 * s + 2 * j + 1]);
+    return w;
+}
+
+// What the rounding of pack_b left: the difference, packed the same way.
+template <bool F16>
+__device__ __forceinline__ u32x4 pack_rest(const f32x16& c, int s, u32x4 packed)
+{
+    float f[8];
+    unpack8<F16>(packed, f);
+    u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = pack2<F16>(c[8 * s + 2 * j] - f[2 * j], c[8 * s + 2 * j + 1] - f[2 * j + 1]);
     return w;
 }
 

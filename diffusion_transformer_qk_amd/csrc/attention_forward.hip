@@ -33,6 +33,7 @@ struct FwdParams {
     int64_t q_bs, q_ts, q_hs, k_bs, k_ts, k_hs, v_bs, v_ts, v_hs, o_bs, o_ts, o_hs;
     int32_t q_tokens, kv_tokens, kv_heads, group, rows;    // rows = q_tokens * group
     int32_t row_blocks;
+    uint32_t pairs;                           // batch * kv_heads
     int32_t splits, tiles_per_split;
     float c;                                  // scale * log2(e)
     float* part_o;                            // [splits][batch * kv_heads * rows][D]
@@ -52,15 +53,17 @@ void attention_forward_kernel(const FwdParams p)
 {
     constexpr int BM = NW * 32, KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
+    // With one wave the call waits for memory, and p can have a second term,
+    // what its rounding to 16 bits left: out is then off by its own rounding
+    // alone.
+    constexpr bool kTwoTerms = NW == 1;
     __shared__ __attribute__((aligned(4 * kTile))) char lds[4 * kTile];   // [buffer][K, V]
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    int64_t block = logical_block<-1>(blockIdx.x, gridDim.x);
-    const int mb_raw = block % p.row_blocks;
-    block /= p.row_blocks;
-    const int split = block % p.splits;
-    const int64_t bh = block / p.splits;                 // sample, key head
+    const BlockOf block(blockIdx.x, p.pairs, p.row_blocks * p.splits);
+    const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
+    const int64_t bh = block.pair;                       // sample, key head
     const int64_t b = bh / p.kv_heads;
     const int hk = bh % p.kv_heads;
     const int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;   // the longest first
@@ -179,9 +182,16 @@ void attention_forward_kernel(const FwdParams p)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const u32x4 pf = pack_b<F16>(s[j], k);
+                u32x4 rest;
+                if constexpr (kTwoTerms)
+                    rest = pack_rest<F16>(s[j], k, pf);
 #pragma unroll
-                for (int i = 0; i < DB; ++i)
-                    o[i] = mfma<F16>(tr_fragment(at, kTile + j * block_bytes<D>(), k, i), pf, o[i]);
+                for (int i = 0; i < DB; ++i) {
+                    const u32x4 vf = tr_fragment(at, kTile + j * block_bytes<D>(), k, i);
+                    o[i] = mfma<F16>(vf, pf, o[i]);
+                    if constexpr (kTwoTerms)
+                        o[i] = mfma<F16>(vf, rest, o[i]);
+                }
             }
         at.flip(2 * kTile);
     }
@@ -198,7 +208,7 @@ void attention_forward_kernel(const FwdParams p)
         if (valid && g == 0)
             p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + qi] = lse2 * kLn2;
     } else {
-        const int64_t slot = (split * ((int64_t)gridDim.x / p.splits / p.row_blocks) + bh) * p.rows + r;
+        const int64_t slot = (split * (int64_t)p.pairs + bh) * p.rows + r;
 #pragma unroll
         for (int i = 0; i < DB; ++i)
             store_column_f32(p.part_o + slot * D + 32 * i, o[i], inv, g, valid);
@@ -207,38 +217,50 @@ void attention_forward_kernel(const FwdParams p)
     }
 }
 
-// Joins the splits of a row: out = sum_k 2^(lse_k - lse) out_k.  A wave a row.
+// Joins the splits of a row: out = sum_k 2^(lse_k - lse) out_k.  A workgroup a
+// row: D / 4 threads hold 4 columns each, 1024 / D such sets take every
+// (1024 / D)th split.
 template <int D, bool F16>
 __global__ __launch_bounds__(256)
-void attention_join_kernel(const FwdParams p, int64_t total)
+void attention_join_kernel(const FwdParams p)
 {
-    const int lane = threadIdx.x % 64;
-    const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-    if (at >= total)
-        return;
+    constexpr int L = D / 4, S = 256 / L;
+    __shared__ float tops[4];
+    __shared__ f32x4 sums[S][L];
+    __shared__ float weights[S];
+    const int64_t total = (int64_t)p.pairs * p.rows, at = blockIdx.x;
     float top = -INFINITY;
-    for (int k = lane; k < p.splits; k += 64)
+    for (int k = threadIdx.x; k < p.splits; k += 256)
         top = fmaxf(top, p.part_lse[k * total + at]);
-    top = wave_max(top);
+    top = block_max<4>(top, tops);
     const float base = top == -INFINITY ? 0.0f : top;
-    constexpr int E = D / 64;
-    float o[E] = {}, l = 0.0f;
-    for (int k = 0; k < p.splits; ++k) {
+    const int set = threadIdx.x / L, col = threadIdx.x % L * 4;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    float l = 0.0f;
+#pragma unroll 4
+    for (int k = set; k < p.splits; k += S) {
         const float w = __builtin_amdgcn_exp2f(p.part_lse[k * total + at] - base);
         l += w;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = __builtin_fmaf(w, p.part_o[(k * total + at) * D + lane * E + e], o[e]);
+        o += w * *reinterpret_cast<const f32x4*>(p.part_o + (k * total + at) * D + col);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    sums[set][threadIdx.x % L] = o;
+    if (threadIdx.x % L == 0)
+        weights[set] = l;
+    __syncthreads();
+    if (set > 0)
+        return;
+#pragma unroll
+    for (int i = 1; i < S; ++i) {
+        o += sums[i][threadIdx.x];
+        l += weights[i];
+    }
+    o *= l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t bh = at / p.rows, b = bh / p.kv_heads;
     const int r = at % p.rows, qi = r / p.group;
     const int head = (int)(bh % p.kv_heads) * p.group + r % p.group;
-    uint16_t* row = p.out + b * p.o_bs + qi * p.o_ts + head * p.o_hs + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        row[e] = (uint16_t)pack2<F16>(o[e] * inv, 0.0f);
-    if (lane == 0)
+    *reinterpret_cast<u32x2*>(p.out + b * p.o_bs + qi * p.o_ts + head * p.o_hs + col) =
+        u32x2{pack2<F16>(o[0], o[1]), pack2<F16>(o[2], o[3])};
+    if (threadIdx.x == 0)
         p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + qi] =
             l == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(l)) * kLn2;
 }
@@ -248,30 +270,60 @@ struct Shape {
     int64_t row_blocks, splits, tiles_per_split;
 };
 
+// Up to 32 rows of a pair (one query, and a few) are one wave's, with tiles of
+// 32 keys: nothing is shared in the workgroup, and as many of them as their
+// LDS allows keep loads in flight.  Calls that leave CUs idle cut the keys:
+// into as many runs as fill the chip once, of at least 8 tiles (4 of the
+// smaller ones), or the launch that joins them costs what they save.
+
 Shape shape_of(const dit_attn_args& a)
 {
     Shape s;
     const int64_t rows = a.q_tokens * (a.heads / a.kv_heads);
-    s.waves = 4;
-    s.tile = 64;
+    s.waves = rows <= 32 ? 1 : 4;
+    s.tile = rows <= 32 ? 32 : 64;
     s.row_blocks = (rows + 32 * s.waves - 1) / (32 * s.waves);
+    const int64_t blocks = s.row_blocks * a.batch * a.kv_heads;
+    const int64_t tiles = (a.kv_tokens + s.tile - 1) / s.tile;
+    // workgroups resident at once: their double buffers in 160 KB of LDS each
+    // CU, at most two of four waves
+    const int64_t per_cu = 160 * 1024 / (8 * s.tile * a.head_dim);
+    const int64_t resident = 256 * (s.waves == 4 && per_cu > 2 ? 2 : per_cu > 8 ? 8 : per_cu);
+    const int64_t least = s.waves == 1 ? 4 : 8;
     s.splits = 1;
-    s.tiles_per_split = (a.kv_tokens + s.tile - 1) / s.tile;
+    if (blocks > 0 && 2 * blocks <= resident && tiles >= 2 * least) {
+        s.splits = resident / blocks;
+        if (s.splits > tiles / least)
+            s.splits = tiles / least;
+    }
+    s.tiles_per_split = (tiles + s.splits - 1) / s.splits;
     if (s.tiles_per_split < 1)
         s.tiles_per_split = 1;
+    s.splits = tiles ? (tiles + s.tiles_per_split - 1) / s.tiles_per_split : 1;
     return s;
 }
 
 using Fn = void (*)(FwdParams);
 
+template <int D, bool F16, bool CAUSAL>
+Fn select(int waves)
+{
+    return waves == 1 ? attention_forward_kernel<D, F16, CAUSAL, 1, 32>
+                      : attention_forward_kernel<D, F16, CAUSAL, 4, 64>;
+}
+
 template <int D>
-Fn select(bool f16, bool causal)
+Fn select(bool f16, bool causal, int waves)
 {
     if (f16)
-        return causal ? attention_forward_kernel<D, true, true, 4, 64>
-                      : attention_forward_kernel<D, true, false, 4, 64>;
-    return causal ? attention_forward_kernel<D, false, true, 4, 64>
-                  : attention_forward_kernel<D, false, false, 4, 64>;
+        return causal ? select<D, true, true>(waves) : select<D, true, false>(waves);
+    return causal ? select<D, false, true>(waves) : select<D, false, false>(waves);
+}
+
+template <int D>
+Fn select_join(bool f16)
+{
+    return f16 ? attention_join_kernel<D, true> : attention_join_kernel<D, false>;
 }
 
 }  // namespace
@@ -342,6 +394,7 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
     p.group = a.heads / a.kv_heads;
     p.rows = (int32_t)(a.q_tokens * p.group);
     p.row_blocks = (int32_t)s.row_blocks;
+    p.pairs = (uint32_t)(a.batch * a.kv_heads);
     p.splits = (int32_t)s.splits;
     p.tiles_per_split = (int32_t)s.tiles_per_split;
     p.c = a.scale * kLog2e;
@@ -349,12 +402,19 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = p.part_o ? p.part_o + s.splits * total * a.head_dim : nullptr;
     const bool f16 = a.dtype == QKR_FP16, causal = a.causal != 0;
-    Fn fn = a.head_dim == 64 ? select<64>(f16, causal)
-            : a.head_dim == 128 ? select<128>(f16, causal) : select<256>(f16, causal);
+    Fn fn = a.head_dim == 64    ? select<64>(f16, causal, s.waves)
+            : a.head_dim == 128 ? select<128>(f16, causal, s.waves)
+                                : select<256>(f16, causal, s.waves);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     void* argv[] = {&p};
     hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(fn),
-                                     dim3((unsigned)(a.batch * a.kv_heads * s.splits * s.row_blocks)),
+                                     dim3((unsigned)(p.pairs * s.splits * s.row_blocks)),
                                      dim3(s.waves * 64), argv, 0, st);
+    if (err == hipSuccess && s.splits > 1) {
+        fn = a.head_dim == 64 ? select_join<64>(f16)
+             : a.head_dim == 128 ? select_join<128>(f16) : select_join<256>(f16);
+        err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)total), dim3(256), argv, 0,
+                              st);
+    }
     return err == hipSuccess ? QKR_OK : QKR_ERR_HIP;
 }
