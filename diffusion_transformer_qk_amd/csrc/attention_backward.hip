@@ -291,7 +291,7 @@ void attention_dkv_kernel(const BwdParams p)
                 dp[j] = F16 ? pr * ((dp[j] - delta[i]) * down) : pr * (dp[j] - delta[i]);
             }
         }
-        if (CAUSAL && k0 + 31 > q0 + shift) {
+        if (CAUSAL && __builtin_expect(k0 + 31 > q0 + shift, 0)) {
             keep_branch();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -457,7 +457,7 @@ void attention_dq_kernel(const BwdParams p)
                 const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c, -lse2));
                 s[i] = F16 ? pr * ((dp[i] - delta) * down) : pr * (dp[i] - delta);
             }
-            if (t * BN + BN > open) {      // hidden keys: their scores are no scores
+            if (__builtin_expect(t * BN + BN > open, 0)) {      // hidden keys: their scores are no scores
                 keep_branch();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
