@@ -155,15 +155,22 @@ __device__ __forceinline__ float largest(const float* v, int n, float* slot)
 
 // ---------------------------------------------------------------- dk and dv
 
+// What bounds it: the matrix rate at the clock that its power leaves (about
+// 1030 TFLOP/s of the four products at head_dim 128, where a large library
+// product reaches 1220), with the LDS reads, one fragment a product, close
+// behind.  Tiles of 64 queries measured 6% faster than tiles of 32, and keeping
+// the phases of a block apart 3% more: left to itself the scheduler mixes two
+// blocks and has to spill.
+//
 // DS waves share a block of 32 keys: each computes its scores and keeps
 // 1 / DS of the columns of its dk and dv (head_dim 256, whose 256 accumulators
 // and 128 registers of k and v would not fit beside the products' operands).
-// The queries are taken 32 at a time.
+// The queries are taken 64 at a time.
 template <int D, bool F16, bool CAUSAL, int NW, int DS>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2)
 void attention_dkv_kernel(const BwdParams p)
 {
-    constexpr int BK = NW / DS * 32, BQ = 32, DB = D / 32 / DS;
+    constexpr int BK = NW / DS * 32, BQ = 64, QB = BQ / 32, DB = D / 32 / DS;
     constexpr int kTile = BQ * D * 2;
     __shared__ __attribute__((aligned(4 * kTile))) char lds[4 * kTile + 2 * BQ * 8];
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
@@ -219,8 +226,8 @@ void attention_dkv_kernel(const BwdParams p)
     for (int i = 0; i < DB; ++i)
         dk[i] = dv[i] = f32x16{};
 
-    // waves 0 and 1 stage the two groups of q's rows, 2 and 3 those of dout's
-    static_assert(NW == 4, "a group of 16 rows a wave");
+    // waves 0 and 1 stage the four groups of q's rows, 2 and 3 those of dout's
+    static_assert(NW == 4, "two groups of 16 rows a wave");
     const bool stages_q = wave < 2;
     const int64_t stage_ts = stages_q ? p.q_ts : p.do_ts;
     const int64_t stage_hs = stages_q ? p.q_hs : p.do_hs;
@@ -235,14 +242,16 @@ void attention_dkv_kernel(const BwdParams p)
     int h = hk * p.group + (per ? t0 / per : 0), next_q = (first + (per ? t0 % per : 0)) * BQ;
     const auto stage = [&](int buf) {
         const int left = p.q_tokens - next_q;
-        rows.load(stage_base + (int64_t)next_q * stage_ts + h * stage_hs, stage_ts, left,
-                  fill + (stages_q ? 0 : kTile), wave & 1);
-        if (wave == 0) {          // lse2 and delta: zero past the last query, as are its rows
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            rows.load(stage_base + (int64_t)next_q * stage_ts + h * stage_hs, stage_ts, left,
+                      fill + (stages_q ? 0 : kTile), (wave & 1) * 2 + i);
+        if (wave < 2) {           // lse2 and delta: zero past the last query, as are its rows
             const uint64_t a = reinterpret_cast<uint64_t>(
                 p.stats + ((b * p.heads + h) * p.q_tokens + next_q) * 2);
             const u32x4 rsrc = {scalar((uint32_t)a), scalar((uint32_t)(a >> 32) & 0xffffu),
                                 scalar((left < BQ ? left : BQ) * 8), kRawBuffer};
-            dma4(rsrc, lane * 4, lds0 + 4 * kTile + buf * BQ * 8);
+            dma4(rsrc, wave * 256 + lane * 4, lds0 + 4 * kTile + buf * BQ * 8 + wave * 256);
         }
         fill ^= 2 * kTile;
         next_q += BQ;
@@ -269,44 +278,49 @@ void attention_dkv_kernel(const BwdParams p)
             stage(buf ^ 1);
         const uint32_t st = lds0 + 4 * kTile + buf * BQ * 8 + 32 * g;
 
-        f32x16 s{}, dp{};
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-            s = mfma<F16>(row_fragment(at, 0, kk), kf[kk], s);
+        for (int y = 0; y < QB; ++y) {
+            __builtin_amdgcn_sched_barrier(0);      // one block after the other
+            f32x16 s{}, dp{};
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-            dp = mfma<F16>(row_fragment(at, kTile, kk), vf[kk], dp);
+            for (int kk = 0; kk < D / 16; ++kk)
+                s = mfma<F16>(row_fragment(at, y * block_bytes<D>(), kk), kf[kk], s);
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-            const f32x4 a = *reinterpret_cast<LdsFloats>(st + 64 * i4);
-            const f32x4 c = *reinterpret_cast<LdsFloats>(st + 64 * i4 + 16);
-            const float lse2[4] = {a[0], a[2], c[0], c[2]};
-            const float delta[4] = {a[1], a[3], c[1], c[3]};
+            for (int kk = 0; kk < D / 16; ++kk)
+                dp = mfma<F16>(row_fragment(at, kTile + y * block_bytes<D>(), kk), vf[kk], dp);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = 4 * i4 + i;
-                const float pr = __builtin_amdgcn_exp2f(
-                    __builtin_fmaf(s[j], p.c, p_shift<F16>() - lse2[i]));
-                s[j] = pr;
-                dp[j] = F16 ? pr * ((dp[j] - delta[i]) * down) : pr * (dp[j] - delta[i]);
+            for (int i4 = 0; i4 < 4; ++i4) {
+                const f32x4 a = *reinterpret_cast<LdsFloats>(st + 256 * y + 64 * i4);
+                const f32x4 c = *reinterpret_cast<LdsFloats>(st + 256 * y + 64 * i4 + 16);
+                const float lse2[4] = {a[0], a[2], c[0], c[2]};
+                const float delta[4] = {a[1], a[3], c[1], c[3]};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 4 * i4 + i;
+                    const float pr = __builtin_amdgcn_exp2f(
+                        __builtin_fmaf(s[j], p.c, p_shift<F16>() - lse2[i]));
+                    s[j] = pr;
+                    dp[j] = F16 ? pr * ((dp[j] - delta[i]) * down) : pr * (dp[j] - delta[i]);
+                }
             }
-        }
-        if (CAUSAL && __builtin_expect(k0 + 31 > q0 + shift, 0)) {
-            keep_branch();
+            if (CAUSAL && __builtin_expect(k0 + 31 > q0 + 32 * y + shift, 0)) {
+                keep_branch();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (key > q0 + 8 * (i / 4) + 4 * g + i % 4 + shift)
-                    s[i] = dp[i] = 0.0f;
-        }
+                for (int i = 0; i < 16; ++i)
+                    if (key > q0 + 32 * y + 8 * (i / 4) + 4 * g + i % 4 + shift)
+                        s[i] = dp[i] = 0.0f;
+            }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const u32x4 pf = pack_b<F16>(s, k), sf = pack_b<F16>(dp, k);
+            for (int k = 0; k < 2; ++k) {
+                const u32x4 pf = pack_b<F16>(s, k), sf = pack_b<F16>(dp, k);
 #pragma unroll
-            for (int i = 0; i < DB; ++i)
-                dv[i] = mfma<F16>(tr_fragment(at, kTile + db0 * kSlab, k, i), pf, dv[i]);
+                for (int i = 0; i < DB; ++i)
+                    dv[i] = mfma<F16>(tr_fragment(at, kTile + y * block_bytes<D>() + db0 * kSlab, k, i), pf, dv[i]);
 #pragma unroll
-            for (int i = 0; i < DB; ++i)
-                dk[i] = mfma<F16>(tr_fragment(at, db0 * kSlab, k, i), sf, dk[i]);
+                for (int i = 0; i < DB; ++i)
+                    dk[i] = mfma<F16>(tr_fragment(at, y * block_bytes<D>() + db0 * kSlab, k, i), sf, dk[i]);
+            }
         }
         q0 = following;
         at.flip(2 * kTile);
@@ -564,8 +578,10 @@ Shape shape_of(const dit_attn_args& a)
     const int64_t bk = 32 * kWaves / waves_per_key_block(a.head_dim), bm = 32 * kWaves;
     s.row_blocks = (rows + bm - 1) / bm;
     s.key_blocks = (a.kv_tokens + bk - 1) / bk;
-    const int64_t resident = a.head_dim == 256 ? 256 : 512;
-    cut(pairs * s.key_blocks, resident, (a.q_tokens + 31) / 32 * group, 16, s.row_splits,
+    // workgroups resident at once (head_dim 64 would hold 3 a CU, but its sums of
+    // more parts cost what that gains: 33 us with 2 as with 3 on 12 x 8 blocks)
+    const int64_t resident = 256 * (a.head_dim == 256 ? 1 : 2);
+    cut(pairs * s.key_blocks, resident, (a.q_tokens + 63) / 64 * group, 8, s.row_splits,
         s.row_tiles_per_split);
     cut(pairs * s.row_blocks, resident, (a.kv_tokens + 63) / 64, 8, s.key_splits,
         s.key_tiles_per_split);

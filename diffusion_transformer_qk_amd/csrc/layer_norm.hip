@@ -59,13 +59,32 @@ __device__ __forceinline__ void load_params(const void* at, int64_t i, int32_t d
 }
 
 // Make the compiler forget what v holds, so that the fp32 values unpacked from
-// it are unpacked again for each pass instead of being kept across them.
+// it are unpacked again for each pass instead of being kept across them: for
+// the longest rows, whose registers would not allow two workgroups a CU (kept,
+// the values save a tenth of the backward pass's instructions).
 template <int VPT>
 __device__ __forceinline__ void forget_unpacked(const u32x4 (&v)[VPT])
 {
+    if constexpr (VPT == 4) {
 #pragma unroll
-    for (int u = 0; u < VPT; ++u)
-        __asm__ volatile("" : "+v"(const_cast<u32x4&>(v[u])));
+        for (int u = 0; u < VPT; ++u)
+            __asm__ volatile("" : "+v"(const_cast<u32x4&>(v[u])));
+    }
+}
+
+// Sum over the wave by lane moves alone; every lane ends with the same bits.
+__device__ __forceinline__ float wave_total(float v)
+{
+    v += dpp<0xB1>(v);      // quad_perm [1,0,3,2]
+    v += dpp<0x4E>(v);      // quad_perm [2,3,0,1]
+    v += dpp<0x141>(v);     // row_half_mirror
+    v += dpp<0x140>(v);     // row_mirror: each 16-lane row's total in all its lanes
+    const uint32_t a = __float_as_uint(v);
+    const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    v = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    const uint32_t b = __float_as_uint(v);
+    const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
 
 // Sums over the row's threads, the same bits in each.  `slot`: 4 floats of LDS
@@ -75,7 +94,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* slot)
 {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        v[i] = wave_sum(v[i]);
+        v[i] = wave_total(v[i]);
     if constexpr (TPR > kWave) {
         if (threadIdx.x % kWave == 0) {
 #pragma unroll
@@ -385,18 +404,25 @@ void layer_norm_parts_kernel(const LnParams p)
     }
 }
 
-using Fn = void (*)(LnParams);
-
 // One wave a row up to this width, the whole workgroup above it.
 constexpr int kWaveHidden = 1024;
+
+// Vectors a thread holds of a row (the kernels' VPT).
+int vectors_of(int hidden)
+{
+    const int nvec = hidden / kVec, threads = hidden <= kWaveHidden ? kWave : kThreads;
+    return (nvec + threads - 1) / threads;
+}
+
+using Fn = void (*)(LnParams);
 
 template <bool F16, bool GRAD>
 Fn select(int hidden)
 {
-    const int nvec = hidden / kVec;
+    const int v = vectors_of(hidden);
     if (hidden <= kWaveHidden)
-        return nvec <= 64 ? layer_norm_kernel<64, 1, F16, GRAD> : layer_norm_kernel<64, 2, F16, GRAD>;
-    switch ((nvec + kThreads - 1) / kThreads) {
+        return v == 1 ? layer_norm_kernel<64, 1, F16, GRAD> : layer_norm_kernel<64, 2, F16, GRAD>;
+    switch (v) {
     case 1: return layer_norm_kernel<256, 1, F16, GRAD>;
     case 2: return layer_norm_kernel<256, 2, F16, GRAD>;
     case 3: return layer_norm_kernel<256, 3, F16, GRAD>;
@@ -404,19 +430,31 @@ Fn select(int hidden)
     }
 }
 
-// Workgroups that a call spreads its rows over.
-constexpr int64_t kTargetBlocks = 768;
+// Workgroups that a call spreads its rows over: whole multiples of what is
+// resident at once.  Measured on 300 MB of rows, in workgroups a CU (GB/s):
+//   forward   512 columns (1 vector): 2: 3530, 3: 4240, 4: 4710
+//            4096 (2 vectors):        2: 4680, 3: 4650, 4: 5000
+//            5120 (3 vectors):        2: 4680, 3: 5000, 4: 4140
+//            8192 (4 vectors):        2: 5060, 3: 4250, 4: 5160
+//   backward 2048 columns (1 vector): 2: 3370, 3: 4120, 4: 4470
+//            4096 (2 vectors):        2: 4730, 3: 4440, 4: 4020
+//            5120 (3 vectors):        2: 4660, 3: 3900, 4: 4400
+int64_t target_blocks(int hidden, bool grad)
+{
+    const int v = vectors_of(hidden);
+    return 256 * (grad ? (v == 1 ? 4 : 2) : (v == 3 ? 3 : 4));
+}
 
 // Workgroups a batch: its rows spread so that the whole call has about
-// kTargetBlocks of them, none without a row.
-int64_t chunks_of(int64_t rows, int hidden, int64_t rows_per_batch)
+// target_blocks() of them, none without a row.
+int64_t chunks_of(int64_t rows, int hidden, int64_t rows_per_batch, bool grad)
 {
     const int64_t per = rows_per_batch < rows ? rows_per_batch : rows;
     const int64_t batches = (rows + per - 1) / per;
     const int64_t at_once = hidden <= kWaveHidden ? 4 : 1;
     const int64_t most = (per + at_once - 1) / at_once;
-    const int64_t want = (kTargetBlocks + batches - 1) / batches;
-    const int64_t chunks = want < most ? want : most;
+    int64_t chunks = target_blocks(hidden, grad) / batches;
+    chunks = chunks < 1 ? 1 : chunks < most ? chunks : most;
     const int64_t each = ((per + chunks - 1) / chunks + at_once - 1) / at_once * at_once;
     return (per + each - 1) / each;
 }
@@ -439,12 +477,12 @@ int check_types(int32_t dtype, int32_t param_dtype, float eps)
     return eps > 0.0f && isfinite(eps) ? QKR_OK : QKR_ERR_ARG;
 }
 
-void fill(LnParams& p, int64_t rows, int hidden, int64_t rows_per_batch)
+void fill(LnParams& p, int64_t rows, int hidden, int64_t rows_per_batch, bool grad)
 {
     p.rows = rows;
     p.hidden = hidden;
     p.rows_per_batch = (uint32_t)(rows_per_batch < rows ? rows_per_batch : rows);
-    p.chunks = (uint32_t)chunks_of(rows, hidden, rows_per_batch);
+    p.chunks = (uint32_t)chunks_of(rows, hidden, rows_per_batch, grad);
     const uint32_t at_once = hidden <= kWaveHidden ? 4 : 1;
     p.rows_per_chunk = ((p.rows_per_batch + p.chunks - 1) / p.chunks + at_once - 1) / at_once * at_once;
 }
@@ -484,7 +522,7 @@ extern "C" int dit_layer_norm(const void* x, void* y, int64_t rows, int32_t hidd
     p.bias = bias;
     p.param_dtype = param_dtype;
     p.eps = eps;
-    fill(p, rows, hidden, rows);
+    fill(p, rows, hidden, rows, false);
     Fn fn = dtype == QKR_FP16 ? select<true, false>(hidden) : select<false, false>(hidden);
     return launch(fn, p.chunks, 0, p, stream) == hipSuccess ? QKR_OK : QKR_ERR_HIP;
 }
@@ -495,7 +533,7 @@ extern "C" int64_t dit_layer_norm_backward_workspace_size(int64_t rows, int32_t 
     const int rc = check_sizes(rows, hidden, rows_per_batch);
     if (rc != QKR_OK || rows == 0)
         return rc;
-    const int64_t chunks = chunks_of(rows, hidden, rows_per_batch);
+    const int64_t chunks = chunks_of(rows, hidden, rows_per_batch, true);
     const int64_t batches = (rows + rows_per_batch - 1) / rows_per_batch;
     return chunks == 1 ? 0 : batches * chunks * 2 * hidden * 4;
 }
@@ -550,7 +588,7 @@ extern "C" int dit_layer_norm_backward(const void* dy, const void* x, void* dx, 
     p.dbias = dbias;
     p.parts = static_cast<float*>(workspace);
     p.eps = eps;
-    fill(p, rows, hidden, rows_per_batch);
+    fill(p, rows, hidden, rows_per_batch, true);
     const int64_t batches = (rows + p.rows_per_batch - 1) / p.rows_per_batch;
     Fn fn = dtype == QKR_FP16 ? select<true, true>(hidden) : select<false, true>(hidden);
     const size_t lds = dweight && hidden <= kWaveHidden ? (size_t)3 * 2 * hidden * 4 : 0;
