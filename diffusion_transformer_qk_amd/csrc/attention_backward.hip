@@ -1,6 +1,6 @@
 // attention_backward.hip -- attention backward for gfx950 (see dit_attention.h).
 //
-// Three kernels on one stream:
+// Two launches, the second in two parts:
 //   rows: lse (in base 2) and delta = dout . out of every query, and for fp16
 //         the norms that bound dout . v;
 //   dkv:  a wave owns 32 keys, keeps their k, v, dk and dv in registers and
@@ -155,6 +155,11 @@ __device__ __forceinline__ float largest(const float* v, int n, float* slot)
 
 // ---------------------------------------------------------------- dk and dv
 
+constexpr int kWaves = 4;
+constexpr int kTileRows = 64;      // queries (dk and dv) or keys (dq) staged at a time
+
+constexpr int waves_per_key_block(int d) { return d == 256 ? 2 : 1; }
+
 // What bounds it: the matrix rate at the clock that its power leaves (about
 // 1030 TFLOP/s of the four products at head_dim 128, where a large library
 // product reaches 1220), with the LDS reads, one fragment a product, close
@@ -166,17 +171,17 @@ __device__ __forceinline__ float largest(const float* v, int n, float* slot)
 // 1 / DS of the columns of its dk and dv (head_dim 256, whose 256 accumulators
 // and 128 registers of k and v would not fit beside the products' operands).
 // The queries are taken 64 at a time.
-template <int D, bool F16, bool CAUSAL, int NW, int DS>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2)
-void attention_dkv_kernel(const BwdParams p)
+template <int D, bool F16, bool CAUSAL>
+__device__ __forceinline__ void key_gradients(const BwdParams& p, const char* lds, float* tops,
+                                              uint32_t bid)
 {
-    constexpr int BK = NW / DS * 32, BQ = 64, QB = BQ / 32, DB = D / 32 / DS;
+    constexpr int NW = kWaves, DS = waves_per_key_block(D);
+    constexpr int BK = NW / DS * 32, BQ = kTileRows, QB = BQ / 32, DB = D / 32 / DS;
     constexpr int kTile = BQ * D * 2;
-    __shared__ __attribute__((aligned(4 * kTile))) char lds[4 * kTile + 2 * BQ * 8];
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const BlockOf block(blockIdx.x, p.pairs, p.key_blocks * p.row_splits);
+    const BlockOf block(bid, p.pairs, p.key_blocks * p.row_splits);
     const int kb = block.part % p.key_blocks, split = block.part / p.key_blocks;
     const int64_t bh = block.pair;
     const int64_t b = bh / p.kv_heads;
@@ -215,7 +220,6 @@ void attention_dkv_kernel(const BwdParams p)
     float down = 1.0f;            // brings dp - delta below 1
     int e = 0;
     if constexpr (F16) {
-        __shared__ float tops[8];
         const int n = p.group * p.stat_blocks;
         e = bound_exponent(largest(p.row_norms + bh * n, n, tops) *
                            largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops + 4)) + 1;
@@ -355,17 +359,17 @@ void attention_dkv_kernel(const BwdParams p)
 
 // ---------------------------------------------------------------- dq
 
-template <int D, bool F16, bool CAUSAL, int NW, int BN>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2)
-void attention_dq_kernel(const BwdParams p)
+template <int D, bool F16, bool CAUSAL>
+__device__ __forceinline__ void query_gradients(const BwdParams& p, const char* lds, float* tops,
+                                                uint32_t bid)
 {
+    constexpr int NW = kWaves, BN = kTileRows;
     constexpr int BM = NW * 32, KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
-    __shared__ __attribute__((aligned(4 * kTile))) char lds[4 * kTile];
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const BlockOf block(blockIdx.x, p.pairs, p.row_blocks * p.key_splits);
+    const BlockOf block(bid, p.pairs, p.row_blocks * p.key_splits);
     const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
     const int64_t bh = block.pair;
     const int64_t b = bh / p.kv_heads;
@@ -406,8 +410,7 @@ void attention_dq_kernel(const BwdParams p)
         }
     }
     const f32x2 st = reinterpret_cast<const f32x2*>(p.stats)[(b * p.heads + head) * p.q_tokens + qi];
-    const float lse2 = st.x - p_shift<F16>(), delta = st.y;
-    float down = 1.0f;
+    const float delta = st.y;
     int e = 0;
     if constexpr (F16) {
         float sq = 0.0f;
@@ -419,11 +422,11 @@ void attention_dq_kernel(const BwdParams p)
             for (int i = 0; i < 8; ++i)
                 sq = __builtin_fmaf(x[i], x[i], sq);
         }
-        __shared__ float tops[4];
         e = bound_exponent(sqrtf(half_sum(sq)) *
                            largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops)) + 1;
-        down = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
+    // ds alone is needed here, so its power of two goes into the exponent of p
+    const float lse2 = st.x - p_shift<F16>() + (float)e;
     f32x16 dq[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i)
@@ -469,7 +472,7 @@ void attention_dq_kernel(const BwdParams p)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.c, -lse2));
-                s[i] = F16 ? pr * ((dp[i] - delta) * down) : pr * (dp[i] - delta);
+                s[i] = pr * (dp[i] - delta);
             }
             if (__builtin_expect(t * BN + BN > open, 0)) {      // hidden keys: their scores are no scores
                 keep_branch();
@@ -502,6 +505,24 @@ void attention_dq_kernel(const BwdParams p)
         for (int i = 0; i < DB; ++i)
             store_column_f32(row + 32 * i, dq[i], f, g, valid);
     }
+}
+
+// Both in one launch, dk and dv first (their workgroups take longer): they do
+// not wait for each other, so the last workgroups of the one leave no CU idle
+// that the other could use.
+template <int D, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2)
+void attention_backward_kernel(const BwdParams p)
+{
+    // two buffers of two tiles, then two of the tiles' lse2 and delta
+    constexpr int kTiles = 4 * kTileRows * D * 2;
+    __shared__ __attribute__((aligned(kTiles))) char lds[kTiles + 2 * kTileRows * 8];
+    __shared__ float tops[8];
+    const uint32_t first = p.pairs * (uint32_t)(p.key_blocks * p.row_splits);
+    if (blockIdx.x < first)
+        key_gradients<D, F16, CAUSAL>(p, lds, tops, blockIdx.x);
+    else
+        query_gradients<D, F16, CAUSAL>(p, lds, tops, blockIdx.x - first);
 }
 
 // Adds the splits' dk and dv, or dq, in order: D / 8 threads a row.
@@ -541,10 +562,6 @@ void attention_sum_kernel(const BwdParams p)
 }
 
 // ---------------------------------------------------------------- launches
-
-constexpr int kWaves = 4;
-
-constexpr int waves_per_key_block(int d) { return d == 256 ? 2 : 1; }
 
 // How a call is cut up, and where its workspace's parts begin (in floats).
 struct Shape {
@@ -600,7 +617,7 @@ Shape shape_of(const dit_attn_args& a)
 template <int D, bool F16, bool CAUSAL>
 hipError_t launch(BwdParams p, hipStream_t st)
 {
-    constexpr int DS = waves_per_key_block(D), R = 256 / (D / 8);
+    constexpr int R = 256 / (D / 8);
     const int64_t pairs = p.pairs;
     void* argv[] = {&p};
     hipError_t err = hipSuccess;
@@ -610,8 +627,8 @@ hipError_t launch(BwdParams p, hipStream_t st)
                                   argv, 0, st);
     };
     go(row_stats_kernel<D, F16>, p.batch * p.heads * p.stat_blocks + (F16 ? pairs * p.value_blocks : 0));
-    go(attention_dkv_kernel<D, F16, CAUSAL, kWaves, DS>, pairs * p.key_blocks * p.row_splits);
-    go(attention_dq_kernel<D, F16, CAUSAL, kWaves, 64>, pairs * p.row_blocks * p.key_splits);
+    go(attention_backward_kernel<D, F16, CAUSAL>,
+       pairs * ((int64_t)p.key_blocks * p.row_splits + (int64_t)p.row_blocks * p.key_splits));
     if (p.row_splits > 1)
         go(attention_sum_kernel<D, F16, true>, (pairs * 2 * p.kv_tokens + R - 1) / R);
     if (p.key_splits > 1)

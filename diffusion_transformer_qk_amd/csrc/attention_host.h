@@ -38,13 +38,10 @@ inline int check_args(const dit_attn_args* a)
         a->kv_tokens >= QKR_MAX_TOKENS || a->batch >= QKR_MAX_TOKENS || a->kv_heads < 1 ||
         a->heads < a->kv_heads || a->heads > QKR_MAX_HEADS || a->heads % a->kv_heads)
         return QKR_ERR_SHAPE;
-    // rows are dealt to workgroups in blocks of 32 or more
-    const int64_t group = a->heads / a->kv_heads;
-    if (a->q_tokens * group >= kMaxRows)
-        return QKR_ERR_SHAPE;
-    const int64_t pairs = a->batch * a->kv_heads;
-    const int64_t long_side = a->q_tokens * group > a->kv_tokens ? a->q_tokens * group : a->kv_tokens;
-    if (pairs >= kMaxBlocks || pairs * (long_side / 32 + 1) >= kMaxBlocks)
+    // tokens are dealt to workgroups in blocks of 32 or more
+    if (a->q_tokens * (a->heads / a->kv_heads) >= kMaxRows ||
+        a->batch * a->heads * (a->q_tokens / 32 + 1) >= kMaxBlocks ||
+        a->batch * a->kv_heads * (a->kv_tokens / 32 + 1) >= kMaxBlocks)
         return QKR_ERR_SHAPE;
     return QKR_OK;
 }

@@ -62,7 +62,9 @@ typedef struct {
 
 #define DIT_ATTN_MAX_TOKEN_STRIDE ((int64_t)1 << 22)
 
-/* What a call computes. */
+/* What a call computes.  heads * (q_tokens / 32 + 1) and kv_heads *
+ * (kv_tokens / 32 + 1), times batch, must stay below 2^23, and q_tokens * heads
+ * / kv_heads below 2^30. */
 typedef struct {
     int64_t batch;              /* 0 is a no-op                                       */
     int64_t q_tokens;           /* 0 .. QKR_MAX_TOKENS - 1                            */
