@@ -24,8 +24,6 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "attention_common.h"
 #include "attention_host.h"
 #include "dit_attention.h"
@@ -183,9 +181,9 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
 
     const BlockOf block(bid, p.pairs, p.key_blocks * p.row_splits);
     const int kb = block.part % p.key_blocks, split = block.part / p.key_blocks;
-    const int64_t bh = block.pair;
-    const int64_t b = bh / p.kv_heads;
-    const int hk = bh % p.kv_heads;
+    const uint32_t bh = block.pair;
+    const int64_t b = bh / (uint32_t)p.kv_heads;
+    const int hk = bh % (uint32_t)p.kv_heads;
     int len = p.kv_tokens;
     if (p.kv_lengths) {
         const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
@@ -207,24 +205,6 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     const int t0 = split * p.row_tiles_per_split;
     const int total = (all < t0 + p.row_tiles_per_split ? all : t0 + p.row_tiles_per_split) - t0;
 
-    u32x4 kf[D / 16], vf[D / 16];
-    {
-        const uint16_t* kr = p.k + b * p.k_bs + (int64_t)key * p.k_ts + hk * p.k_hs + 8 * g;
-        const uint16_t* vr = p.v + b * p.v_bs + (int64_t)key * p.v_ts + hk * p.v_hs + 8 * g;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            kf[kk] = key < len ? load16<false>(kr + 16 * kk) : u32x4{0, 0, 0, 0};
-            vf[kk] = key < len ? load16<false>(vr + 16 * kk) : u32x4{0, 0, 0, 0};
-        }
-    }
-    float down = 1.0f;            // brings dp - delta below 1
-    int e = 0;
-    if constexpr (F16) {
-        const int n = p.group * p.stat_blocks;
-        e = bound_exponent(largest(p.row_norms + bh * n, n, tops) *
-                           largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops + 4)) + 1;
-        down = __builtin_amdgcn_ldexpf(1.0f, -e);
-    }
     f32x16 dk[DB], dv[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i)
@@ -265,14 +245,32 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
         }
     };
 
+    int q0 = next_q;
+    if (total > 0)
+        stage(0);                 // before k and v: the waits run together
+    u32x4 kf[D / 16], vf[D / 16];
+    {
+        const uint16_t* kr = p.k + b * p.k_bs + (int64_t)key * p.k_ts + hk * p.k_hs + 8 * g;
+        const uint16_t* vr = p.v + b * p.v_bs + (int64_t)key * p.v_ts + hk * p.v_hs + 8 * g;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            kf[kk] = key < len ? load16<false>(kr + 16 * kk) : u32x4{0, 0, 0, 0};
+            vf[kk] = key < len ? load16<false>(vr + 16 * kk) : u32x4{0, 0, 0, 0};
+        }
+    }
+    float down = 1.0f;            // brings dp - delta below 1
+    int e = 0;
+    if constexpr (F16) {
+        const int n = p.group * p.stat_blocks;
+        e = bound_exponent(largest(p.row_norms + bh * n, n, tops) *
+                           largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops + 4)) + 1;
+        down = __builtin_amdgcn_ldexpf(1.0f, -e);
+    }
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         settle(kf[kk]);
         settle(vf[kk]);
     }
-    int q0 = next_q;
-    if (total > 0)
-        stage(0);
     for (int t = 0; t < total; ++t) {
         const int buf = t & 1;
         wait_staged();
@@ -371,9 +369,9 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
 
     const BlockOf block(bid, p.pairs, p.row_blocks * p.key_splits);
     const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
-    const int64_t bh = block.pair;
-    const int64_t b = bh / p.kv_heads;
-    const int hk = bh % p.kv_heads;
+    const uint32_t bh = block.pair;
+    const int64_t b = bh / (uint32_t)p.kv_heads;
+    const int hk = bh % (uint32_t)p.kv_heads;
     const int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;
     int len = p.kv_tokens;
     if (p.kv_lengths) {
@@ -399,6 +397,27 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
         open = s < open ? s : open;
     }
 
+    f32x16 dq[DB];
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+        dq[i] = f32x16{};
+
+    const Stager<D> ks(lane, p.k_ts), vs(lane, p.v_ts);
+    const uint16_t* kbase = p.k + b * p.k_bs + hk * p.k_hs;
+    const uint16_t* vbase = p.v + b * p.v_bs + hk * p.v_hs;
+    uint32_t fill = lds_address(lds);
+    TileAt at(fill, lane);
+    const auto stage = [&](int t) {
+        const int64_t first = (int64_t)t * BN;
+#pragma unroll
+        for (int i = 0; i < BN / 16 / NW; ++i) {
+            ks.load(kbase + first * p.k_ts, p.k_ts, len - (int)first, fill, wave + i * NW);
+            vs.load(vbase + first * p.v_ts, p.v_ts, len - (int)first, fill + kTile, wave + i * NW);
+        }
+        fill ^= 2 * kTile;
+    };
+    if (t0 < tiles)
+        stage(t0);                // before q and dout: the waits run together
     u32x4 qf[D / 16], df[D / 16];
     {
         const uint16_t* qr = p.q + b * p.q_bs + qi * p.q_ts + head * p.q_hs + 8 * g;
@@ -427,33 +446,11 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
     }
     // ds alone is needed here, so its power of two goes into the exponent of p
     const float lse2 = st.x - p_shift<F16>() + (float)e;
-    f32x16 dq[DB];
-#pragma unroll
-    for (int i = 0; i < DB; ++i)
-        dq[i] = f32x16{};
-
-    const Stager<D> ks(lane, p.k_ts), vs(lane, p.v_ts);
-    const uint16_t* kbase = p.k + b * p.k_bs + hk * p.k_hs;
-    const uint16_t* vbase = p.v + b * p.v_bs + hk * p.v_hs;
-    uint32_t fill = lds_address(lds);
-    TileAt at(fill, lane);
-    const auto stage = [&](int t) {
-        const int64_t first = (int64_t)t * BN;
-#pragma unroll
-        for (int i = 0; i < BN / 16 / NW; ++i) {
-            ks.load(kbase + first * p.k_ts, p.k_ts, len - (int)first, fill, wave + i * NW);
-            vs.load(vbase + first * p.v_ts, p.v_ts, len - (int)first, fill + kTile, wave + i * NW);
-        }
-        fill ^= 2 * kTile;
-    };
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         settle(qf[kk]);
         settle(df[kk]);
     }
-
-    if (t0 < tiles)
-        stage(t0);
     for (int t = t0; t < tiles; ++t) {
         wait_staged();
         __syncthreads();
@@ -687,8 +684,7 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     if (meet(ws_r, lse_r) || meet(ws_r, len_r))
         return QKR_ERR_ARG;
     for (int i = 0; i < 8; ++i) {
-        const bool there = all[i].e.tokens != 0;
-        const Range x = there ? range(a, all[i].t, all[i].e) : Range{nullptr, 0};
+        const Range x = range(a, all[i].t, all[i].e);
         if (meet(x, ws_r))
             return QKR_ERR_ARG;
         if (i < 5)
@@ -701,21 +697,14 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     }
 
     BwdParams p = {};
-    const auto set = [](const dit_attn_tensor* t, auto*& at, int64_t& bs, int64_t& ts, int64_t& hs) {
-        using P = typename std::remove_reference<decltype(at)>::type;
-        if (t) {
-            at = static_cast<P>(t->data);
-            bs = t->batch_stride, ts = t->token_stride, hs = t->head_stride;
-        }
-    };
-    set(dout, p.dout, p.do_bs, p.do_ts, p.do_hs);
-    set(q, p.q, p.q_bs, p.q_ts, p.q_hs);
-    set(k, p.k, p.k_bs, p.k_ts, p.k_hs);
-    set(v, p.v, p.v_bs, p.v_ts, p.v_hs);
-    set(out, p.out, p.o_bs, p.o_ts, p.o_hs);
-    set(dq, p.dq, p.dq_bs, p.dq_ts, p.dq_hs);
-    set(dk, p.dk, p.dk_bs, p.dk_ts, p.dk_hs);
-    set(dv, p.dv, p.dv_bs, p.dv_ts, p.dv_hs);
+    unpack(dout, p.dout, p.do_bs, p.do_ts, p.do_hs);
+    unpack(q, p.q, p.q_bs, p.q_ts, p.q_hs);
+    unpack(k, p.k, p.k_bs, p.k_ts, p.k_hs);
+    unpack(v, p.v, p.v_bs, p.v_ts, p.v_hs);
+    unpack(out, p.out, p.o_bs, p.o_ts, p.o_hs);
+    unpack(dq, p.dq, p.dq_bs, p.dq_ts, p.dq_hs);
+    unpack(dk, p.dk, p.dk_bs, p.dk_ts, p.dk_hs);
+    unpack(dv, p.dv, p.dv_bs, p.dv_ts, p.dv_hs);
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
     p.batch = a.batch;

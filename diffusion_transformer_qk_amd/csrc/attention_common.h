@@ -48,7 +48,7 @@ constexpr uint32_t kRawBuffer = 0x00020000u;   // raw buffer resource, 32-bit da
 // pairs, which are of one sample and so of one length, go to different dies.)
 // The last pairs % 8 are cut into eighths, one a die.
 struct BlockOf {
-    int64_t pair;
+    uint32_t pair;
     int32_t part;
 
     __device__ __forceinline__ BlockOf(uint32_t bid, uint32_t pairs, uint32_t parts)

@@ -72,9 +72,9 @@ void attention_forward_kernel(const FwdParams p)
 
     const BlockOf block(blockIdx.x, p.pairs, p.row_blocks * p.splits);
     const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
-    const int64_t bh = block.pair;                       // sample, key head
-    const int64_t b = bh / p.kv_heads;
-    const int hk = bh % p.kv_heads;
+    const uint32_t bh = block.pair;                      // sample, key head
+    const int64_t b = bh / (uint32_t)p.kv_heads;
+    const int hk = bh % (uint32_t)p.kv_heads;
     const int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;   // the longest first
 
     int len = p.kv_tokens;
@@ -393,17 +393,13 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
         return QKR_ERR_ARG;
 
     const Shape s = shape_of(a);
-    FwdParams p;
-    p.q = static_cast<const uint16_t*>(q->data);
-    p.k = static_cast<const uint16_t*>(k->data);
-    p.v = static_cast<const uint16_t*>(v->data);
-    p.out = static_cast<uint16_t*>(out->data);
+    FwdParams p = {};
+    unpack(q, p.q, p.q_bs, p.q_ts, p.q_hs);
+    unpack(k, p.k, p.k_bs, p.k_ts, p.k_hs);
+    unpack(v, p.v, p.v_bs, p.v_ts, p.v_hs);
+    unpack(out, p.out, p.o_bs, p.o_ts, p.o_hs);
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
-    p.q_bs = q->batch_stride, p.q_ts = q->token_stride, p.q_hs = q->head_stride;
-    p.k_bs = k->batch_stride, p.k_ts = k->token_stride, p.k_hs = k->head_stride;
-    p.v_bs = v->batch_stride, p.v_ts = v->token_stride, p.v_hs = v->head_stride;
-    p.o_bs = out->batch_stride, p.o_ts = out->token_stride, p.o_hs = out->head_stride;
     p.q_tokens = (int32_t)a.q_tokens;
     p.kv_tokens = (int32_t)a.kv_tokens;
     p.kv_heads = a.kv_heads;

@@ -30,7 +30,7 @@ inline int check_args(const dit_attn_args* a)
     if (!a)
         return QKR_ERR_NULL;
     if (a->dtype < QKR_BF16 || a->dtype > QKR_FP32 || (a->causal != 0 && a->causal != 1) ||
-        !isfinite(a->scale) || !(a->scale > 0.0f))
+        !isfinite(a->scale * 1.5f) || !(a->scale > 0.0f))      // it is used times log2(e)
         return QKR_ERR_ARG;
     if (a->dtype == QKR_FP32 || (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256))
         return QKR_ERR_UNSUPPORTED;
@@ -57,7 +57,7 @@ inline uint64_t span(const dit_attn_args& a, const dit_attn_tensor* t, const Ext
 
 inline Range range(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e)
 {
-    return Range{t->data, span(a, t, e) * 2};
+    return e.tokens ? Range{t->data, span(a, t, e) * 2} : Range{nullptr, 0};
 }
 
 inline bool meet(const Range& x, const Range& y) { return qkr_host::overlaps(x.at, x.bytes, y.at, y.bytes); }
@@ -123,6 +123,19 @@ inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor* x, const Ext
     if (ahead < 0)
         ahead += ts;
     return !(wx <= ahead && ahead + wy <= ts);
+}
+
+// A tensor's pointer and strides as a kernel takes them; one without tokens may
+// be NULL.
+template <typename T>
+inline void unpack(const dit_attn_tensor* t, T*& at, int64_t& bs, int64_t& ts, int64_t& hs)
+{
+    if (!t)
+        return;
+    at = static_cast<T*>(t->data);
+    bs = t->batch_stride;
+    ts = t->token_stride;
+    hs = t->head_stride;
 }
 
 }  // namespace qkr_attn_host

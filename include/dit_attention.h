@@ -54,7 +54,8 @@ extern "C" {
  * buffer are such tensors.  data must be 16-byte aligned, the strides
  * multiples of 8 and not negative, token_stride at least head_dim (where
  * tokens > 1) and at most DIT_ATTN_MAX_TOKEN_STRIDE.  Elements of an output
- * must not share memory; a batch or head stride of an input may be 0. */
+ * must not share memory; a batch or head stride of an input may be 0.  A tensor
+ * of 0 tokens is not looked at and may be NULL. */
 typedef struct {
     void* data;
     int64_t batch_stride, token_stride, head_stride;
@@ -74,7 +75,7 @@ typedef struct {
     int32_t head_dim;           /* 64, 128 or 256                                     */
     int32_t causal;             /* 0 or 1                                             */
     int32_t dtype;              /* QKR_BF16 or QKR_FP16, of every tensor but lse      */
-    float scale;                /* finite and > 0                                     */
+    float scale;                /* > 0, finite also times log2(e)                     */
     const int32_t* kv_lengths;  /* device array [batch], or NULL; a length below 0    */
                                 /* counts as 0, one above kv_tokens as kv_tokens      */
 } dit_attn_args;

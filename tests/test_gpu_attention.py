@@ -218,6 +218,41 @@ def test_no_queries_or_no_keys():
     assert (dq == 0).all()
 
 
+def test_missing_tensors_without_tokens():
+    """From C a tensor of no tokens may be NULL."""
+    from diffusion_transformer_qk_amd import binding as b
+
+    lib = b.load_library()
+    q, _, _, dout = tensors(22, "fp16", 2, 5, 7, 2, 2, 64)
+    args = b.AttnArgs(2, 5, 0, 2, 2, 64, 0, b.QKR_FP16, 0.125, None)
+    t = lambda x: b._attn_tensor(x, "x")  # noqa: E731
+    out, lse, dq = torch.ones_like(q), torch.ones((2, 2, 5), device=DEV), torch.ones_like(q)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=DEV)
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.dit_attention(args, t(q), None, None, t(out), lse.data_ptr(), 0, 0, st) == 0
+    assert lib.dit_attention_backward(args, t(dout), t(q), None, None, t(out), lse.data_ptr(), t(dq), None, None,
+                                      ws.data_ptr(), ws.numel(), st) == 0
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (lse == -math.inf).all() and (dq == 0).all()
+
+
+@pytest.mark.parametrize("dtype,sq,sk,h,hk,causal", [
+    ("bf16", 1, 4000, 8, 2, False), ("fp16", 60, 3000, 2, 1, False), ("fp16", 1500, 130, 4, 4, True),
+    ("bf16", 900, 900, 3, 3, True)])
+def test_workspaces_of_any_contents(dtype, sq, sk, h, hk, causal):
+    """NaN patterns in the workspace, and one larger than needed, change nothing
+    (calls that cut the keys, the queries, both, and neither)."""
+    q, k, v, dout = tensors(34, dtype, 1, sq, sk, h, hk, 128)
+    out, lse = qkr.attention(q, k, v, causal=causal)
+    want = qkr.attention_backward(dout, q, k, v, out, lse, causal=causal)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    out2, lse2 = qkr.attention(q, k, v, causal=causal, workspace=ws)
+    ws.fill_(255)
+    got = qkr.attention_backward(dout, q, k, v, out, lse, causal=causal, workspace=ws)
+    assert same_bits(out, out2) and same_bits(lse, lse2)
+    assert all(same_bits(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("causal", [False, True])
 def test_results_do_not_change_from_run_to_run(causal):
     q, k, v, dout = tensors(23, "fp16", 2, 700, 700, 4, 2, 128)
@@ -246,8 +281,7 @@ def test_few_keys_under_many_queries():
     check(*tensors(26, "bf16", 1, 3000, 20, 2, 2, 128))
 
 
-def test_a_long_call_on_sampled_rows():
-    """2000 x 2000 with 3 heads: all of it."""
+def test_a_longer_call():
     check(*tensors(27, "bf16", 1, 2000, 2000, 3, 3, 128))
 
 

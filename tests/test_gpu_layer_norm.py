@@ -170,6 +170,14 @@ def test_modulation_gradients(rows, batches, per, hidden):
     check_backward(dy, x, scale, 1.0, per or rows // batches, got)
 
 
+@pytest.mark.parametrize("param", ["bf16", "fp16"])
+def test_modulation_of_16_bits(param):
+    """1 + scale is formed in fp32, not in the scale's type."""
+    x, dy = rows_of(9, 60, 512, "bf16"), rows_of(10, 60, 512, "bf16", 1 / 16)
+    scale = (params_of(11, (2, 512), "fp32")[1] / 100).to(TYPES[param])
+    check_backward(dy, x, scale, 1.0, 30, qkr.fuse_scale_shift_backward(dy, x, scale))
+
+
 def test_modulation_rows_that_no_row_uses_get_zeros():
     x, dy = rows_of(12, 20, 128, "bf16"), rows_of(13, 20, 128, "bf16")
     scale = params_of(14, (5, 128), "fp32")[1]
