@@ -172,9 +172,17 @@ def qknorm_rope_fused_raw(qkv: int, q: int, k: int, tokens: int, heads: int, hea
                                      stream or None))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported at the first call that needs it (the raw entry points
+    work without)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _x_code(t) -> int:
@@ -343,10 +351,14 @@ def dit_fuse_scale_shift_raw(x: int, y: int, rows: int, hidden: int, rows_per_ba
 
 def _mod_code(t) -> int:
     torch = _torch()
-    codes = {torch.bfloat16: QKR_BF16, torch.float16: QKR_FP16, torch.float32: QKR_FP32}
-    if t.dtype not in codes:
-        raise ValueError("scale/shift must be bfloat16, float16 or float32, got %s" % t.dtype)
-    return codes[t.dtype]
+    dtype = t.dtype
+    if dtype == torch.float32:
+        return QKR_FP32
+    if dtype == torch.bfloat16:
+        return QKR_BF16
+    if dtype == torch.float16:
+        return QKR_FP16
+    raise ValueError("scale/shift must be bfloat16, float16 or float32, got %s" % dtype)
 
 
 def fuse_scale_shift(x, scale, shift, *, out=None, eps: float = 1e-6,
@@ -657,37 +669,38 @@ def layer_norm_backward_workspace_size(rows: int, hidden: int, rows_per_batch: i
         rows, hidden, max(1, rows) if rows_per_batch is None else rows_per_batch))
 
 
-def _norm_backward(dy, x, weight, form, rows_per_batch, params_shape, out, eps, workspace, stream):
+def _norm_backward(dy, x, weight, form, rows, hidden, rows_per_batch, params_shape, out, eps,
+                   workspace, stream):
     torch = _torch()
     lib = load_library()
-    hidden = x.shape[-1]
-    rows = x.numel() // hidden if x.numel() else 0
+    device = x.device
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must match x in shape and dtype")
+    if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
+        raise ValueError("out must match x in shape and dtype")
     dweight = dbias = None
+    ws_bytes = 0
     with _launch_stream_context(x, stream):
         if params_shape is not None:
             make = torch.empty if rows else torch.zeros     # without rows the sums are empty
-            dweight = make(params_shape, dtype=torch.float32, device=x.device)
-            dbias = make(params_shape, dtype=torch.float32, device=x.device)
+            dweight = make(params_shape, dtype=torch.float32, device=device)
+            dbias = make(params_shape, dtype=torch.float32, device=device)
             if workspace is None:
-                need = int(lib.dit_layer_norm_backward_workspace_size(rows, hidden, rows_per_batch))
-                if need < 0:
-                    raise QkrError(need, strerror(need))
-                if need > 0:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+                ws_bytes = lib.dit_layer_norm_backward_workspace_size(rows, hidden, rows_per_batch)
+                if ws_bytes < 0:
+                    raise QkrError(ws_bytes, strerror(ws_bytes))
+                if ws_bytes > 0:
+                    workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+            else:
+                ws_bytes = workspace.numel() * workspace.element_size()
         if out is None:
             out = torch.empty_like(x)
-    if out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must match x in shape and dtype")
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     ctx, stream_ptr = _call_context(x, (dy, out, weight, workspace), stream)
     with ctx:
         status = lib.dit_layer_norm_backward(
-            _ptr(dy), _ptr(x), _ptr(out), rows, hidden, rows_per_batch,
-            _ptr(weight), form, QKR_FP32 if weight is None else _mod_code(weight),
-            _ptr(dweight), _ptr(dbias), float(eps), _x_code(x),
-            _ptr(workspace), ws_bytes, stream_ptr)
+            _ptr(dy), _ptr(x), _ptr(out), rows, hidden, rows_per_batch, _ptr(weight), form,
+            QKR_FP32 if weight is None else _mod_code(weight), _ptr(dweight), _ptr(dbias),
+            float(eps), _x_code(x), _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return out, dweight, dbias
 
@@ -705,9 +718,9 @@ def layer_norm_backward(dy, x, weight=None, *, out=None, eps: float = 1e-6, work
     hidden = x.shape[-1]
     if weight is not None and weight.shape != (hidden,):
         raise ValueError("weight must be [%d]" % hidden)
-    rows = x.numel() // hidden if x.numel() else 0
-    return _norm_backward(dy, x, weight, DIT_LN_WEIGHT, max(1, rows),
-                          None if weight is None else (hidden,), out, eps, workspace, stream)
+    rows = x.numel() // hidden if hidden else 0
+    return _norm_backward(dy, x, weight, DIT_LN_WEIGHT, rows, hidden, max(1, rows),
+                          None if weight is None else hidden, out, eps, workspace, stream)
 
 
 def fuse_scale_shift_backward(dy, x, scale, *, out=None, eps: float = 1e-6,
@@ -732,8 +745,8 @@ def fuse_scale_shift_backward(dy, x, scale, *, out=None, eps: float = 1e-6,
     used = -(-rows // rows_per_batch) if rows_per_batch > 0 else 0
     if used > batches:
         raise ValueError("scale holds fewer batches than the rows need")
-    dx, dscale, dshift = _norm_backward(dy, x, scale, DIT_LN_ONE_PLUS, rows_per_batch, scale.shape,
-                                        out, eps, workspace, stream)
+    dx, dscale, dshift = _norm_backward(dy, x, scale, DIT_LN_ONE_PLUS, rows, hidden, rows_per_batch,
+                                        scale.shape, out, eps, workspace, stream)
     if 0 < used < batches:
         with _launch_stream_context(x, stream):
             for t in (dscale, dshift):
