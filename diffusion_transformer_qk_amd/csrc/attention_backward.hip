@@ -43,8 +43,8 @@ struct BwdParams {
     uint32_t pairs;                           // batch * kv_heads
     int32_t q_tokens, kv_tokens, heads, kv_heads, group, rows;
     int32_t row_blocks, key_blocks;
-    int32_t row_splits, row_tiles_per_split;  // of the query tiles, in dkv
-    int32_t key_splits, key_tiles_per_split;  // of the key tiles, in dq
+    int32_t row_splits;                       // of the query tiles, in dkv
+    int32_t key_splits;                       // of the key tiles, in dq
     int32_t stat_blocks, value_blocks;        // runs of a head's rows, of a key head's values
     float scale, c;                           // c = scale * log2(e)
     float* stats;                             // [batch][heads][q_tokens][lse2, delta]
@@ -180,7 +180,10 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
     const BlockOf block(bid, p.pairs, p.key_blocks * p.row_splits);
-    const int kb = block.part % p.key_blocks, split = block.part / p.key_blocks;
+    // causal: the first key blocks are seen by most queries; turning the order
+    // from split to split keeps them from meeting on the same CUs
+    const int split = block.part / p.key_blocks;
+    const int kb = (block.part + (CAUSAL ? split : 0)) % p.key_blocks;
     const uint32_t bh = block.pair;
     const int64_t b = bh / (uint32_t)p.kv_heads;
     const int hk = bh % (uint32_t)p.kv_heads;
@@ -202,8 +205,9 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     const int tiles = (p.q_tokens + BQ - 1) / BQ;
     const int per = tiles > first ? tiles - first : 0;    // tiles of one query head
     const int all = kb * BK < len ? per * p.group : 0;
-    const int t0 = split * p.row_tiles_per_split;
-    const int total = (all < t0 + p.row_tiles_per_split ? all : t0 + p.row_tiles_per_split) - t0;
+    const int each = (all + p.row_splits - 1) / p.row_splits;
+    const int t0 = split * each;
+    const int total = (all < t0 + each ? all : t0 + each) - t0;
 
     f32x16 dk[DB], dv[DB];
 #pragma unroll
@@ -389,8 +393,9 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
         end = sees < end ? (sees < 0 ? 0 : sees) : end;
     }
     const int all = (end + BN - 1) / BN;
-    const int t0 = split * p.key_tiles_per_split;
-    const int tiles = all < t0 + p.key_tiles_per_split ? all : t0 + p.key_tiles_per_split;
+    const int each = (all + p.key_splits - 1) / p.key_splits;
+    const int t0 = split * each;
+    const int tiles = all < t0 + each ? all : t0 + each;
     int open = len;
     if (CAUSAL) {
         const int s = (r0 < p.rows ? r0 : p.rows - 1) / p.group + shift + 1;
@@ -562,26 +567,21 @@ void attention_sum_kernel(const BwdParams p)
 
 // How a call is cut up, and where its workspace's parts begin (in floats).
 struct Shape {
-    int64_t row_blocks, key_blocks, row_splits, row_tiles_per_split, key_splits, key_tiles_per_split;
+    int64_t row_blocks, key_blocks, row_splits, key_splits;
     int64_t stat_blocks, value_blocks;
     int64_t row_norms, value_norms, part_kv, part_q, floats;
 };
 
-// The splits of `tiles` tiles that let `blocks` workgroups fill a chip that
-// holds `resident`: none if they fill half of it, and runs of at least `least`
-// tiles (about 10 us of work, twice what the launch that adds them costs).
-void cut(int64_t blocks, int64_t resident, int64_t tiles, int64_t least, int64_t& splits, int64_t& each)
+// The splits of at most `tiles` tiles that let `blocks` workgroups fill a chip
+// that holds `resident`: none if they fill half of it, and runs of at least
+// `least` tiles (about 10 us of work, twice what the launch that adds them
+// costs).  A workgroup divides the tiles that its masks leave.
+int64_t splits_of(int64_t blocks, int64_t resident, int64_t tiles, int64_t least)
 {
-    splits = 1;
-    if (blocks > 0 && 2 * blocks <= resident && tiles >= 2 * least) {
-        splits = resident / blocks;
-        if (splits > tiles / least)
-            splits = tiles / least;
-    }
-    each = (tiles + splits - 1) / splits;
-    if (each < 1)
-        each = 1;
-    splits = tiles ? (tiles + each - 1) / each : 1;
+    if (blocks == 0 || 2 * blocks > resident || tiles < 2 * least)
+        return 1;
+    const int64_t fill = resident / blocks, most = tiles / least;
+    return fill < most ? fill : most;
 }
 
 Shape shape_of(const dit_attn_args& a)
@@ -595,10 +595,8 @@ Shape shape_of(const dit_attn_args& a)
     // workgroups resident at once (head_dim 64 would hold 3 a CU, but its sums of
     // more parts cost what that gains: 33 us with 2 as with 3 on 12 x 8 blocks)
     const int64_t resident = 256 * (a.head_dim == 256 ? 1 : 2);
-    cut(pairs * s.key_blocks, resident, (a.q_tokens + 63) / 64 * group, 8, s.row_splits,
-        s.row_tiles_per_split);
-    cut(pairs * s.row_blocks, resident, (a.kv_tokens + 63) / 64, 8, s.key_splits,
-        s.key_tiles_per_split);
+    s.row_splits = splits_of(pairs * s.key_blocks, resident, (a.q_tokens + 63) / 64 * group, 8);
+    s.key_splits = splits_of(pairs * s.row_blocks, resident, (a.kv_tokens + 63) / 64, 8);
     const int64_t run = 4 * 256 / (a.head_dim / 8);
     s.stat_blocks = (a.q_tokens + run - 1) / run;
     s.value_blocks = (a.kv_tokens + run - 1) / run;
@@ -722,9 +720,7 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     p.row_blocks = (int32_t)shape.row_blocks;
     p.key_blocks = (int32_t)shape.key_blocks;
     p.row_splits = (int32_t)shape.row_splits;
-    p.row_tiles_per_split = (int32_t)shape.row_tiles_per_split;
     p.key_splits = (int32_t)shape.key_splits;
-    p.key_tiles_per_split = (int32_t)shape.key_tiles_per_split;
     p.stat_blocks = (int32_t)shape.stat_blocks;
     p.value_blocks = (int32_t)shape.value_blocks;
     p.row_norms = p.stats + shape.row_norms;

@@ -34,7 +34,7 @@ struct FwdParams {
     int32_t q_tokens, kv_tokens, kv_heads, group, rows;    // rows = q_tokens * group
     int32_t row_blocks;
     uint32_t pairs;                           // batch * kv_heads
-    int32_t splits, tiles_per_split;
+    int32_t splits;                           // of the key tiles
     float c;                                  // scale * log2(e)
     float* part_o;                            // [splits][batch * kv_heads * rows][D]
     float* part_lse;                          // [splits][batch * kv_heads * rows], base 2
@@ -93,8 +93,9 @@ void attention_forward_kernel(const FwdParams p)
         end = sees < end ? (sees < 0 ? 0 : sees) : end;
     }
     const int tiles = (end + BN - 1) / BN;
-    const int t0 = split * p.tiles_per_split;
-    const int t1 = tiles < t0 + p.tiles_per_split ? tiles : t0 + p.tiles_per_split;
+    // an even share of the tiles that this row block's masks leave
+    const int each = (tiles + p.splits - 1) / p.splits;
+    const int t0 = split * each, t1 = tiles < t0 + each ? tiles : t0 + each;
     // keys below this are seen by every row of the wave
     int open = len;
     if (CAUSAL) {
@@ -284,7 +285,7 @@ void attention_join_kernel(const FwdParams p)
 
 struct Shape {
     int waves;
-    int64_t row_blocks, splits, tiles_per_split;
+    int64_t row_blocks, splits;
 };
 
 // Up to 32 rows of a pair (one query, and a few) are one wave's: nothing is
@@ -292,7 +293,6 @@ struct Shape {
 // in flight.  Calls that leave CUs idle cut the keys: into as many runs as fill
 // the chip once, of at least 16 tiles (4 of one wave, which wait for memory),
 // or the launch that joins them costs what they save.
-
 Shape shape_of(const dit_attn_args& a)
 {
     Shape s;
@@ -312,10 +312,6 @@ Shape shape_of(const dit_attn_args& a)
         if (s.splits > tiles / least)
             s.splits = tiles / least;
     }
-    s.tiles_per_split = (tiles + s.splits - 1) / s.splits;
-    if (s.tiles_per_split < 1)
-        s.tiles_per_split = 1;
-    s.splits = tiles ? (tiles + s.tiles_per_split - 1) / s.tiles_per_split : 1;
     return s;
 }
 
@@ -408,7 +404,6 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
     p.row_blocks = (int32_t)s.row_blocks;
     p.pairs = (uint32_t)(a.batch * a.kv_heads);
     p.splits = (int32_t)s.splits;
-    p.tiles_per_split = (int32_t)s.tiles_per_split;
     p.c = a.scale * kLog2e;
     const int64_t total = a.batch * a.kv_heads * (int64_t)p.rows;
     p.part_o = static_cast<float*>(workspace);
