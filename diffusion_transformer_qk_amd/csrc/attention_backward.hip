@@ -66,56 +66,70 @@ __device__ __forceinline__ int bound_exponent(float bound)
     return __builtin_amdgcn_frexp_expf(bound);
 }
 
-// Rows of one workgroup of the kernel below: D / 8 lanes a row, 4 rows each.
-template <int D>
-constexpr int stat_rows() { return 4 * 256 / (D / 8); }
+// Rows of a workgroup of the kernel below: 32 queries a wave, or D / 8 lanes a
+// value, 4 values each.
+constexpr int kStatRows = 128;
+constexpr int value_rows(int d) { return 4 * 256 / (d / 8); }
 
 // lse in base 2 and delta of a run of one head's queries.  fp16: also the
 // largest |dout| of the run, and in further workgroups the largest |v| of a run
 // of a key head's values in use.
+//
+// delta is the diagonal of out dout^T, taken on the matrix cores in the order
+// in which dout . v is summed: where out is a copy of one value (a query that
+// sees one key, or gives one all its weight) dp - delta is then exactly 0, and
+// not what two orders of summation differ by.
 template <int D, bool F16>
 __global__ __launch_bounds__(256)
 void row_stats_kernel(const BwdParams p)
 {
-    constexpr int L = D / 8, R = 256 / L;
     __shared__ float tops[4];
-    const int d0 = threadIdx.x % L * 8, row0 = threadIdx.x / L;
     const int64_t rows = p.batch * p.heads * p.stat_blocks;
     float top = 0.0f;
     if (blockIdx.x < rows) {
+        const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
         const int64_t bh = blockIdx.x / p.stat_blocks, b = bh / p.heads;
         const int h = bh % p.heads;
-        const uint16_t* dor = p.dout + b * p.do_bs + h * p.do_hs + d0;
-        const uint16_t* outr = p.out + b * p.o_bs + h * p.o_hs + d0;
+        const int64_t qi = (int64_t)(blockIdx.x % p.stat_blocks) * kStatRows + threadIdx.x / 64 * 32 + n;
+        const bool there = qi < p.q_tokens;
+        const uint16_t* dor = p.dout + b * p.do_bs + qi * p.do_ts + h * p.do_hs + 8 * g;
+        const uint16_t* outr = p.out + b * p.o_bs + qi * p.o_ts + h * p.o_hs + 8 * g;
+        u32x4 df[D / 16], of[D / 16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t qi = (int64_t)(blockIdx.x % p.stat_blocks) * 4 * R + i * R + row0;
-            const bool there = qi < p.q_tokens;
-            float x[8], y[8];
-            unpack8<F16>(there ? load16<false>(dor + qi * p.do_ts) : u32x4{0, 0, 0, 0}, x);
-            unpack8<F16>(there ? load16<false>(outr + qi * p.o_ts) : u32x4{0, 0, 0, 0}, y);
-            float dot = 0.0f, sq = 0.0f;
+        for (int kk = 0; kk < D / 16; ++kk) {
+            df[kk] = there ? load16<false>(dor + 16 * kk) : u32x4{0, 0, 0, 0};
+            of[kk] = there ? load16<false>(outr + 16 * kk) : u32x4{0, 0, 0, 0};
+        }
+        f32x16 c{};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dot = __builtin_fmaf(x[j], y[j], dot);
-                if (F16)
-                    sq = __builtin_fmaf(x[j], x[j], sq);
-            }
+        for (int kk = 0; kk < D / 16; ++kk)
+            c = mfma<F16>(of[kk], df[kk], c);
+        float delta = 0.0f;
 #pragma unroll
-            for (int w = 1; w < L; w *= 2) {
-                dot += __shfl_xor(dot, w);
-                if (F16)
-                    sq += __shfl_xor(sq, w);
+        for (int i = 0; i < 16; ++i)
+            if (8 * (i / 4) + 4 * g + i % 4 == n)
+                delta = c[i];
+        if (there && ((n >> 2) & 1) == g) {     // the half of the wave that holds row n of column n
+            const float lse = p.lse[bh * p.q_tokens + qi];
+            // a query without keys: exp2(s - inf) is 0 for every score
+            const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+            reinterpret_cast<f32x2*>(p.stats)[bh * p.q_tokens + qi] = f32x2{lse2, delta};
+        }
+        if constexpr (F16) {
+            float sq = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                float x[8];
+                unpack8<true>(df[kk], x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sq = __builtin_fmaf(x[i], x[i], sq);
             }
-            top = fmaxf(top, sq);
-            if (there && d0 == 0) {
-                const float lse = p.lse[bh * p.q_tokens + qi];
-                // a query without keys: exp2(s - inf) is 0 for every score
-                const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
-                reinterpret_cast<f32x2*>(p.stats)[bh * p.q_tokens + qi] = f32x2{lse2, dot};
-            }
+            top = half_sum(sq);
         }
     } else if constexpr (F16) {
+        constexpr int L = D / 8, R = 256 / L;
+        const int d0 = threadIdx.x % L * 8, row0 = threadIdx.x / L;
         const int64_t at = blockIdx.x - rows, bh = at / p.value_blocks, b = bh / p.kv_heads;
         int len = p.kv_tokens;
         if (p.kv_lengths && p.kv_lengths[b] < len)
@@ -123,7 +137,7 @@ void row_stats_kernel(const BwdParams p)
         const uint16_t* vr = p.v + b * p.v_bs + bh % p.kv_heads * p.v_hs + d0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t j = at % p.value_blocks * 4 * R + i * R + row0;
+            const int64_t j = at % p.value_blocks * value_rows(D) + i * R + row0;
             float x[8], sq = 0.0f;
             unpack8<true>(j < len ? load16<false>(vr + j * p.v_ts) : u32x4{0, 0, 0, 0}, x);
 #pragma unroll
@@ -597,9 +611,8 @@ Shape shape_of(const dit_attn_args& a)
     const int64_t resident = 256 * (a.head_dim == 256 ? 1 : 2);
     s.row_splits = splits_of(pairs * s.key_blocks, resident, (a.q_tokens + 63) / 64 * group, 8);
     s.key_splits = splits_of(pairs * s.row_blocks, resident, (a.kv_tokens + 63) / 64, 8);
-    const int64_t run = 4 * 256 / (a.head_dim / 8);
-    s.stat_blocks = (a.q_tokens + run - 1) / run;
-    s.value_blocks = (a.kv_tokens + run - 1) / run;
+    s.stat_blocks = (a.q_tokens + kStatRows - 1) / kStatRows;
+    s.value_blocks = (a.kv_tokens + value_rows(a.head_dim) - 1) / value_rows(a.head_dim);
     const auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
     s.row_norms = whole(a.batch * a.heads * a.q_tokens * 2);
     s.value_norms = s.row_norms + whole(a.batch * a.heads * s.stat_blocks);

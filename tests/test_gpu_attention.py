@@ -130,6 +130,21 @@ def test_rows_of_very_different_gradients_keep_theirs_in_fp16():
     assert (off <= 2 * 2.0 ** -11 * grad.norm(dim=3) + 64 ** 0.5 * 2.0 ** -25).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_query_with_one_key_moves_neither(dtype, d):
+    """Its probability is 1 whatever q and k are: their gradients are 0, not
+    what two sums of dout . v differ by."""
+    for sq, sk, h, hk, lengths, causal in ((1, 1, 3, 3, None, False), (70, 1, 4, 2, None, False),
+                                           (40, 90, 2, 1, [1, 0, 1], False), (1, 1, 2, 2, None, True)):
+        q, k, v, dout = tensors(35, dtype, 3, sq, sk, h, hk, d)
+        _, _, (dq, dk, _) = check(q, k, v, dout, lengths=lengths, causal=causal)
+        assert (dq == 0).all() and (dk == 0).all()
+    q, k, v, dout = tensors(36, dtype, 1, 64, 64, 1, 1, d)
+    dq = check(q, k, v, dout, causal=True)[2][0]
+    assert (dq[:, 0] == 0).all()
+
+
 @pytest.mark.parametrize("scale", [0.01, 1.0])
 def test_scale(scale):
     check(*tensors(15, "bf16", 1, 40, 70, 2, 2, 64), scale=scale)
