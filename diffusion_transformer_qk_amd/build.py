@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libqknorm_rope.so")
 # The attention kernels: a library of their own, because every kernel of
 # libqknorm_rope.so is memory-bound work without matrix instructions and the
 # tests hold its whole code to that.  libqknorm_rope.so names it as a
-# dependency beside itself, so one library is still all that a caller links.
+# dependency beside itself, so loading the one brings the other along (a C
+# program that calls attention links both).
 ATTN_SRCS = [os.path.join(PKG, "csrc", "attention_forward.hip"),
              os.path.join(PKG, "csrc", "attention_backward.hip")]
 ATTN_LIB = os.path.join(PKG, "libdit_attention.so")

@@ -169,6 +169,7 @@ __device__ __forceinline__ float largest(const float* v, int n, float* slot)
 
 constexpr int kWaves = 4;
 constexpr int kTileRows = 64;      // queries (dk and dv) or keys (dq) staged at a time
+constexpr int kFewRows = 32;
 
 constexpr int waves_per_key_block(int d) { return d == 256 ? 2 : 1; }
 
@@ -183,7 +184,7 @@ constexpr int waves_per_key_block(int d) { return d == 256 ? 2 : 1; }
 // 1 / DS of the columns of its dk and dv (head_dim 256, whose 256 accumulators
 // and 128 registers of k and v would not fit beside the products' operands).
 // The queries are taken 64 at a time.
-template <int D, bool F16, bool CAUSAL>
+template <int D, bool F16, bool CAUSAL, bool TWO>
 __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* lds, float* tops,
                                               uint32_t bid)
 {
@@ -334,12 +335,25 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const u32x4 pf = pack_b<F16>(s, k), sf = pack_b<F16>(dp, k);
+                u32x4 p_rest, s_rest;
+                if constexpr (TWO) {
+                    p_rest = pack_rest<F16>(s, k, pf);
+                    s_rest = pack_rest<F16>(dp, k, sf);
+                }
 #pragma unroll
-                for (int i = 0; i < DB; ++i)
-                    dv[i] = mfma<F16>(tr_fragment(at, kTile + y * block_bytes<D>() + db0 * kSlab, k, i), pf, dv[i]);
+                for (int i = 0; i < DB; ++i) {
+                    const u32x4 f = tr_fragment(at, kTile + y * block_bytes<D>() + db0 * kSlab, k, i);
+                    dv[i] = mfma<F16>(f, pf, dv[i]);
+                    if constexpr (TWO)
+                        dv[i] = mfma<F16>(f, p_rest, dv[i]);
+                }
 #pragma unroll
-                for (int i = 0; i < DB; ++i)
-                    dk[i] = mfma<F16>(tr_fragment(at, y * block_bytes<D>() + db0 * kSlab, k, i), sf, dk[i]);
+                for (int i = 0; i < DB; ++i) {
+                    const u32x4 f = tr_fragment(at, y * block_bytes<D>() + db0 * kSlab, k, i);
+                    dk[i] = mfma<F16>(f, sf, dk[i]);
+                    if constexpr (TWO)
+                        dk[i] = mfma<F16>(f, s_rest, dk[i]);
+                }
             }
         }
         q0 = following;
@@ -375,7 +389,7 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
 
 // ---------------------------------------------------------------- dq
 
-template <int D, bool F16, bool CAUSAL>
+template <int D, bool F16, bool CAUSAL, bool TWO>
 __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* lds, float* tops,
                                                 uint32_t bid)
 {
@@ -500,9 +514,16 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const u32x4 sf = pack_b<F16>(s, k);
+                u32x4 s_rest;
+                if constexpr (TWO)
+                    s_rest = pack_rest<F16>(s, k, sf);
 #pragma unroll
-                for (int i = 0; i < DB; ++i)
-                    dq[i] = mfma<F16>(tr_fragment(at, j * block_bytes<D>(), k, i), sf, dq[i]);
+                for (int i = 0; i < DB; ++i) {
+                    const u32x4 f = tr_fragment(at, j * block_bytes<D>(), k, i);
+                    dq[i] = mfma<F16>(f, sf, dq[i]);
+                    if constexpr (TWO)
+                        dq[i] = mfma<F16>(f, s_rest, dq[i]);
+                }
             }
         }
         at.flip(2 * kTile);
@@ -526,8 +547,20 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
 // Both in one launch, dk and dv first (their workgroups take longer): they do
 // not wait for each other, so the last workgroups of the one leave no CU idle
 // that the other could use.
-template <int D, bool F16, bool CAUSAL>
-__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2)
+//
+// TWO: p and ds go into the products as two 16-bit terms, the second being what
+// the rounding of the first left, so that the gradients are off by their own
+// rounding alone.  It is for calls of up to kFewRows rows a key head, which wait
+// for memory and launches (16 queries over 32760 keys, 5 heads of 128: 76 us,
+// 70 with one term; 2 x 1 over 256, 24 heads of 64: 18 us with either).
+constexpr int backward_waves(int d, bool f16, bool two)
+{
+    // fp16's scaling and both terms together need more than 256 registers
+    return d == 256 || (d == 128 && f16 && two) ? 1 : 2;
+}
+
+template <int D, bool F16, bool CAUSAL, bool TWO>
+__global__ __launch_bounds__(kWaves * 64, backward_waves(D, F16, TWO))
 void attention_backward_kernel(const BwdParams p)
 {
     // two buffers of two tiles, then two of the tiles' lse2 and delta
@@ -536,9 +569,9 @@ void attention_backward_kernel(const BwdParams p)
     __shared__ float tops[8];
     const uint32_t first = p.pairs * (uint32_t)(p.key_blocks * p.row_splits);
     if (blockIdx.x < first)
-        key_gradients<D, F16, CAUSAL>(p, lds, tops, blockIdx.x);
+        key_gradients<D, F16, CAUSAL, TWO>(p, lds, tops, blockIdx.x);
     else
-        query_gradients<D, F16, CAUSAL>(p, lds, tops, blockIdx.x - first);
+        query_gradients<D, F16, CAUSAL, TWO>(p, lds, tops, blockIdx.x - first);
 }
 
 // Adds the splits' dk and dv, or dq, in order: D / 8 threads a row.
@@ -635,7 +668,8 @@ hipError_t launch(BwdParams p, hipStream_t st)
                                   argv, 0, st);
     };
     go(row_stats_kernel<D, F16>, p.batch * p.heads * p.stat_blocks + (F16 ? pairs * p.value_blocks : 0));
-    go(attention_backward_kernel<D, F16, CAUSAL>,
+    go(p.rows <= kFewRows ? attention_backward_kernel<D, F16, CAUSAL, true>
+                          : attention_backward_kernel<D, F16, CAUSAL, false>,
        pairs * ((int64_t)p.key_blocks * p.row_splits + (int64_t)p.row_blocks * p.key_splits));
     if (p.row_splits > 1)
         go(attention_sum_kernel<D, F16, true>, (pairs * 2 * p.kv_tokens + R - 1) / R);

@@ -1,7 +1,9 @@
 /*
  * dit_attention.h -- C ABI of attention, forward and backward, for AMD
  * Instinct MI355X (gfx950): the step between the QK-norm + RoPE pass of
- * qknorm_rope.h and a block's output projection.
+ * qknorm_rope.h and a block's output projection.  The functions are in
+ * libdit_attention.so, which libqknorm_rope.so loads (a program that calls them
+ * links both).
  *
  * For sample b, query i, head h (which reads key/value head
  * h / (heads / kv_heads)) and the keys j that query i sees:

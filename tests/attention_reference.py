@@ -8,6 +8,8 @@ The bounds follow from the arithmetic.  With u half a step of the 16-bit type
     relative e_p = 2 e_s + (keys + 16) f (numerator, denominator, exp2);
   p is rounded to 16 bits before it is multiplied (u), the output once (u);
   fp16 products of p below its normal range add 2^-24 / 2^7 of the largest p.
+Calls of up to 32 query rows a key head round p and ds in two terms: u^2 in the
+place of u there (two_terms).
 Backward, p comes from lse (its rounding: 2 f |lse|), ds = p (dp - delta) is
 rounded to 16 bits, dp is off by (D + 4) f sum|dout v| and delta by the
 rounding of out (u sum|dout out|, out being a 16-bit input) and its own sum.
@@ -54,6 +56,10 @@ def clean(x, lengths):
     return torch.where(keep[:, :, None, None], x, torch.zeros_like(x))
 
 
+def two_terms(q, k):
+    return q.shape[1] * q.shape[2] // k.shape[2] <= 32
+
+
 def forward(q, k, v, causal=False, lengths=None, scale=None):
     """dict of out, lse, p (64 bits, heads first) and the bounds of out and lse."""
     group = q.shape[2] // k.shape[2]
@@ -70,17 +76,19 @@ def forward(q, k, v, causal=False, lengths=None, scale=None):
                     torch.zeros_like(s))
     out = p @ vh
     u, f = half_step(q.dtype), F32
+    u_p = u * u if two_terms(q, k) else u
     mag = (qh.abs() @ kh.abs().transpose(2, 3)) * scale
     e_s = ((d + 4) * f * mag + 2 * f * mag).amax(3, keepdim=True) if keys else torch.zeros_like(lse)
     e_p = 2 * e_s + (keys + 16) * f
     pv = p @ vh.abs()
-    bound = (u * out.abs() + (1 + u) * (u + e_p) * pv + subnormal_step(q.dtype)
+    bound = (u * out.abs() + (1 + u) * (u_p + e_p) * pv + subnormal_step(q.dtype)
              + 2 * TINY * vh.abs().sum(2, keepdim=True))
     if q.dtype == torch.float16:
         bound = bound + 2.0 ** -31 * vh.abs().sum(2, keepdim=True) * p.amax(3, keepdim=True) if keys else bound
     lse_bound = e_s + (keys + 16) * f + 4 * f * torch.where(some, lse.abs(), torch.zeros_like(lse))
     return dict(out=out, lse=lse[..., 0], p=p, some=some[..., 0], e_p=e_p, scale=scale, bound=bound,
-                lse_bound=lse_bound[..., 0], q=qh, k=kh, v=vh, group=group)
+                lse_bound=lse_bound[..., 0], q=qh, k=kh, v=vh, group=group,
+                u_p=u_p)
 
 
 def backward(ref, dout, out16, dtype):
@@ -99,7 +107,8 @@ def backward(ref, dout, out16, dtype):
         do.abs() * o16.abs()).sum(3, keepdim=True)
     e_p = ref["e_p"] + 4 * f * torch.where(ref["some"], ref["lse"].abs(),
                                            torch.zeros_like(ref["lse"]))[..., None]
-    e_ds = (u + e_p) * ds.abs() + (1 + u) * p * (e_dp + e_delta) + TINY * (1 + (dp - delta).abs())
+    u_p = ref["u_p"]
+    e_ds = (u_p + e_p) * ds.abs() + (1 + u) * p * (e_dp + e_delta) + TINY * (1 + (dp - delta).abs())
     keys, rows = k.shape[2], q.shape[2] * group
     small = torch.zeros((), dtype=torch.float64, device=q.device)
     if dtype == torch.float16 and p.numel():
@@ -121,7 +130,7 @@ def backward(ref, dout, out16, dtype):
                      + rows * f * joined(scale * (ds.abs().transpose(2, 3) @ q.abs()))
                      + joined(scale * small * q.abs().sum(2, keepdim=True).expand_as(k)) + tail)
     dv = joined(p.transpose(2, 3) @ do)
-    e_pr = (u + e_p) * p + 2 * TINY
+    e_pr = (u_p + e_p) * p + 2 * TINY
     got["dv"] = dv, (u * dv.abs() + (1 + u) * joined(e_pr.transpose(2, 3) @ do.abs())
                      + rows * f * joined(p.transpose(2, 3) @ do.abs())
                      + joined(2.0 ** -39 * do.abs().sum(2, keepdim=True).expand_as(v)) + tail)

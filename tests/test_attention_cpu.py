@@ -230,13 +230,15 @@ def test_kernels_do_not_spill_and_keep_their_waves(objects):
         kernels += yaml.safe_load(doc[:doc.index("\n...")] if "\n..." in doc else doc)["amdhsa.kernels"]
     # 3 head sizes x 2 types x 2 maskings, forward with 1 and 4 waves
     assert sum("attention_forward_kernel" in k[".name"] for k in kernels) == 24
-    assert sum("attention_backward_kernel" in k[".name"] for k in kernels) == 12
+    # and backward with one term of p and ds and with two
+    assert sum("attention_backward_kernel" in k[".name"] for k in kernels) == 24
     for k in kernels:
         # (scalar registers may be parked in lanes of a vector register, not in memory)
         assert not (k[".private_segment_fixed_size"] or k[".vgpr_spill_count"]), k[".name"]
         assert k[".group_segment_fixed_size"] <= 160 * 1024
         m = re.search(r"attention_(forward|backward)_kernelILi(\d+)E", k[".name"])
-        if m and not k[".name"].count("ELi1EEE"):
+        # the kernels for few rows (forward: one wave; backward: two terms) take what they need
+        if m and not k[".name"].count("ELi1EEE") and not ("backward" in k[".name"] and "Lb1EEE" in k[".name"]):
             waves = {("forward", "64"): 4, ("forward", "128"): 3, ("forward", "256"): 2,
                      ("backward", "64"): 3, ("backward", "128"): 2, ("backward", "256"): 1}[m.groups()]
             assert 512 // (-(-k[".vgpr_count"] // 8) * 8) >= waves, (k[".name"], k[".vgpr_count"])
