@@ -235,52 +235,70 @@ void attention_forward_kernel(const FwdParams p)
     }
 }
 
-// Joins the splits of a row: out = sum_k 2^(lse_k - lse) out_k.  A workgroup a
-// row: D / 4 threads hold 4 columns each, 1024 / D such sets take every
-// (1024 / D)th split.
-template <int D, bool F16>
-__global__ __launch_bounds__(256)
-void attention_join_kernel(const FwdParams p)
+// A row of out and its lse (given in base 2).
+template <bool F16>
+__device__ __forceinline__ void store_joined(const FwdParams& p, int64_t at, int col, f32x4 o, float lse2)
 {
-    constexpr int L = D / 4, S = 256 / L;
-    __shared__ float tops[4];
-    __shared__ f32x4 sums[S][L];
-    __shared__ float weights[S];
-    const int64_t total = (int64_t)p.pairs * p.rows, at = blockIdx.x;
-    float top = -INFINITY;
-    for (int k = threadIdx.x; k < p.splits; k += 256)
-        top = fmaxf(top, p.part_lse[k * total + at]);
-    top = block_max<4>(top, tops);
-    const float base = top == -INFINITY ? 0.0f : top;
-    const int set = threadIdx.x / L, col = threadIdx.x % L * 4;
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    float l = 0.0f;
-#pragma unroll 4
-    for (int k = set; k < p.splits; k += S) {
-        const float w = __builtin_amdgcn_exp2f(p.part_lse[k * total + at] - base);
-        l += w;
-        o += w * *reinterpret_cast<const f32x4*>(p.part_o + (k * total + at) * D + col);
-    }
-    sums[set][threadIdx.x % L] = o;
-    if (threadIdx.x % L == 0)
-        weights[set] = l;
-    __syncthreads();
-    if (set > 0)
-        return;
-#pragma unroll
-    for (int i = 1; i < S; ++i) {
-        o += sums[i][threadIdx.x];
-        l += weights[i];
-    }
-    o *= l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t bh = at / p.rows, b = bh / p.kv_heads;
     const int r = at % p.rows, qi = r / p.group;
     const int head = (int)(bh % p.kv_heads) * p.group + r % p.group;
     *reinterpret_cast<u32x2*>(p.out + b * p.o_bs + qi * p.o_ts + head * p.o_hs + col) =
         u32x2{pack2<F16>(o[0], o[1]), pack2<F16>(o[2], o[3])};
-    if (threadIdx.x == 0)
-        p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + qi] =
-            l == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(l)) * kLn2;
+    if (col == 0)
+        p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + qi] = lse2 * kLn2;
+}
+
+// Joins the splits of a row: out = sum_k 2^(lse_k - lse) out_k.  D / 4 threads
+// hold 4 columns each.  With many splits (kManySplits or more) a workgroup
+// takes one row and its 1024 / D such sets every (1024 / D)th split; with fewer
+// each set takes a row of its own.
+constexpr int kManySplits = 16;
+
+template <int D, bool F16, bool MANY>
+__global__ __launch_bounds__(256)
+void attention_join_kernel(const FwdParams p)
+{
+    constexpr int L = D / 4, S = 256 / L;
+    const int set = threadIdx.x / L, col = threadIdx.x % L * 4;
+    const int64_t total = (int64_t)p.pairs * p.rows;
+    const int64_t at = MANY ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * S + set;
+    float top = -INFINITY, l = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (MANY) {
+        __shared__ float tops[4];
+        for (int k = threadIdx.x; k < p.splits; k += 256)
+            top = fmaxf(top, p.part_lse[k * total + at]);
+        top = block_max<4>(top, tops);
+    } else {
+        if (at >= total)
+            return;
+        for (int k = 0; k < p.splits; ++k)
+            top = fmaxf(top, p.part_lse[k * total + at]);
+    }
+    const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+    for (int k = MANY ? set : 0; k < p.splits; k += MANY ? S : 1) {
+        const float w = __builtin_amdgcn_exp2f(p.part_lse[k * total + at] - base);
+        l += w;
+        o += w * *reinterpret_cast<const f32x4*>(p.part_o + (k * total + at) * D + col);
+    }
+    if constexpr (MANY) {
+        __shared__ f32x4 sums[S][L];
+        __shared__ float weights[S];
+        sums[set][threadIdx.x % L] = o;
+        if (threadIdx.x % L == 0)
+            weights[set] = l;
+        __syncthreads();
+        if (set > 0)
+            return;
+#pragma unroll
+        for (int i = 1; i < S; ++i) {
+            o += sums[i][threadIdx.x];
+            l += weights[i];
+        }
+    }
+    o *= l == 0.0f ? 0.0f : 1.0f / l;
+    store_joined<F16>(p, at, col, o, l == 0.0f ? -INFINITY : base + __builtin_amdgcn_logf(l));
 }
 
 struct Shape {
@@ -333,9 +351,11 @@ Fn select(bool f16, bool causal, int waves)
 }
 
 template <int D>
-Fn select_join(bool f16)
+Fn select_join(bool f16, bool many)
 {
-    return f16 ? attention_join_kernel<D, true> : attention_join_kernel<D, false>;
+    if (many)
+        return f16 ? attention_join_kernel<D, true, true> : attention_join_kernel<D, false, true>;
+    return f16 ? attention_join_kernel<D, true, false> : attention_join_kernel<D, false, false>;
 }
 
 }  // namespace
@@ -418,10 +438,13 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
                                      dim3((unsigned)(p.pairs * s.splits * s.row_blocks)),
                                      dim3(s.waves * 64), argv, 0, st);
     if (err == hipSuccess && s.splits > 1) {
-        fn = a.head_dim == 64 ? select_join<64>(f16)
-             : a.head_dim == 128 ? select_join<128>(f16) : select_join<256>(f16);
-        err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)total), dim3(256), argv, 0,
-                              st);
+        const bool many = s.splits >= kManySplits;
+        fn = a.head_dim == 64    ? select_join<64>(f16, many)
+             : a.head_dim == 128 ? select_join<128>(f16, many)
+                                 : select_join<256>(f16, many);
+        const int64_t rows = many ? 1 : 1024 / a.head_dim;
+        err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)((total + rows - 1) / rows)),
+                              dim3(256), argv, 0, st);
     }
     return err == hipSuccess ? QKR_OK : QKR_ERR_HIP;
 }
