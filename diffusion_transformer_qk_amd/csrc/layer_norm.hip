@@ -468,6 +468,12 @@ int check_sizes(int64_t rows, int32_t hidden, int64_t rows_per_batch)
     return QKR_OK;
 }
 
+// Weight rows that the rows use; rows_per_batch may be any size.
+int64_t batches_of(int64_t rows, int64_t rows_per_batch)
+{
+    return rows / rows_per_batch + (rows % rows_per_batch != 0);
+}
+
 int check_types(int32_t dtype, int32_t param_dtype, float eps)
 {
     if (dtype < QKR_BF16 || dtype > QKR_FP32 || param_dtype < QKR_BF16 || param_dtype > QKR_FP32)
@@ -534,7 +540,7 @@ extern "C" int64_t dit_layer_norm_backward_workspace_size(int64_t rows, int32_t 
     if (rc != QKR_OK || rows == 0)
         return rc;
     const int64_t chunks = chunks_of(rows, hidden, rows_per_batch, true);
-    const int64_t batches = (rows + rows_per_batch - 1) / rows_per_batch;
+    const int64_t batches = batches_of(rows, rows_per_batch);
     return chunks == 1 ? 0 : batches * chunks * 2 * hidden * 4;
 }
 
@@ -563,7 +569,7 @@ extern "C" int dit_layer_norm_backward(const void* dy, const void* x, void* dx, 
     if (need && !aligned16(workspace))
         return QKR_ERR_ALIGN;
     const uint64_t bytes = (uint64_t)rows * (uint64_t)hidden * 2u;
-    const uint64_t params = (uint64_t)((rows + rows_per_batch - 1) / rows_per_batch) * (uint64_t)hidden;
+    const uint64_t params = (uint64_t)batches_of(rows, rows_per_batch) * (uint64_t)hidden;
     const struct { const void* at; uint64_t n; } in[] = {
         {dy, bytes}, {x, bytes}, {weight, weight ? params * (param_dtype == QKR_FP32 ? 4u : 2u) : 0}};
     const struct { const void* at; uint64_t n; } out[] = {
@@ -589,7 +595,7 @@ extern "C" int dit_layer_norm_backward(const void* dy, const void* x, void* dx, 
     p.parts = static_cast<float*>(workspace);
     p.eps = eps;
     fill(p, rows, hidden, rows_per_batch, true);
-    const int64_t batches = (rows + p.rows_per_batch - 1) / p.rows_per_batch;
+    const int64_t batches = batches_of(rows, rows_per_batch);
     Fn fn = dtype == QKR_FP16 ? select<true, true>(hidden) : select<false, true>(hidden);
     const size_t lds = dweight && hidden <= kWaveHidden ? (size_t)3 * 2 * hidden * 4 : 0;
     hipError_t err = launch(fn, batches * p.chunks, lds, p, stream);

@@ -73,6 +73,17 @@ def test_norm_workspaces():
         assert n % (2 * hidden * 4) == 0 and 0 < n <= 1024 * 2 * hidden * 4
 
 
+def test_one_weight_row_for_any_number_of_rows():
+    """rows_per_batch may be far above the rows, up to the largest number."""
+    size = qkr.layer_norm_backward_workspace_size
+    for rows, hidden in ((100, 512), (32760, 5120), ((1 << 24) - 1, 64)):
+        for per in (rows, rows + 1, 1 << 40, (1 << 63) - 1):
+            assert size(rows, hidden, per) == size(rows, hidden)
+    assert ln_back(per=(1 << 63) - 1, ws=0) == b.QKR_ERR_WORKSPACE
+    assert ln_back(per=(1 << 63) - 1, ws_bytes=size(100, 512) - 1) == b.QKR_ERR_WORKSPACE
+    assert ln_back(per=(1 << 63) - 1, dw=A + 2 * FAR) == b.QKR_ERR_ARG
+
+
 def qk(**over):
     v = dict(qkv=(A, A + FAR, A + 2 * FAR), q=None, k=None, tokens=100, heads=4, head_dim=64, qg=A + 3 * FAR,
              kg=A + 3 * FAR + 4096, dqg=A + 4 * FAR, dkg=A + 4 * FAR + 4096, eps=1e-6, cos=A + 5 * FAR,
