@@ -94,7 +94,9 @@ inline int check_tensor(const dit_attn_args& a, const dit_attn_tensor* t, const 
     if (!qkr_host::aligned16(t->data) || t->batch_stride % 8 || t->token_stride % 8 ||
         t->head_stride % 8)
         return QKR_ERR_ALIGN;
-    constexpr int64_t kMax = (int64_t)1 << 44;     // spans stay far inside 64 bits
+    // more than the card holds, and batch * heads < 2^23 (check_args) keeps a
+    // span in bytes inside 64 bits
+    constexpr int64_t kMax = (int64_t)1 << 38;
     if (t->batch_stride < 0 || t->token_stride < 0 || t->head_stride < 0 || t->batch_stride > kMax ||
         t->head_stride > kMax || t->token_stride > DIT_ATTN_MAX_TOKEN_STRIDE ||
         (e.tokens > 1 && t->token_stride < a.head_dim))

@@ -107,6 +107,15 @@ def test_bad_layouts(over, code):
     assert backward(dq=tensor(over.get("data", A + 5 * FAR), 100, 8, **t)) == code
 
 
+def test_strides_whose_spans_would_wrap():
+    """A span of 2^64 bytes would count as none, and its overlaps as none."""
+    a = args(batch=1 << 20, q_tokens=1, kv_tokens=1, heads=1, kv_heads=1)
+    for stride in (1 << 43, (1 << 38) + 8):
+        assert forward(a, out=tensor(A + FAR, 1, 1, batch_stride=stride)) == b.QKR_ERR_SHAPE
+        assert backward(a, dq=tensor(A + FAR, 1, 1, batch_stride=stride)) == b.QKR_ERR_SHAPE
+    assert forward(a, out=tensor(A + FAR, 1, 1, batch_stride=1 << 38)) == b.QKR_ERR_ARG
+
+
 def test_outputs_must_not_share_memory():
     # with themselves
     assert forward(out=tensor(A + 3 * FAR, 100, 8, head_stride=0)) == b.QKR_ERR_ARG
