@@ -742,14 +742,14 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     }
 
     BwdParams p = {};
-    unpack(dout, p.dout, p.do_bs, p.do_ts, p.do_hs);
-    unpack(q, p.q, p.q_bs, p.q_ts, p.q_hs);
-    unpack(k, p.k, p.k_bs, p.k_ts, p.k_hs);
-    unpack(v, p.v, p.v_bs, p.v_ts, p.v_hs);
-    unpack(out, p.out, p.o_bs, p.o_ts, p.o_hs);
-    unpack(dq, p.dq, p.dq_bs, p.dq_ts, p.dq_hs);
-    unpack(dk, p.dk, p.dk_bs, p.dk_ts, p.dk_hs);
-    unpack(dv, p.dv, p.dv_bs, p.dv_ts, p.dv_hs);
+    unpack(a, dout, eq, p.dout, p.do_bs, p.do_ts, p.do_hs);
+    unpack(a, q, eq, p.q, p.q_bs, p.q_ts, p.q_hs);
+    unpack(a, k, ekv, p.k, p.k_bs, p.k_ts, p.k_hs);
+    unpack(a, v, ekv, p.v, p.v_bs, p.v_ts, p.v_hs);
+    unpack(a, out, eq, p.out, p.o_bs, p.o_ts, p.o_hs);
+    unpack(a, dq, eq, p.dq, p.dq_bs, p.dq_ts, p.dq_hs);
+    unpack(a, dk, ekv, p.dk, p.dk_bs, p.dk_ts, p.dk_hs);
+    unpack(a, dv, ekv, p.dv, p.dv_bs, p.dv_ts, p.dv_hs);
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
     p.batch = a.batch;

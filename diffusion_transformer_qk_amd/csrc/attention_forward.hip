@@ -410,10 +410,10 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
 
     const Shape s = shape_of(a);
     FwdParams p = {};
-    unpack(q, p.q, p.q_bs, p.q_ts, p.q_hs);
-    unpack(k, p.k, p.k_bs, p.k_ts, p.k_hs);
-    unpack(v, p.v, p.v_bs, p.v_ts, p.v_hs);
-    unpack(out, p.out, p.o_bs, p.o_ts, p.o_hs);
+    unpack(a, q, eq, p.q, p.q_bs, p.q_ts, p.q_hs);
+    unpack(a, k, ekv, p.k, p.k_bs, p.k_ts, p.k_hs);
+    unpack(a, v, ekv, p.v, p.v_bs, p.v_ts, p.v_hs);
+    unpack(a, out, eq, p.out, p.o_bs, p.o_ts, p.o_hs);
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
     p.q_tokens = (int32_t)a.q_tokens;

@@ -128,15 +128,18 @@ inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor* x, const Ext
 }
 
 // A tensor's pointer and strides as a kernel takes them; one without tokens may
-// be NULL.
+// be NULL.  The token stride of one token may be anything, but the kernels count
+// on at least head_dim: what they stage past the last token lies outside the
+// buffer's range, and reads as zero, only if its rows are a row apart.
 template <typename T>
-inline void unpack(const dit_attn_tensor* t, T*& at, int64_t& bs, int64_t& ts, int64_t& hs)
+inline void unpack(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e, T*& at, int64_t& bs,
+                   int64_t& ts, int64_t& hs)
 {
     if (!t)
         return;
     at = static_cast<T*>(t->data);
     bs = t->batch_stride;
-    ts = t->token_stride;
+    ts = e.tokens > 1 ? t->token_stride : a.head_dim;
     hs = t->head_stride;
 }
 

@@ -194,6 +194,22 @@ def test_fused_buffers_and_other_layouts_give_the_same_bits(d):
     assert (wide[:, :, :, d:] == 7).all() and (wide[:, (0, -1)] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("stride", [0, 8])
+def test_one_token_of_any_stride(dtype, stride):
+    """A single token's stride is never stepped over: 0 and less than a row give
+    the contiguous call's bits, though kernels stage tiles of many rows."""
+    for sq, sk, h, hk in ((1, 70, 4, 2), (70, 1, 2, 2), (1, 1, 3, 1)):
+        x = tensors(37, dtype, 2, sq, sk, h, hk, 128)
+        odd = [t.as_strided(t.shape, (t.stride(0), stride, *t.stride()[2:])) if t.shape[1] == 1 else t for t in x]
+        out, lse = qkr.attention(*x[:3])
+        out2, lse2 = qkr.attention(*odd[:3])
+        assert same_bits(out, out2) and same_bits(lse, lse2)
+        want = qkr.attention_backward(x[3], *x[:3], out, lse)
+        got = qkr.attention_backward(odd[3], *odd[:3], out, lse)
+        assert all(same_bits(a, b) for a, b in zip(got, want))
+
+
 def test_expanded_heads_and_samples_as_inputs():
     """k and v of one sample and head, expanded without memory of their own."""
     q, _, _, dout = tensors(19, "bf16", 3, 40, 90, 4, 4, 64)
