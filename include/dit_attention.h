@@ -25,15 +25,18 @@
  * any gradient; a key that no query sees gets zero gradients.
  *
  * The products take 16-bit operands and accumulate in fp32: p and ds are
- * rounded to the tensors' type before the products that use them; scores,
- * sums, lse and delta are fp32; each output is rounded once.  For fp16, p and
- * ds are scaled by powers of two into its range first, so neither long rows
- * nor small gradients sink into its subnormals.  Results do not depend on the
- * order in which workgroups run (no atomic additions).
+ * rounded to the tensors' type before the products that use them (for up to 32
+ * query rows a key head what that leaves is added as a second operand);
+ * scores, sums, lse and delta are fp32; each output is rounded once.  For
+ * fp16, p and ds are scaled by powers of two into its range first, so neither
+ * long rows nor small gradients sink into its subnormals (ds by a bound on its
+ * query for dq, by the largest of the key head's queries for dk).  Results do
+ * not depend on the order in which workgroups run (no atomic additions).
  *
- * Keys and values at or past kv_lengths[b] are not read.  A key that causality
- * hides from a query takes part in the products with probability 0, so an
- * infinity or NaN in it can reach a query whose tile of 64 keys holds it.
+ * Keys and values at or past kv_lengths[b] are not read.  A query and a key
+ * that causality hides from each other take part in the products with
+ * probability 0, so an infinity or NaN in one can reach the other where a tile
+ * of 64 queries or keys holds it.
  *
  * All pointers are DEVICE pointers owned by the caller.  The library
  * allocates, frees and synchronises nothing and keeps no state between calls.
