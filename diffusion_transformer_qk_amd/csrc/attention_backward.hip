@@ -1,8 +1,8 @@
 // attention_backward.hip -- attention backward for gfx950 (see dit_attention.h).
 //
 // Two launches, the second in two parts:
-//   rows: lse (in base 2) and delta = dout . out of every query, and for fp16
-//         the norms that bound dout . v;
+//   rows: lse (in base 2; for fp16 less the power of two of p) and delta =
+//         dout . out of every query, and for fp16 the norms that bound dout . v;
 //   dkv:  a wave owns 32 keys, keeps their k, v, dk and dv in registers and
 //         walks the queries: S = Q K^T and dP = dO V^T come out with queries
 //         down the registers, so packed P and dS are the B operands of
@@ -71,7 +71,7 @@ __device__ __forceinline__ int bound_exponent(float bound)
 constexpr int kStatRows = 128;
 constexpr int value_rows(int d) { return 4 * 256 / (d / 8); }
 
-// lse in base 2 and delta of a run of one head's queries.  fp16: also the
+// lse2 (above) and delta of a run of one head's queries.  fp16: also the
 // largest |dout| of the run, and in further workgroups the largest |v| of a run
 // of a key head's values in use.
 //
@@ -112,7 +112,7 @@ void row_stats_kernel(const BwdParams p)
         if (there && ((n >> 2) & 1) == g) {     // the half of the wave that holds row n of column n
             const float lse = p.lse[bh * p.q_tokens + qi];
             // a query without keys: exp2(s - inf) is 0 for every score
-            const float lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+            const float lse2 = lse == -INFINITY ? INFINITY : __builtin_fmaf(lse, kLog2e, -p_shift<F16>());
             reinterpret_cast<f32x2*>(p.stats)[bh * p.q_tokens + qi] = f32x2{lse2, delta};
         }
         if constexpr (F16) {
@@ -319,8 +319,7 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = 4 * i4 + i;
-                    const float pr = __builtin_amdgcn_exp2f(
-                        __builtin_fmaf(s[j], p.c, p_shift<F16>() - lse2[i]));
+                    const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], p.c, -lse2[i]));
                     s[j] = pr;
                     dp[j] = F16 ? pr * ((dp[j] - delta[i]) * down) : pr * (dp[j] - delta[i]);
                 }
@@ -478,7 +477,7 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
                            largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops)) + 1;
     }
     // ds alone is needed here, so its power of two goes into the exponent of p
-    const float lse2 = st.x - p_shift<F16>() + (float)e;
+    const float lse2 = st.x + (float)e;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         settle(qf[kk]);
