@@ -171,8 +171,6 @@ constexpr int kWaves = 4;
 constexpr int kTileRows = 64;      // queries (dk and dv) or keys (dq) staged at a time
 constexpr int kFewRows = 32;
 
-constexpr int waves_per_key_block(int d) { return d == 256 ? 2 : 1; }
-
 // What bounds it: the matrix rate at the clock that its power leaves (about
 // 1030 TFLOP/s of the four products at head_dim 128, where a large library
 // product reaches 1220), with the LDS reads, one fragment a product, close
@@ -180,16 +178,19 @@ constexpr int waves_per_key_block(int d) { return d == 256 ? 2 : 1; }
 // the phases of a block apart 3% more: left to itself the scheduler mixes two
 // blocks and has to spill.
 //
-// DS waves share a block of 32 keys: each computes its scores and keeps
-// 1 / DS of the columns of its dk and dv (head_dim 256, whose 256 accumulators
-// and 128 registers of k and v would not fit beside the products' operands).
-// The queries are taken 64 at a time.
+// head_dim 256 takes all 512 registers of a lane: 256 accumulators, 128 of k and
+// v, 32 scores.  The barriers to the scheduler that only it has keep a phase's
+// operands from being read in the one before, which would spill.  (Two waves to a
+// block of keys, each with the scores of all and half the columns of dk and dv,
+// compute 6 products for 4: 1400 against 1075 us on 16 heads of 4096 tokens, 150
+// against 120 on 2 x 16 heads of 700, but 48 against 58 on 8 heads of 512, whose
+// 32 workgroups leave most CUs idle either way.)
 template <int D, bool F16, bool CAUSAL, bool TWO>
 __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* lds, float* tops,
                                               uint32_t bid)
 {
-    constexpr int NW = kWaves, DS = waves_per_key_block(D);
-    constexpr int BK = NW / DS * 32, BQ = kTileRows, QB = BQ / 32, DB = D / 32 / DS;
+    constexpr int NW = kWaves;
+    constexpr int BK = NW * 32, BQ = kTileRows, QB = BQ / 32, DB = D / 32;
     constexpr int kTile = BQ * D * 2;
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -208,9 +209,8 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
         len = given < 0 ? 0 : given < len ? given : len;
     }
     const int shift = p.kv_tokens - p.q_tokens;
-    const int k0 = kb * BK + wave / DS * 32;              // the wave's first key
+    const int k0 = kb * BK + wave * 32;                   // the wave's first key
     const int key = k0 + n;                               // this lane's
-    const int db0 = DS == 1 ? 0 : wave % DS * DB;         // the wave's first column block
     // the first query that sees one of the workgroup's keys, in whole tiles
     int first = 0;
     if (CAUSAL) {
@@ -281,8 +281,9 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     int e = 0;
     if constexpr (F16) {
         const int n = p.group * p.stat_blocks;
-        e = bound_exponent(largest(p.row_norms + bh * n, n, tops) *
-                           largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops + 4)) + 1;
+        e = __builtin_amdgcn_readfirstlane(
+                bound_exponent(largest(p.row_norms + bh * n, n, tops) *
+                               largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops + 4))) + 1;
         down = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
 #pragma unroll
@@ -331,8 +332,12 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
                     if (key > q0 + 32 * y + 8 * (i / 4) + 4 * g + i % 4 + shift)
                         s[i] = dp[i] = 0.0f;
             }
+            if constexpr (D == 256)
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+                if constexpr (D == 256)
+                    __builtin_amdgcn_sched_barrier(0);
                 const u32x4 pf = pack_b<F16>(s, k), sf = pack_b<F16>(dp, k);
                 u32x4 p_rest, s_rest;
                 if constexpr (TWO) {
@@ -341,14 +346,14 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
                 }
 #pragma unroll
                 for (int i = 0; i < DB; ++i) {
-                    const u32x4 f = tr_fragment(at, kTile + y * block_bytes<D>() + db0 * kSlab, k, i);
+                    const u32x4 f = tr_fragment(at, kTile + y * block_bytes<D>(), k, i);
                     dv[i] = mfma<F16>(f, pf, dv[i]);
                     if constexpr (TWO)
                         dv[i] = mfma<F16>(f, p_rest, dv[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < DB; ++i) {
-                    const u32x4 f = tr_fragment(at, y * block_bytes<D>() + db0 * kSlab, k, i);
+                    const u32x4 f = tr_fragment(at, y * block_bytes<D>(), k, i);
                     dk[i] = mfma<F16>(f, sf, dk[i]);
                     if constexpr (TWO)
                         dk[i] = mfma<F16>(f, s_rest, dk[i]);
@@ -359,29 +364,37 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
         at.flip(2 * kTile);
     }
 
-    const bool valid = key < p.kv_tokens;
-    const int64_t to = valid ? key : p.kv_tokens - 1;
+    // the lane's place again: kept over the loop it would take registers that
+    // head_dim 256 does not have (nor, below, for more than one block at a time)
+    int lane_now = lane;
+    if constexpr (D == 256) {
+        lane_now = threadIdx.x % 64;
+        __asm__ volatile("" : "+v"(lane_now));
+    }
+    const int gs = lane_now >> 5, ks = k0 + (lane_now & 31);
+    const bool valid = ks < p.kv_tokens;
+    const int64_t to = valid ? ks : p.kv_tokens - 1;
     const float fv = F16 ? 0x1p-15f : 1.0f;
     const float fk = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
-    if (key >= len) {             // the scores of a padding key are no scores
-#pragma unroll
-        for (int i = 0; i < DB; ++i)
-            dk[i] = dv[i] = f32x16{};
-    }
+    const bool seen = ks < len;   // the scores of a padding key are no scores
     if (p.row_splits == 1) {
-        uint16_t* kr = p.dk + b * p.dk_bs + to * p.dk_ts + hk * p.dk_hs + 32 * db0;
-        uint16_t* vr = p.dv + b * p.dv_bs + to * p.dv_ts + hk * p.dv_hs + 32 * db0;
+        uint16_t* kr = p.dk + b * p.dk_bs + to * p.dk_ts + hk * p.dk_hs;
+        uint16_t* vr = p.dv + b * p.dv_bs + to * p.dv_ts + hk * p.dv_hs;
 #pragma unroll
         for (int i = 0; i < DB; ++i) {
-            store_column<F16>(kr + 32 * i, dk[i], fk, g, valid);
-            store_column<F16>(vr + 32 * i, dv[i], fv, g, valid);
+            if constexpr (D == 256)
+                __builtin_amdgcn_sched_barrier(0);
+            store_column<F16>(kr + 32 * i, dk[i], fk, gs, valid, seen);
+            store_column<F16>(vr + 32 * i, dv[i], fv, gs, valid, seen);
         }
     } else {
-        float* row = p.part_kv + ((split * (int64_t)p.pairs + bh) * p.kv_tokens + to) * 2 * D + 32 * db0;
+        float* row = p.part_kv + ((split * (int64_t)p.pairs + bh) * p.kv_tokens + to) * 2 * D;
 #pragma unroll
         for (int i = 0; i < DB; ++i) {
-            store_column_f32(row + 32 * i, dk[i], fk, g, valid);
-            store_column_f32(row + D + 32 * i, dv[i], fv, g, valid);
+            if constexpr (D == 256)
+                __builtin_amdgcn_sched_barrier(0);
+            store_column_f32(row + 32 * i, dk[i], fk, gs, valid, seen);
+            store_column_f32(row + D + 32 * i, dv[i], fv, gs, valid, seen);
         }
     }
 }
@@ -635,9 +648,9 @@ Shape shape_of(const dit_attn_args& a)
     Shape s;
     const int64_t group = a.heads / a.kv_heads, rows = a.q_tokens * group;
     const int64_t pairs = a.batch * a.kv_heads;
-    const int64_t bk = 32 * kWaves / waves_per_key_block(a.head_dim), bm = 32 * kWaves;
-    s.row_blocks = (rows + bm - 1) / bm;
-    s.key_blocks = (a.kv_tokens + bk - 1) / bk;
+    constexpr int64_t per = 32 * kWaves;
+    s.row_blocks = (rows + per - 1) / per;
+    s.key_blocks = (a.kv_tokens + per - 1) / per;
     // workgroups resident at once (head_dim 64 would hold 3 a CU, but its sums of
     // more parts cost what that gains: 33 us with 2 as with 3 on 12 x 8 blocks)
     const int64_t resident = 256 * (a.head_dim == 256 ? 1 : 2);

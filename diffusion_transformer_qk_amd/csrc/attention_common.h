@@ -274,19 +274,21 @@ __device__ __forceinline__ void settle(u32x4& f) { __asm__ volatile("" : "+v"(f)
 // selects that all of them execute.
 __device__ __forceinline__ void keep_branch() { __asm__ volatile("" ::: "memory"); }
 
-// Column n (this lane's) of a C block, times `f`, as 16-bit elements d0 + 0..31
-// at `row`: the halves of the wave trade groups of 4 so that each lane stores
-// 16 bytes at a time.
+// Column n (this lane's) of a C block, times `f` (zeros unless `keep`), as
+// 16-bit elements d0 + 0..31 at `row`: the halves of the wave trade groups of 4
+// so that each lane stores 16 bytes at a time.
 template <bool F16>
-__device__ __forceinline__ void store_column(uint16_t* row, const f32x16& c, float f, int g, bool valid)
+__device__ __forceinline__ void store_column(uint16_t* row, const f32x16& c, float f, int g, bool valid,
+                                             bool keep = true)
 {
+    const auto at = [&](int i) { return keep ? c[i] * f : 0.0f; };
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
         u32x4 w;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint32_t a = pack2<F16>(c[4 * i + 2 * j] * f, c[4 * i + 2 * j + 1] * f);
-            const uint32_t b = pack2<F16>(c[4 * i + 4 + 2 * j] * f, c[4 * i + 4 + 2 * j + 1] * f);
+            const uint32_t a = pack2<F16>(at(4 * i + 2 * j), at(4 * i + 2 * j + 1));
+            const uint32_t b = pack2<F16>(at(4 * i + 4 + 2 * j), at(4 * i + 4 + 2 * j + 1));
             const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
             w[j] = r[0];
             w[2 + j] = r[1];
@@ -297,13 +299,15 @@ __device__ __forceinline__ void store_column(uint16_t* row, const f32x16& c, flo
 }
 
 // The same in fp32.
-__device__ __forceinline__ void store_column_f32(float* row, const f32x16& c, float f, int g, bool valid)
+__device__ __forceinline__ void store_column_f32(float* row, const f32x16& c, float f, int g, bool valid,
+                                                 bool keep = true)
 {
+    const auto at = [&](int i) { return keep ? c[i] * f : 0.0f; };
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (valid)
             *reinterpret_cast<f32x4*>(row + 8 * i + 4 * g) =
-                f32x4{c[4 * i] * f, c[4 * i + 1] * f, c[4 * i + 2] * f, c[4 * i + 3] * f};
+                f32x4{at(4 * i), at(4 * i + 1), at(4 * i + 2), at(4 * i + 3)};
 }
 
 }  // namespace qkr_attn
