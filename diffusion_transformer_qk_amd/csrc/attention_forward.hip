@@ -51,16 +51,17 @@ constexpr float kSlack = 8.0f;
 // o take 24, 96 or 192 of them a lane beside the 16 scores and the operands.
 constexpr int waves_per_simd(int d) { return d == 64 ? 4 : d == 128 ? 3 : 2; }
 
-// Keys of a tile.  Tiles of 64 keys with two waves a SIMD measured 1 to 2%
-// slower on 32768 queries and 10% on 512 keys (head_dim 128), where the last
-// tile and the start of a workgroup count.
-constexpr int kTileKeys = 32;
+// Keys of a tile.  head_dim 128: 64 keys, which leave two waves a SIMD, measured
+// 1 to 2% slower on 32768 queries and 10% on 512 keys, where the last tile and the
+// start of a workgroup count.  head_dim 64, where a tile's fixed work weighs most
+// and the waves stay four: 32 heads of 4096 take 158 us with 64 keys, 168 with 32.
+constexpr int tile_keys(int d, int waves) { return d == 64 && waves == 4 ? 64 : 32; }
 
 template <int D, bool F16, bool CAUSAL, int NW>
 __global__ __launch_bounds__(NW * 64, NW == 4 ? waves_per_simd(D) : D == 256 ? 1 : 2)
 void attention_forward_kernel(const FwdParams p)
 {
-    constexpr int BM = NW * 32, BN = kTileKeys, KB = BN / 32, DB = D / 32;
+    constexpr int BM = NW * 32, BN = tile_keys(D, NW), KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
     // With one wave the call waits for memory, and p can have a second term,
     // what its rounding to 16 bits left: out is then off by its own rounding
@@ -124,11 +125,14 @@ void attention_forward_kernel(const FwdParams p)
     const auto stage = [&](int t) {
         const int64_t first = (int64_t)t * BN;
         const int left = len - (int)first;
-        if constexpr (NW == 4) {           // two groups of 16 rows each of K and of V
-            if (wave < 2)
-                ks.load(kbase + first * p.k_ts, p.k_ts, left, fill, wave);
-            else
-                vs.load(vbase + first * p.v_ts, p.v_ts, left, fill + kTile, wave - 2);
+        if constexpr (NW == 4) {           // groups of 16 rows: two waves K's, two V's
+#pragma unroll
+            for (int i = 0; i < BN / 32; ++i) {
+                if (wave < 2)
+                    ks.load(kbase + first * p.k_ts, p.k_ts, left, fill, wave + 2 * i);
+                else
+                    vs.load(vbase + first * p.v_ts, p.v_ts, left, fill + kTile, wave - 2 + 2 * i);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -309,7 +313,7 @@ struct Shape {
 // Up to 32 rows of a pair (one query, and a few) are one wave's: nothing is
 // shared in the workgroup, and as many of them as their LDS allows keep loads
 // in flight.  Calls that leave CUs idle cut the keys: into as many runs as fill
-// the chip once, of at least 16 tiles (4 of one wave, which wait for memory),
+// the chip once, of at least 512 keys (128 for one wave, which waits for memory),
 // or the launch that joins them costs what they save.
 Shape shape_of(const dit_attn_args& a)
 {
@@ -318,12 +322,13 @@ Shape shape_of(const dit_attn_args& a)
     s.waves = rows <= 32 ? 1 : 4;
     s.row_blocks = (rows + 32 * s.waves - 1) / (32 * s.waves);
     const int64_t blocks = s.row_blocks * a.batch * a.kv_heads;
-    const int64_t tiles = (a.kv_tokens + kTileKeys - 1) / kTileKeys;
+    const int keys = tile_keys(a.head_dim, s.waves);
+    const int64_t tiles = (a.kv_tokens + keys - 1) / keys;
     // workgroups resident at once: four waves by their registers, one by the
     // double buffers in 160 KB of LDS a CU (8 at most, the waves of two SIMDs)
-    const int64_t by_lds = 160 * 1024 / (8 * kTileKeys * a.head_dim);
+    const int64_t by_lds = 160 * 1024 / (8 * keys * a.head_dim);
     const int64_t resident = 256 * (s.waves == 4 ? waves_per_simd(a.head_dim) : by_lds > 8 ? 8 : by_lds);
-    const int64_t least = s.waves == 1 ? 4 : 16;
+    const int64_t least = (s.waves == 1 ? 128 : 512) / keys;
     s.splits = 1;
     if (blocks > 0 && 2 * blocks <= resident && tiles >= 2 * least) {
         s.splits = resident / blocks;
