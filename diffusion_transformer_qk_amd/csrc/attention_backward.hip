@@ -43,6 +43,7 @@ struct BwdParams {
     uint32_t pairs;                           // batch * kv_heads
     int32_t q_tokens, kv_tokens, heads, kv_heads, group, rows;
     int32_t row_blocks, key_blocks;
+    int32_t column_waves;                     // waves to a block of keys, in dkv (DS)
     int32_t row_splits;                       // of the query tiles, in dkv
     int32_t key_splits;                       // of the key tiles, in dq
     int32_t stat_blocks, value_blocks;        // runs of a head's rows, of a key head's values
@@ -180,17 +181,18 @@ constexpr int kFewRows = 32;
 //
 // head_dim 256 takes all 512 registers of a lane: 256 accumulators, 128 of k and
 // v, 32 scores.  The barriers to the scheduler that only it has keep a phase's
-// operands from being read in the one before, which would spill.  (Two waves to a
-// block of keys, each with the scores of all and half the columns of dk and dv,
-// compute 6 products for 4: 1400 against 1075 us on 16 heads of 4096 tokens, 150
-// against 120 on 2 x 16 heads of 700, but 48 against 58 on 8 heads of 512, whose
-// 32 workgroups leave most CUs idle either way.)
-template <int D, bool F16, bool CAUSAL, bool TWO>
+// operands from being read in the one before, which would spill.
+//
+// DS = 2, for head_dim 256: two waves share a block of 32 keys, each with the
+// scores of all and half the columns of dk and dv.  That is 6 products for 4, but
+// twice the workgroups, for calls that leave CUs idle (8 heads of 512 tokens: 50
+// against 57 us; 16 heads of 4096, which do not: 1400 against 1140).
+template <int D, bool F16, bool CAUSAL, bool TWO, int DS>
 __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* lds, float* tops,
                                               uint32_t bid)
 {
     constexpr int NW = kWaves;
-    constexpr int BK = NW * 32, BQ = kTileRows, QB = BQ / 32, DB = D / 32;
+    constexpr int BK = NW / DS * 32, BQ = kTileRows, QB = BQ / 32, DB = D / 32 / DS;
     constexpr int kTile = BQ * D * 2;
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -209,8 +211,9 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
         len = given < 0 ? 0 : given < len ? given : len;
     }
     const int shift = p.kv_tokens - p.q_tokens;
-    const int k0 = kb * BK + wave * 32;                   // the wave's first key
+    const int k0 = kb * BK + wave / DS * 32;              // the wave's first key
     const int key = k0 + n;                               // this lane's
+    const int db0 = DS == 1 ? 0 : wave % DS * DB;         // the wave's first column block
     // the first query that sees one of the workgroup's keys, in whole tiles
     int first = 0;
     if (CAUSAL) {
@@ -346,14 +349,14 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
                 }
 #pragma unroll
                 for (int i = 0; i < DB; ++i) {
-                    const u32x4 f = tr_fragment(at, kTile + y * block_bytes<D>(), k, i);
+                    const u32x4 f = tr_fragment(at, kTile + y * block_bytes<D>() + db0 * kSlab, k, i);
                     dv[i] = mfma<F16>(f, pf, dv[i]);
                     if constexpr (TWO)
                         dv[i] = mfma<F16>(f, p_rest, dv[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < DB; ++i) {
-                    const u32x4 f = tr_fragment(at, y * block_bytes<D>(), k, i);
+                    const u32x4 f = tr_fragment(at, y * block_bytes<D>() + db0 * kSlab, k, i);
                     dk[i] = mfma<F16>(f, sf, dk[i]);
                     if constexpr (TWO)
                         dk[i] = mfma<F16>(f, s_rest, dk[i]);
@@ -378,8 +381,8 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     const float fk = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
     const bool seen = ks < len;   // the scores of a padding key are no scores
     if (p.row_splits == 1) {
-        uint16_t* kr = p.dk + b * p.dk_bs + to * p.dk_ts + hk * p.dk_hs;
-        uint16_t* vr = p.dv + b * p.dv_bs + to * p.dv_ts + hk * p.dv_hs;
+        uint16_t* kr = p.dk + b * p.dk_bs + to * p.dk_ts + hk * p.dk_hs + 32 * db0;
+        uint16_t* vr = p.dv + b * p.dv_bs + to * p.dv_ts + hk * p.dv_hs + 32 * db0;
 #pragma unroll
         for (int i = 0; i < DB; ++i) {
             if constexpr (D == 256)
@@ -388,7 +391,7 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
             store_column<F16>(vr + 32 * i, dv[i], fv, gs, valid, seen);
         }
     } else {
-        float* row = p.part_kv + ((split * (int64_t)p.pairs + bh) * p.kv_tokens + to) * 2 * D;
+        float* row = p.part_kv + ((split * (int64_t)p.pairs + bh) * p.kv_tokens + to) * 2 * D + 32 * db0;
 #pragma unroll
         for (int i = 0; i < DB; ++i) {
             if constexpr (D == 256)
@@ -580,9 +583,12 @@ void attention_backward_kernel(const BwdParams p)
     __shared__ __attribute__((aligned(kTiles))) char lds[kTiles + 2 * kTileRows * 8];
     __shared__ float tops[8];
     const uint32_t first = p.pairs * (uint32_t)(p.key_blocks * p.row_splits);
-    if (blockIdx.x < first)
-        key_gradients<D, F16, CAUSAL, TWO>(p, lds, tops, blockIdx.x);
-    else
+    if (blockIdx.x < first) {
+        if (D == 256 && p.column_waves == 2)
+            key_gradients<D, F16, CAUSAL, TWO, D == 256 ? 2 : 1>(p, lds, tops, blockIdx.x);
+        else
+            key_gradients<D, F16, CAUSAL, TWO, 1>(p, lds, tops, blockIdx.x);
+    } else
         query_gradients<D, F16, CAUSAL, TWO>(p, lds, tops, blockIdx.x - first);
 }
 
@@ -626,7 +632,7 @@ void attention_sum_kernel(const BwdParams p)
 
 // How a call is cut up, and where its workspace's parts begin (in floats).
 struct Shape {
-    int64_t row_blocks, key_blocks, row_splits, key_splits;
+    int64_t row_blocks, key_blocks, column_waves, row_splits, key_splits;
     int64_t stat_blocks, value_blocks;
     int64_t row_norms, value_norms, part_kv, part_q, floats;
 };
@@ -650,12 +656,19 @@ Shape shape_of(const dit_attn_args& a)
     const int64_t pairs = a.batch * a.kv_heads;
     constexpr int64_t per = 32 * kWaves;
     s.row_blocks = (rows + per - 1) / per;
-    s.key_blocks = (a.kv_tokens + per - 1) / per;
     // workgroups resident at once (head_dim 64 would hold 3 a CU, but its sums of
     // more parts cost what that gains: 33 us with 2 as with 3 on 12 x 8 blocks)
     const int64_t resident = 256 * (a.head_dim == 256 ? 1 : 2);
-    s.row_splits = splits_of(pairs * s.key_blocks, resident, (a.q_tokens + 63) / 64 * group, 8);
     s.key_splits = splits_of(pairs * s.row_blocks, resident, (a.kv_tokens + 63) / 64, 8);
+    // head_dim 256: two waves to a block of keys if all workgroups still run at once
+    for (s.column_waves = a.head_dim == 256 ? 2 : 1;; s.column_waves = 1) {
+        const int64_t keys = per / s.column_waves;
+        s.key_blocks = (a.kv_tokens + keys - 1) / keys;
+        s.row_splits = splits_of(pairs * s.key_blocks, resident, (a.q_tokens + 63) / 64 * group, 8);
+        if (s.column_waves == 1 ||
+            pairs * (s.key_blocks * s.row_splits + s.row_blocks * s.key_splits) <= resident)
+            break;
+    }
     s.stat_blocks = (a.q_tokens + kStatRows - 1) / kStatRows;
     s.value_blocks = (a.kv_tokens + value_rows(a.head_dim) - 1) / value_rows(a.head_dim);
     const auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
@@ -778,6 +791,7 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     const Shape shape = shape_of(a);
     p.row_blocks = (int32_t)shape.row_blocks;
     p.key_blocks = (int32_t)shape.key_blocks;
+    p.column_waves = (int32_t)shape.column_waves;
     p.row_splits = (int32_t)shape.row_splits;
     p.key_splits = (int32_t)shape.key_splits;
     p.stat_blocks = (int32_t)shape.stat_blocks;

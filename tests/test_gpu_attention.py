@@ -304,6 +304,15 @@ def test_few_queries_over_many_keys(dtype, d, batch, sq, sk, h, hk, lengths):
     check(*tensors(24, dtype, batch, sq, sk, h, hk, d), lengths=lengths)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True])
+def test_head_dim_256_in_many_workgroups(dtype, causal):
+    """More workgroups than CUs, where a wave keeps all columns of dk and dv
+    (smaller calls share them between two)."""
+    check(*tensors(38, dtype, 5, 300, 290, 16, 8, 256), causal=causal, lengths=[290, 129, 0, 64, 257])
+    check(*tensors(39, dtype, 30, 3, 140, 16, 8, 256), causal=causal)
+
+
 def test_few_queries_over_many_keys_causal():
     check(*tensors(25, "bf16", 1, 9, 3000, 4, 2, 128), causal=True)
 
