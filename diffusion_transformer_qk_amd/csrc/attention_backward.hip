@@ -97,10 +97,11 @@ void row_stats_kernel(const BwdParams p)
         const uint16_t* outr = p.out + b * p.o_bs + qi * p.o_ts + h * p.o_hs + 8 * g;
         u32x4 df[D / 16], of[D / 16];
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
+        for (int kk = 0; kk < D / 16; ++kk)
             df[kk] = there ? load16<false>(dor + 16 * kk) : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
             of[kk] = there ? load16<false>(outr + 16 * kk) : u32x4{0, 0, 0, 0};
-        }
         f32x16 c{};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
