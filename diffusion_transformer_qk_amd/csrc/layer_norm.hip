@@ -132,9 +132,11 @@ constexpr float kTinySum = 0x1p-100f;
 // sum g (x - mean), all of x * 2^-shift.  shift is 0 unless the plain sums
 // leave fp32's range (16-bit values beyond about 1e17, or squares that sink
 // into the subnormals while eps is as small): then it is the binary exponent
-// of the row's largest |x|, an exact scaling.
+// of the row's largest |x|, an exact scaling.  rstd_x is 1 / sqrt(var + eps) of
+// x itself, the factor of dx: at most 1 / sqrt(eps), so it is always finite,
+// which rstd of a scaled row need not be (eps 2^-2shift may sink to 0).
 struct RowStats {
-    float mean, rstd, g, gd;
+    float mean, rstd, rstd_x, g, gd;
     int shift;
 };
 
@@ -197,7 +199,7 @@ __device__ __forceinline__ RowStats row_stats(const u32x4 (&x)[VPT], const u32x4
     float ss;
     RowStats s = plain_stats<TPR, VPT, F16, GRAD, false>(x, dy, w, t, nvec, hidden, eps, 0, slot, ss);
     if (__builtin_expect(s.rstd <= 0x1.fffffep127f && (ss >= kTinySum || eps >= kTinySum), 1)) {
-        s.rstd = __builtin_amdgcn_rsqf(s.rstd);
+        s.rstd = s.rstd_x = __builtin_amdgcn_rsqf(s.rstd);
         return s;
     }
     float m = 0.0f;            // the same branch in every thread of the row
@@ -213,12 +215,15 @@ __device__ __forceinline__ RowStats row_stats(const u32x4 (&x)[VPT], const u32x4
     const float eps_s = __builtin_amdgcn_ldexpf(eps, -2 * e);
     if (!(eps_s <= 0x1.fffffep127f)) {
         // the variance is below eps by more than 2^128
-        s.rstd = rsqrt_full_range(eps);
+        s.rstd = s.rstd_x = rsqrt_full_range(eps);
         return s;
     }
     s = plain_stats<TPR, VPT, F16, GRAD, true>(x, dy, w, t, nvec, hidden, eps_s, e, slot, ss);
-    // a constant row of large values: eps 2^-2e may underflow to 0
+    // a constant row of large values: eps 2^-2e may underflow to 0.  Any finite
+    // rstd gives its n, which is exactly 0 (sums of up to 8192 equal 16-bit
+    // values do not round), but not its dx.
     s.rstd = __builtin_amdgcn_rsqf(fmaxf(s.rstd, 0x1p-126f));
+    s.rstd_x = ss == 0.0f ? rsqrt_full_range(eps) : __builtin_amdgcn_ldexpf(s.rstd, -e);
     return s;
 }
 
@@ -305,9 +310,7 @@ void layer_norm_kernel(const LnParams p)
                     const float e = s.shift ? __builtin_amdgcn_ldexpf(f[k], -s.shift) : f[k];
                     const float n = (e - s.mean) * s.rstd;
                     if constexpr (GRAD) {
-                        o[k] = __builtin_fmaf(-n, c2, __builtin_fmaf(d[k], w[u][k], -c1)) * s.rstd;
-                        if (s.shift)
-                            o[k] = __builtin_amdgcn_ldexpf(o[k], -s.shift);
+                        o[k] = __builtin_fmaf(-n, c2, __builtin_fmaf(d[k], w[u][k], -c1)) * s.rstd_x;
                         dw[u][k] = __builtin_fmaf(d[k], n, dw[u][k]);
                         db[u][k] += d[k];
                     } else {

@@ -292,3 +292,49 @@ def test_runs_streams_and_graph_replays_give_the_same_bits():
         graph.replay()
         torch.cuda.synchronize()
         assert all(same_bits(a, c) for a, c in zip(kept, want))
+
+
+@pytest.mark.parametrize("hidden", [256, 2560])
+@pytest.mark.parametrize("eps", [1e-6, 1e-35])
+def test_gradients_at_the_ends_of_the_range(hidden, eps):
+    """The rows of test_values_at_the_ends_of_the_range, backwards: dx is as
+    large as rstd, at most 1 / sqrt(eps), which bf16 holds."""
+    x = rows_of(18, 12, hidden, "bf16")
+    big = 2.0 ** 110 * rows_of(19, 12, hidden, "bf16").double()
+    small = 2.0 ** -120 * rows_of(20, 12, hidden, "bf16").double()
+    x[1] = big[1].to(x.dtype)
+    x[3] = small[3].to(x.dtype)
+    x[5] = 3.0
+    x[7] = 0.0
+    x[9] = 1e38
+    w = params_of(21, (hidden,), "fp32")[0]
+    dy = rows_of(22, 12, hidden, "bf16", 1e-3)
+    got = qkr.layer_norm_backward(dy, x, w, eps=eps)
+    check_backward(dy, x, w[None], 0.0, 12, got, eps)
+
+
+@pytest.mark.parametrize("one", [0.0, 1.0])
+@pytest.mark.parametrize("hidden", [256, 2560])
+@pytest.mark.parametrize("eps", [1e-6, 1e-35, 1e-37, 3e-45])
+def test_gradients_of_constant_rows(hidden, eps, one):
+    """A row of one value has n = 0 exactly (up to 8192 copies of a 16-bit value
+    add up without rounding), so dx = (g - avg g) / sqrt(eps) whatever the
+    value, dweight is 0 and dbias the sum of dy.  eps is the fp32 number."""
+    values = [3.0, 0.0, 1024.0, -1e38, 1e18, 2.0 ** -100, 3e38, -2.0 ** -126, 1e30]
+    x = torch.tensor(values)[:, None].expand(-1, hidden).bfloat16().to(DEV)
+    dy = rows_of(36, len(values), hidden, "bf16", 1e-3)
+    w = params_of(37, (1, hidden), "fp32")[0]
+    if one:
+        dx, dw, db = qkr.fuse_scale_shift_backward(dy, x, w, eps=eps)
+    else:
+        dx, dw, db = qkr.layer_norm_backward(dy, x, w[0], eps=eps)
+    g = dy.double() * (w.double() + one)
+    c1 = g.mean(1, keepdim=True)
+    rstd = float(torch.tensor(eps, dtype=torch.float32).double()) ** -0.5
+    want = rstd * (g - c1)
+    bound = half_step(x) * want.abs() + tail(x) + rstd * (
+        C * g.abs().mean(1, keepdim=True) + C * (g.abs() + c1.abs()))
+    off = (dx.double() - want).abs()
+    assert (off <= bound).all(), [float(v) for v in (off - bound).amax(1)]
+    assert (dw == 0).all()
+    assert ((db.double().view(-1) - dy.double().sum(0)).abs() <= 200 * F * dy.double().abs().sum(0)).all()
