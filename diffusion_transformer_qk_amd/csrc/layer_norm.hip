@@ -198,7 +198,9 @@ __device__ __forceinline__ RowStats row_stats(const u32x4 (&x)[VPT], const u32x4
 {
     float ss;
     RowStats s = plain_stats<TPR, VPT, F16, GRAD, false>(x, dy, w, t, nvec, hidden, eps, 0, slot, ss);
-    if (__builtin_expect(s.rstd <= 0x1.fffffep127f && (ss >= kTinySum || eps >= kTinySum), 1)) {
+    // sum g (x - mean) may leave the range where its factors do not
+    if (__builtin_expect(s.rstd <= 0x1.fffffep127f && (ss >= kTinySum || eps >= kTinySum) &&
+                             (!GRAD || fabsf(s.gd) <= 0x1.fffffep127f), 1)) {
         s.rstd = s.rstd_x = __builtin_amdgcn_rsqf(s.rstd);
         return s;
     }

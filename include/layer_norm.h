@@ -18,7 +18,9 @@
  * Math is fp32; y and dx are rounded once, to nearest even, to x's dtype;
  * dweight and dbias are fp32 sums in an order that depends on the sizes alone,
  * so results do not change from run to run.  Rows of any finite values are
- * normalised correctly, as fuse_scale_shift.h describes.
+ * normalised correctly, as fuse_scale_shift.h describes, and get their
+ * gradients, as long as the sums of |g| over a row stay in fp32's range (bf16
+ * gradients of 1e34 may leave it; the row's dx is then infinite or NaN).
  *
  * Pointers are DEVICE pointers owned by the caller; the library allocates,
  * frees and synchronises nothing and work is only enqueued on `stream`.

@@ -338,3 +338,13 @@ def test_gradients_of_constant_rows(hidden, eps, one):
     assert (off <= bound).all(), [float(v) for v in (off - bound).amax(1)]
     assert (dw == 0).all()
     assert ((db.double().view(-1) - dy.double().sum(0)).abs() <= 200 * F * dy.double().abs().sum(0)).all()
+
+
+def test_products_of_large_values_and_gradients():
+    """x of 1e17, whose squares still add up in fp32, times gradients of 1e22,
+    whose products with it do not: dx is about 1e5."""
+    for hidden in (256, 2560):
+        x = rows_of(38, 12, hidden, "bf16", 1e17)
+        dy = rows_of(39, 12, hidden, "bf16", 1e22)
+        w = params_of(40, (hidden,), "fp32")[0]
+        check_backward(dy, x, w[None], 0.0, 12, qkr.layer_norm_backward(dy, x, w))
