@@ -145,9 +145,10 @@ __device__ __forceinline__ u32x4 head_backward(u32x4 xv, u32x4 gv, const float c
     t = head_sum<L>(t);
     const float q = __builtin_fmaf(ss, 1.0f / D, eps);
     float r = __builtin_amdgcn_rsqf(q), rx = r;        // u = x * rx, dx = r (..)
-    if (__builtin_expect(!(q <= 0x1.fffffep127f && (ss >= kTinySum || eps >= kTinySum)), 0)) {
-        // the plain sum of squares is out of range: the same on x * 2^-e, e the
-        // exponent of the head's largest |x| (the same branch in all its lanes)
+    if (__builtin_expect(!(q <= 0x1.fffffep127f && (ss >= kTinySum || eps >= kTinySum) &&
+                           fabsf(t) <= 0x1.fffffep127f), 0)) {
+        // a plain sum is out of range: the same on x * 2^-e, e the exponent of
+        // the head's largest |x| (the same branch in all its lanes)
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)

@@ -14,7 +14,8 @@
  * separately for Q and K.  cos and sin are tables and get no gradient.  Math
  * is fp32; dx is rounded once, to nearest even; dgamma is an fp32 sum in an
  * order that depends on the sizes alone.  Any finite x is handled, as
- * qknorm_rope.h describes.
+ * qknorm_rope.h describes, as long as the sums of |g| over a head stay in
+ * fp32's range.
  *
  * Pointers are DEVICE pointers owned by the caller; the library allocates,
  * frees and synchronises nothing and work is only enqueued on `stream`.

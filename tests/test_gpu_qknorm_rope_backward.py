@@ -226,3 +226,11 @@ def test_runs_streams_and_graph_replays_give_the_same_bits():
         graph.replay()
         torch.cuda.synchronize()
         assert all(same_bits(a, c) for a, c in zip((*kept, out), want))
+
+
+def test_products_of_large_values_and_gradients():
+    """x of 1e17, whose squares still add up in fp32, times gradients of 1e23,
+    whose products with it do not: dx is about 1e6."""
+    x, do, gam = inputs(7, 20, 4, 128, "bf16")
+    x, do = (x.double() * 1e17).to(x.dtype), (do.double() * 1e24).to(x.dtype)
+    check(x, do, gam, *tables(20, 4, 128, "interleaved", "shared", "fp32"), "interleaved", "shared")
