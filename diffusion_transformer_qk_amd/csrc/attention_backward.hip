@@ -67,6 +67,11 @@ __device__ __forceinline__ int bound_exponent(float bound)
     return __builtin_amdgcn_frexp_expf(bound);
 }
 
+// A row's squared norm, or 0 if it holds an infinity or NaN: such a row is lost
+// whatever scales it, and counted it would leave all others unscaled, those
+// that causality hides from it among them.
+__device__ __forceinline__ float finite(float sq) { return sq <= 0x1.fffffep127f ? sq : 0.0f; }
+
 // Rows of a workgroup of the kernel below: 32 queries a wave, or D / 8 lanes a
 // value, 4 values each.
 constexpr int kStatRows = 128;
@@ -127,7 +132,7 @@ void row_stats_kernel(const BwdParams p)
                 for (int i = 0; i < 8; ++i)
                     sq = __builtin_fmaf(x[i], x[i], sq);
             }
-            top = half_sum(sq);
+            top = finite(half_sum(sq));
         }
     } else if constexpr (F16) {
         constexpr int L = D / 8, R = 256 / L;
@@ -148,7 +153,7 @@ void row_stats_kernel(const BwdParams p)
 #pragma unroll
             for (int w = 1; w < L; w *= 2)
                 sq += __shfl_xor(sq, w);
-            top = fmaxf(top, sq);
+            top = fmaxf(top, finite(sq));
         }
     }
     if constexpr (F16) {

@@ -410,3 +410,28 @@ def test_another_stream_and_graph_replays():
             torch.cuda.synchronize()
             assert all(same_bits(a, b) for a, b in zip(kept, want))
     assert torch.isfinite(by_hand[0]).all()
+
+
+def test_an_infinity_reaches_no_pair_far_from_it_in_fp16():
+    """Under causality an infinite dout row or v row of one position leaves the
+    gradients of pairs 192 or more positions on the hidden side as they are,
+    also where p (dp - delta) lies above fp16's range unless it is scaled."""
+    s, far = 500, 192
+    q, k, v, dout = tensors(44, "fp16", 1, s, s, 2, 2, 64)
+    dout = (dout.float() * 2048).half()
+    out, lse = qkr.attention(q, k, v, causal=True)
+    for at in (0, 130):
+        # query `at` has nothing to do with the keys behind it
+        bad, zero = dout.clone(), dout.clone()
+        bad[:, at], zero[:, at] = math.inf, 0
+        _, dk, dv = qkr.attention_backward(bad, q, k, v, out, lse, causal=True)
+        _, dk0, dv0 = qkr.attention_backward(zero, q, k, v, out, lse, causal=True)
+        assert torch.isfinite(dk0).all()
+        assert same_bits(dk[:, at + far:], dk0[:, at + far:]) and same_bits(dv[:, at + far:], dv0[:, at + far:])
+    for at in (s - 1, s - 140):
+        # key `at` has nothing to do with the queries before it
+        bad, zero = v.clone(), v.clone()
+        bad[:, at], zero[:, at] = -math.inf, 0
+        dq = qkr.attention_backward(dout, q, k, bad, out, lse, causal=True)[0]
+        dq0 = qkr.attention_backward(dout, q, k, zero, out, lse, causal=True)[0]
+        assert torch.isfinite(dq0).all() and same_bits(dq[:, :at - far], dq0[:, :at - far])
