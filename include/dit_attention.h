@@ -34,9 +34,9 @@
  * not depend on the order in which workgroups run (no atomic additions).
  *
  * Keys and values at or past kv_lengths[b] are not read.  A query and a key
- * that causality hides from each other take part in the products with
- * probability 0, so an infinity or NaN in one can reach the other where a tile
- * of 64 queries or keys holds it.
+ * that causality hides from each other may take part in the products with
+ * probability 0, so an infinity or NaN in one can reach the other where the key
+ * lies less than 192 positions behind the last one that the query sees.
  *
  * All pointers are DEVICE pointers owned by the caller.  The library
  * allocates, frees and synchronises nothing and keeps no state between calls.

@@ -435,3 +435,29 @@ def test_an_infinity_reaches_no_pair_far_from_it_in_fp16():
         dq = qkr.attention_backward(dout, q, k, bad, out, lse, causal=True)[0]
         dq0 = qkr.attention_backward(dout, q, k, zero, out, lse, causal=True)[0]
         assert torch.isfinite(dq0).all() and same_bits(dq[:, :at - far], dq0[:, :at - far])
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp16", 64), ("bf16", 128), ("bf16", 256)])
+def test_a_hidden_value_reaches_192_positions_at_most(dtype, d, bad):
+    """A NaN or infinity in a key or query takes part, with p = 0, in the rows
+    of its workgroup and tile that causality hides from it, and in no others."""
+    s, at, far = 700, 350, 192
+    q, k, v, dout = tensors(45, dtype, 1, s, s, 2, 2, d)
+    v[:, at], dout[:, at] = 0, 0            # so that fp16's scaling is the same
+    out, lse = qkr.attention(q, k, v, causal=True)
+    want = qkr.attention_backward(dout, q, k, v, out, lse, causal=True)
+    for name in ("k", "v"):
+        x = dict(k=k.clone(), v=v.clone())
+        x[name][:, at] = bad
+        out2, lse2 = qkr.attention(q, x["k"], x["v"], causal=True)
+        dq = qkr.attention_backward(dout, q, x["k"], x["v"], out, lse, causal=True)[0]
+        n = at - far + 1
+        assert same_bits(out2[:, :n], out[:, :n]) and same_bits(lse2[:, :, :n].contiguous(), lse[:, :, :n].contiguous())
+        assert same_bits(dq[:, :n], want[0][:, :n])
+    for name in ("q", "dout"):
+        x = dict(q=q.clone(), dout=dout.clone())
+        x[name][:, at] = bad
+        _, dk, dv = qkr.attention_backward(x["dout"], x["q"], k, v, out, lse, causal=True)
+        n = at + far
+        assert same_bits(dk[:, n:], want[1][:, n:]) and same_bits(dv[:, n:], want[2][:, n:])
