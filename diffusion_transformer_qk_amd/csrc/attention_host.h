@@ -104,14 +104,68 @@ inline int check_tensor(const dit_attn_args& a, const dit_attn_tensor* t, const 
     return written && overlaps_itself(a, t, e) ? QKR_ERR_ARG : QKR_OK;
 }
 
+// One dimension of two tensors that step through it alike: the stride, and each
+// one's number of steps.
+struct Steps {
+    int64_t stride, x, y;
+};
+
+// Whether, of two tensors whose elements are runs of `width` at the steps of n
+// dimensions (largest stride first), y's first run `ahead` of x's, two runs
+// meet: whether the steps' difference can bring `ahead` within a run.  Along one
+// dimension only a few differences can, unless its stride is far below what the
+// smaller ones cover: then this says yes without looking.
+inline bool runs_meet(int64_t ahead, const Steps* d, int n, int64_t width)
+{
+    if (n == 0)
+        return -width < ahead && ahead < width;
+    int64_t back = width - 1, forth = width - 1;     // what the smaller dimensions can take off or add
+    for (int i = 1; i < n; ++i) {
+        back += d[i].x * d[i].stride;
+        forth += d[i].y * d[i].stride;
+    }
+    // ahead + k stride in [-forth, back], k in [-x, y]
+    const auto floor_div = [](int64_t p, int64_t q) { return p / q - (p % q < 0); };
+    int64_t first = -floor_div(forth + ahead, d->stride), last = floor_div(back - ahead, d->stride);
+    first = first < -d->x ? -d->x : first;
+    last = last > d->y ? d->y : last;
+    if (last - first >= 16)
+        return true;
+    for (int64_t k = first; k <= last; ++k)
+        if (runs_meet(ahead + k * d->stride, d + 1, n - 1, width))
+            return true;
+    return false;
+}
+
 // Whether two tensors may share an element.  Ranges that do not meet settle
-// it; tensors that interleave are told apart where they are slices of one
-// buffer: rows of the same token stride whose columns do not meet, at batch
-// strides that are whole rows.
+// it; of tensors that interleave, slices of one buffer are told apart: those of
+// the same strides whatever their order, and rows of the same token stride whose
+// columns do not meet, at batch strides that are whole rows.
 inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor* x, const Extent& ex,
                      const dit_attn_tensor* y, const Extent& ey)
 {
     if (ex.tokens == 0 || ey.tokens == 0 || !meet(range(a, x, ex), range(a, y, ey)))
+        return false;
+    const int64_t ahead =                                 // both are 16-byte aligned
+        (reinterpret_cast<intptr_t>(y->data) - reinterpret_cast<intptr_t>(x->data)) / 2;
+    const struct { int64_t nx, ny, sx, sy; } dims[] = {
+        {a.batch, a.batch, x->batch_stride, y->batch_stride},
+        {ex.tokens, ey.tokens, x->token_stride, y->token_stride},
+        {ex.heads, ey.heads, x->head_stride, y->head_stride}};
+    Steps steps[3];
+    int n = 0;
+    bool alike = true;
+    for (const auto& d : dims) {
+        const int64_t s = d.nx > 1 ? d.sx : d.sy;
+        alike = alike && (d.nx == 1 || d.ny == 1 || d.sx == d.sy);
+        if (s == 0 || (d.nx == 1 && d.ny == 1))           // a dimension that leads nowhere
+            continue;
+        int i = n++;
+        for (; i > 0 && steps[i - 1].stride < s; --i)
+            steps[i] = steps[i - 1];
+        steps[i] = Steps{s, d.nx - 1, d.ny - 1};
+    }
+    if (alike && !runs_meet(ahead, steps, n, a.head_dim))
         return false;
     const int64_t ts = x->token_stride;
     if (ts != y->token_stride || ts == 0)
@@ -120,11 +174,8 @@ inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor* x, const Ext
         return true;
     const int64_t wx = (ex.heads - 1) * x->head_stride + a.head_dim;
     const int64_t wy = (ey.heads - 1) * y->head_stride + a.head_dim;
-    const intptr_t bytes = reinterpret_cast<intptr_t>(y->data) - reinterpret_cast<intptr_t>(x->data);
-    int64_t ahead = bytes / 2 % ts;                 // y's columns begin here in x's rows
-    if (ahead < 0)
-        ahead += ts;
-    return !(wx <= ahead && ahead + wy <= ts);
+    const int64_t column = ahead % ts < 0 ? ahead % ts + ts : ahead % ts;   // where y's begin in x's rows
+    return !(wx <= column && column + wy <= ts);
 }
 
 // A tensor's pointer and strides as a kernel takes them; one without tokens may

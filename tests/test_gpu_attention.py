@@ -461,3 +461,45 @@ def test_a_hidden_value_reaches_192_positions_at_most(dtype, d, bad):
         _, dk, dv = qkr.attention_backward(x["dout"], x["q"], k, v, out, lse, causal=True)
         n = at + far
         assert same_bits(dk[:, n:], want[1][:, n:]) and same_bits(dv[:, n:], want[2][:, n:])
+
+
+@pytest.mark.parametrize("order", ["sbthd", "bshtd", "btshd", "bthsd", "thbsd"])
+@pytest.mark.parametrize("hk", [4, 2])
+def test_slices_of_buffers_of_any_order(order, hk):
+    """q, k, v and out, and the gradients, as slices of one buffer whose
+    dimensions (batch, sequence, tensor, head, element) stand in any order: the
+    contiguous calls' bits, and every other element as it was."""
+    b, s, h, d = 2, 100, 4, 64
+    size = dict(b=b, s=s, t=5, h=h, d=d)
+
+    def buffer(*values):
+        """A buffer and its four slices, with these values in the first of them."""
+        buf = torch.full([size[c] for c in order], 9.0, dtype=torch.bfloat16, device=DEV)
+        whole = buf.permute([order.index(c) for c in "tbshd"])
+        views = [whole[i, :, :, :n] for i, n in enumerate((h, hk, hk, h))]
+        for view, value in zip(views, values):
+            view.copy_(value)
+        return buf, views
+
+    q, k, v, dout = tensors(41, "bf16", b, s, s, h, hk, d)
+    out, lse = qkr.attention(q, k, v)
+    grads = qkr.attention_backward(dout, q, k, v, out, lse)
+
+    buf, (vq, vk, vv, vo) = buffer(q, k, v)
+    assert same_bits(qkr.attention(vq, vk, vv, out=vo)[1], lse)
+    assert same_bits(buf, buffer(q, k, v, out)[0])
+    for given in ((dout, q, k, v, out), (dout, vq, vk, vv, vo)):
+        buf, (vdq, vdk, vdv, _) = buffer()
+        qkr.attention_backward(*given, lse, dq=vdq, dk=vdk, dv=vdv)
+        assert same_bits(buf, buffer(*grads)[0])
+
+
+def test_gradients_over_the_buffer_they_were_cut_from_are_refused():
+    """dq in the place of q, k's slice one element on, two gradients in one place."""
+    buf = draw(42, 100, 2, 3, 4, 64)
+    q, k, v = buf.permute(2, 1, 0, 3, 4).unbind(0)
+    out, lse = qkr.attention(q, k, v)
+    grads = torch.empty_like(buf).permute(2, 1, 0, 3, 4)
+    for dq, dk in ((q, grads[1]), (grads[0], v), (grads[0], grads[0]), (grads[0], grads[2])):
+        with pytest.raises(qkr.QkrError):
+            qkr.attention_backward(out, q, k, v, out, lse, dq=dq, dk=dk, dv=grads[2])
