@@ -558,9 +558,9 @@ def attention(q, k, v, *, causal: bool = False, kv_lengths=None, scale: float | 
     kv_heads, head_dim] of bfloat16 or float16 (or without the batch dimension
     for one sample); any strides that are multiples of 8 with the last
     dimension contiguous, so the slices of a fused QKV buffer serve as they
-    are.  ``heads`` is a multiple of ``kv_heads``; consecutive query heads
-    share a key head.  ``kv_lengths``: int32 [batch], the keys in use of each
-    sample.  ``causal``: the last query sees the last key of kv_tokens, the
+    are (a dimension of one element may have any stride).  ``heads`` is a
+    multiple of ``kv_heads``; consecutive query heads share a key head.
+    ``kv_lengths``: int32 [batch], the keys in use of each sample.  ``causal``: the last query sees the last key of kv_tokens, the
     one before it one key fewer.  ``scale`` defaults to head_dim ** -0.5.
     ``out`` (like q, same rules for strides) and ``lse`` (float32 [batch,
     heads, tokens], the log of each row's sum of exponentials, which the

@@ -740,8 +740,9 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     if (a.batch == 0 || (a.q_tokens == 0 && a.kv_tokens == 0))
         return QKR_OK;
     const Extent eq = {a.q_tokens, a.heads}, ekv = {a.kv_tokens, a.kv_heads};
-    const struct { const dit_attn_tensor* t; Extent e; } all[] = {
-        {dout, eq}, {q, eq}, {k, ekv}, {v, ekv}, {out, eq}, {dq, eq}, {dk, ekv}, {dv, ekv}};
+    const struct { dit_attn_tensor t; Extent e; } all[] = {
+        {plain(a, dout, eq), eq}, {plain(a, q, eq), eq}, {plain(a, k, ekv), ekv}, {plain(a, v, ekv), ekv},
+        {plain(a, out, eq), eq}, {plain(a, dq, eq), eq}, {plain(a, dk, ekv), ekv}, {plain(a, dv, ekv), ekv}};
     for (int i = 0; i < 8; ++i)
         if ((rc = check_tensor(a, all[i].t, all[i].e, i >= 5)))
             return rc;
@@ -773,14 +774,14 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     }
 
     BwdParams p = {};
-    unpack(a, dout, eq, p.dout, p.do_bs, p.do_ts, p.do_hs);
-    unpack(a, q, eq, p.q, p.q_bs, p.q_ts, p.q_hs);
-    unpack(a, k, ekv, p.k, p.k_bs, p.k_ts, p.k_hs);
-    unpack(a, v, ekv, p.v, p.v_bs, p.v_ts, p.v_hs);
-    unpack(a, out, eq, p.out, p.o_bs, p.o_ts, p.o_hs);
-    unpack(a, dq, eq, p.dq, p.dq_bs, p.dq_ts, p.dq_hs);
-    unpack(a, dk, ekv, p.dk, p.dk_bs, p.dk_ts, p.dk_hs);
-    unpack(a, dv, ekv, p.dv, p.dv_bs, p.dv_ts, p.dv_hs);
+    unpack(all[0].t, p.dout, p.do_bs, p.do_ts, p.do_hs);
+    unpack(all[1].t, p.q, p.q_bs, p.q_ts, p.q_hs);
+    unpack(all[2].t, p.k, p.k_bs, p.k_ts, p.k_hs);
+    unpack(all[3].t, p.v, p.v_bs, p.v_ts, p.v_hs);
+    unpack(all[4].t, p.out, p.o_bs, p.o_ts, p.o_hs);
+    unpack(all[5].t, p.dq, p.dq_bs, p.dq_ts, p.dq_hs);
+    unpack(all[6].t, p.dk, p.dk_bs, p.dk_ts, p.dk_hs);
+    unpack(all[7].t, p.dv, p.dv_bs, p.dv_ts, p.dv_hs);
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
     p.batch = a.batch;

@@ -389,8 +389,10 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
     if (a.batch == 0 || a.q_tokens == 0)
         return QKR_OK;
     const Extent eq = {a.q_tokens, a.heads}, ekv = {a.kv_tokens, a.kv_heads};
-    if ((rc = check_tensor(a, q, eq, false)) || (rc = check_tensor(a, k, ekv, false)) ||
-        (rc = check_tensor(a, v, ekv, false)) || (rc = check_tensor(a, out, eq, true)))
+    const dit_attn_tensor tq = plain(a, q, eq), tk = plain(a, k, ekv), tv = plain(a, v, ekv),
+                          to = plain(a, out, eq);
+    if ((rc = check_tensor(a, tq, eq, false)) || (rc = check_tensor(a, tk, ekv, false)) ||
+        (rc = check_tensor(a, tv, ekv, false)) || (rc = check_tensor(a, to, eq, true)))
         return rc;
     const uint64_t lse_bytes = (uint64_t)a.batch * a.heads * a.q_tokens * 4;
     if (!lse)
@@ -404,21 +406,21 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
         return QKR_ERR_ALIGN;
     const Range lse_r = {lse, lse_bytes}, ws_r = {workspace, (uint64_t)need};
     const Range len_r = {a.kv_lengths, a.kv_lengths ? (uint64_t)a.batch * 4 : 0};
-    const Range in[] = {range(a, q, eq), range(a, k, ekv), range(a, v, ekv), len_r};
-    const Range o = range(a, out, eq);
+    const Range in[] = {range(a, tq, eq), range(a, tk, ekv), range(a, tv, ekv), len_r};
+    const Range o = range(a, to, eq);
     for (const Range& x : in)
         if (meet(x, lse_r) || meet(x, ws_r))
             return QKR_ERR_ARG;
     if (meet(o, lse_r) || meet(o, ws_r) || meet(lse_r, ws_r) || meet(o, len_r) ||
-        may_meet(a, out, eq, q, eq) || may_meet(a, out, eq, k, ekv) || may_meet(a, out, eq, v, ekv))
+        may_meet(a, to, eq, tq, eq) || may_meet(a, to, eq, tk, ekv) || may_meet(a, to, eq, tv, ekv))
         return QKR_ERR_ARG;
 
     const Shape s = shape_of(a);
     FwdParams p = {};
-    unpack(a, q, eq, p.q, p.q_bs, p.q_ts, p.q_hs);
-    unpack(a, k, ekv, p.k, p.k_bs, p.k_ts, p.k_hs);
-    unpack(a, v, ekv, p.v, p.v_bs, p.v_ts, p.v_hs);
-    unpack(a, out, eq, p.out, p.o_bs, p.o_ts, p.o_hs);
+    unpack(tq, p.q, p.q_bs, p.q_ts, p.q_hs);
+    unpack(tk, p.k, p.k_bs, p.k_ts, p.k_hs);
+    unpack(tv, p.v, p.v_bs, p.v_ts, p.v_hs);
+    unpack(to, p.out, p.o_bs, p.o_ts, p.o_hs);
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
     p.q_tokens = (int32_t)a.q_tokens;

@@ -46,28 +46,45 @@ inline int check_args(const dit_attn_args* a)
     return QKR_OK;
 }
 
+// A call's tensor as the checks and kernels take it: the strides of dimensions
+// of one element, which may be anything, replaced by some that fit (0, and for a
+// token at least head_dim: what kernels stage past the last token lies outside
+// the buffer's range, and reads as zero, only if its rows are a row apart).  One
+// without tokens may be NULL.
+inline dit_attn_tensor plain(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e)
+{
+    dit_attn_tensor p = t ? *t : dit_attn_tensor{};
+    if (a.batch == 1)
+        p.batch_stride = 0;
+    if (e.tokens <= 1)
+        p.token_stride = a.head_dim;
+    if (e.heads == 1)
+        p.head_stride = 0;
+    return p;
+}
+
 // Elements from the first to one past the last of a tensor.
-inline uint64_t span(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e)
+inline uint64_t span(const dit_attn_args& a, const dit_attn_tensor& t, const Extent& e)
 {
     if (e.tokens == 0)
         return 0;
-    return (uint64_t)(a.batch - 1) * t->batch_stride + (uint64_t)(e.tokens - 1) * t->token_stride +
-           (uint64_t)(e.heads - 1) * t->head_stride + a.head_dim;
+    return (uint64_t)(a.batch - 1) * t.batch_stride + (uint64_t)(e.tokens - 1) * t.token_stride +
+           (uint64_t)(e.heads - 1) * t.head_stride + a.head_dim;
 }
 
-inline Range range(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e)
+inline Range range(const dit_attn_args& a, const dit_attn_tensor& t, const Extent& e)
 {
-    return e.tokens ? Range{t->data, span(a, t, e) * 2} : Range{nullptr, 0};
+    return e.tokens ? Range{t.data, span(a, t, e) * 2} : Range{nullptr, 0};
 }
 
 inline bool meet(const Range& x, const Range& y) { return qkr_host::overlaps(x.at, x.bytes, y.at, y.bytes); }
 
 // Whether two elements of the tensor share memory, or may: each dimension,
 // smallest stride first, has to step past all that the smaller ones cover.
-inline bool overlaps_itself(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e)
+inline bool overlaps_itself(const dit_attn_args& a, const dit_attn_tensor& t, const Extent& e)
 {
-    struct { int64_t n, s; } dim[3] = {{a.batch, t->batch_stride}, {e.tokens, t->token_stride},
-                                       {e.heads, t->head_stride}};
+    struct { int64_t n, s; } dim[3] = {{a.batch, t.batch_stride}, {e.tokens, t.token_stride},
+                                       {e.heads, t.head_stride}};
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 2 - i; ++j)
             if (dim[j].s > dim[j + 1].s) {
@@ -85,21 +102,21 @@ inline bool overlaps_itself(const dit_attn_args& a, const dit_attn_tensor* t, co
     return false;
 }
 
-inline int check_tensor(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e, bool written)
+inline int check_tensor(const dit_attn_args& a, const dit_attn_tensor& t, const Extent& e, bool written)
 {
     if (e.tokens == 0)
         return QKR_OK;
-    if (!t || !t->data)
+    if (!t.data)
         return QKR_ERR_NULL;
-    if (!qkr_host::aligned16(t->data) || t->batch_stride % 8 || t->token_stride % 8 ||
-        t->head_stride % 8)
+    if (!qkr_host::aligned16(t.data) || t.batch_stride % 8 || t.token_stride % 8 ||
+        t.head_stride % 8)
         return QKR_ERR_ALIGN;
     // more than the card holds, and batch * heads < 2^23 (check_args) keeps a
     // span in bytes inside 64 bits
     constexpr int64_t kMax = (int64_t)1 << 38;
-    if (t->batch_stride < 0 || t->token_stride < 0 || t->head_stride < 0 || t->batch_stride > kMax ||
-        t->head_stride > kMax || t->token_stride > DIT_ATTN_MAX_TOKEN_STRIDE ||
-        (e.tokens > 1 && t->token_stride < a.head_dim))
+    if (t.batch_stride < 0 || t.token_stride < 0 || t.head_stride < 0 || t.batch_stride > kMax ||
+        t.head_stride > kMax || t.token_stride > DIT_ATTN_MAX_TOKEN_STRIDE ||
+        t.token_stride < a.head_dim)
         return QKR_ERR_SHAPE;
     return written && overlaps_itself(a, t, e) ? QKR_ERR_ARG : QKR_OK;
 }
@@ -141,17 +158,17 @@ inline bool runs_meet(int64_t ahead, const Steps* d, int n, int64_t width)
 // it; of tensors that interleave, slices of one buffer are told apart: those of
 // the same strides whatever their order, and rows of the same token stride whose
 // columns do not meet, at batch strides that are whole rows.
-inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor* x, const Extent& ex,
-                     const dit_attn_tensor* y, const Extent& ey)
+inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor& x, const Extent& ex,
+                     const dit_attn_tensor& y, const Extent& ey)
 {
     if (ex.tokens == 0 || ey.tokens == 0 || !meet(range(a, x, ex), range(a, y, ey)))
         return false;
     const int64_t ahead =                                 // both are 16-byte aligned
-        (reinterpret_cast<intptr_t>(y->data) - reinterpret_cast<intptr_t>(x->data)) / 2;
+        (reinterpret_cast<intptr_t>(y.data) - reinterpret_cast<intptr_t>(x.data)) / 2;
     const struct { int64_t nx, ny, sx, sy; } dims[] = {
-        {a.batch, a.batch, x->batch_stride, y->batch_stride},
-        {ex.tokens, ey.tokens, x->token_stride, y->token_stride},
-        {ex.heads, ey.heads, x->head_stride, y->head_stride}};
+        {a.batch, a.batch, x.batch_stride, y.batch_stride},
+        {ex.tokens, ey.tokens, x.token_stride, y.token_stride},
+        {ex.heads, ey.heads, x.head_stride, y.head_stride}};
     Steps steps[3];
     int n = 0;
     bool alike = true;
@@ -167,31 +184,25 @@ inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor* x, const Ext
     }
     if (alike && !runs_meet(ahead, steps, n, a.head_dim))
         return false;
-    const int64_t ts = x->token_stride;
-    if (ts != y->token_stride || ts == 0)
+    const int64_t ts = x.token_stride;
+    if (ts != y.token_stride || ts == 0)
         return true;
-    if (a.batch > 1 && (x->batch_stride % ts || y->batch_stride % ts))
+    if (a.batch > 1 && (x.batch_stride % ts || y.batch_stride % ts))
         return true;
-    const int64_t wx = (ex.heads - 1) * x->head_stride + a.head_dim;
-    const int64_t wy = (ey.heads - 1) * y->head_stride + a.head_dim;
+    const int64_t wx = (ex.heads - 1) * x.head_stride + a.head_dim;
+    const int64_t wy = (ey.heads - 1) * y.head_stride + a.head_dim;
     const int64_t column = ahead % ts < 0 ? ahead % ts + ts : ahead % ts;   // where y's begin in x's rows
     return !(wx <= column && column + wy <= ts);
 }
 
-// A tensor's pointer and strides as a kernel takes them; one without tokens may
-// be NULL.  The token stride of one token may be anything, but the kernels count
-// on at least head_dim: what they stage past the last token lies outside the
-// buffer's range, and reads as zero, only if its rows are a row apart.
+// A tensor's pointer and strides as a kernel takes them.
 template <typename T>
-inline void unpack(const dit_attn_args& a, const dit_attn_tensor* t, const Extent& e, T*& at, int64_t& bs,
-                   int64_t& ts, int64_t& hs)
+inline void unpack(const dit_attn_tensor& t, T*& at, int64_t& bs, int64_t& ts, int64_t& hs)
 {
-    if (!t)
-        return;
-    at = static_cast<T*>(t->data);
-    bs = t->batch_stride;
-    ts = e.tokens > 1 ? t->token_stride : a.head_dim;
-    hs = t->head_stride;
+    at = static_cast<T*>(t.data);
+    bs = t.batch_stride;
+    ts = t.token_stride;
+    hs = t.head_stride;
 }
 
 }  // namespace qkr_attn_host

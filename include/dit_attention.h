@@ -57,10 +57,10 @@ extern "C" {
  * data + b * batch_stride + t * token_stride + h * head_stride + d (strides in
  * elements).  The slices of a fused [batch, tokens, 3 * heads * head_dim]
  * buffer are such tensors.  data must be 16-byte aligned, the strides
- * multiples of 8 and not negative, token_stride at least head_dim (where
- * tokens > 1) and at most DIT_ATTN_MAX_TOKEN_STRIDE.  Elements of an output
- * must not share memory; a batch or head stride of an input may be 0.  A tensor
- * of 0 tokens is not looked at and may be NULL. */
+ * multiples of 8 and not negative, token_stride at least head_dim and at most
+ * DIT_ATTN_MAX_TOKEN_STRIDE; the stride of a dimension of one element may be
+ * anything.  Elements of an output must not share memory; a batch or head stride
+ * of an input may be 0.  A tensor of 0 tokens is not looked at and may be NULL. */
 typedef struct {
     void* data;
     int64_t batch_stride, token_stride, head_stride;

@@ -39,7 +39,7 @@ bool share(const std::set<int64_t>& x, const std::set<int64_t>& y)
 bool said(const dit_attn_args& a, const dit_attn_tensor& x, const Extent& ex, const dit_attn_tensor& y,
           const Extent& ey)
 {
-    return qkr_attn_host::may_meet(a, &x, ex, &y, ey);
+    return qkr_attn_host::may_meet(a, qkr_attn_host::plain(a, &x, ex), ex, qkr_attn_host::plain(a, &y, ey), ey);
 }
 
 int wrong(const char* what, const dit_attn_args& a, const dit_attn_tensor& x, const Extent& ex,
@@ -91,7 +91,7 @@ int main()
         ++(meet ? joined : apart);
     }
 
-    // any strides, zeros and ones that fold onto themselves among them: never
+    // any strides (odd and negative ones of single elements too), zeros and ones that fold onto themselves among them: never
     // apart where they share
     for (int n = 0; n < 40000; ++n) {
         dit_attn_args a = {};
@@ -105,6 +105,14 @@ int main()
             t[i] = dit_attn_tensor{kAt + 16 * below(200), 8 * below(80), kDim + 8 * below(60), 8 * below(40)};
             if (i && alike)
                 t[1] = dit_attn_tensor{t[1].data, t[0].batch_stride, t[0].token_stride, t[0].head_stride};
+        }
+        for (int i = 0; i < 2; ++i) {
+            if (a.batch == 1 && below(2))
+                t[i].batch_stride = -3;
+            if (e[i].tokens == 1 && below(2))
+                t[i].token_stride = 5242881;
+            if (e[i].heads == 1 && below(2))
+                t[i].head_stride = INT64_MIN;
         }
         const bool meet = share(runs(a, t[0], e[0]), runs(a, t[1], e[1]));
         if (meet && (!said(a, t[0], e[0], t[1], e[1]) || !said(a, t[1], e[1], t[0], e[0])))

@@ -271,3 +271,20 @@ def test_the_main_library_brings_the_attention_library_along():
                            check=True).stdout
     assert "getenv" not in names
     assert ctypes.CDLL(qkr.LIB_PATH).dit_attention
+
+
+def test_strides_of_a_dimension_of_one_do_not_count():
+    """They get past the checks of the layouts (to the overlap of q and out)."""
+    a = args(batch=1, q_tokens=1, kv_tokens=1, heads=1, kv_heads=1)
+    for stride in (3, -8, 1 << 40, (1 << 22) + 8):
+        over = dict(batch_stride=stride, token_stride=stride, head_stride=stride)
+        t = [tensor(A + i * FAR, 1, 1, **over) for i in range(9)]
+        assert forward(a, q=t[0], k=t[1], v=t[2], out=t[0]) == b.QKR_ERR_ARG
+        assert forward(a, q=t[0], k=t[1], v=t[2], out=t[3], lse=A + 3 * FAR) == b.QKR_ERR_ARG
+        assert backward(a, dout=t[0], q=t[1], k=t[2], v=t[3], out=t[4], dq=t[5], dk=t[6], dv=t[6]) == b.QKR_ERR_ARG
+        assert backward(a, dq=tensor(A, 1, 1, batch_stride=1, token_stride=stride, head_stride=stride,
+                                     data=A + 5 * FAR + 8)) == b.QKR_ERR_ALIGN
+    # and of more than one they do
+    two = args(batch=1, q_tokens=2, kv_tokens=1, heads=1, kv_heads=1)
+    assert forward(two, q=tensor(A, 2, 1, token_stride=3)) == b.QKR_ERR_ALIGN
+    assert forward(two, q=tensor(A, 2, 1, token_stride=(1 << 22) + 8)) == b.QKR_ERR_SHAPE

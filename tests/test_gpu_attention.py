@@ -503,3 +503,20 @@ def test_gradients_over_the_buffer_they_were_cut_from_are_refused():
     for dq, dk in ((q, grads[1]), (grads[0], v), (grads[0], grads[0]), (grads[0], grads[2])):
         with pytest.raises(qkr.QkrError):
             qkr.attention_backward(out, q, k, v, out, lse, dq=dq, dk=dk, dv=grads[2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_strides_of_a_dimension_of_one_do_not_count(dtype):
+    """One token, one sample and one head of strides that nothing steps over
+    (above the limits, negative in C, odd) give the contiguous call's bits."""
+    for batch, sq, sk, h, hk in ((2, 1, 70, 4, 2), (1, 70, 1, 2, 2), (1, 1, 1, 1, 1), (1, 40, 70, 3, 1)):
+        x = tensors(43, dtype, batch, sq, sk, h, hk, 128)
+        out, lse = qkr.attention(*x[:3])
+        want = qkr.attention_backward(x[3], *x[:3], out, lse)
+        for stride in (5242880, 3, 1 << 39):
+            odd = [t.as_strided(t.shape, [stride if n == 1 else st for n, st in zip(t.shape, t.stride())])
+                   for t in (*x, torch.empty_like(out), *map(torch.empty_like, want))]
+            out2, lse2 = qkr.attention(*odd[:3], out=odd[4])
+            assert same_bits(out, out2.contiguous()) and same_bits(lse, lse2)
+            got = qkr.attention_backward(odd[3], *odd[:3], odd[4], lse, dq=odd[5], dk=odd[6], dv=odd[7])
+            assert all(same_bits(a, b.contiguous()) for a, b in zip(want, got))
