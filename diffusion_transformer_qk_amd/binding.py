@@ -705,12 +705,14 @@ def _norm_backward(dy, x, weight, form, rows, hidden, rows_per_batch, params_sha
     return out, dweight, dbias
 
 
-def layer_norm_backward(dy, x, weight=None, *, out=None, eps: float = 1e-6, workspace=None,
-                        stream=None):
+def layer_norm_backward(dy, x, weight=None, *, out=None, eps: float = 1e-6,
+                        param_grads: bool | None = None, workspace=None, stream=None):
     """Backward pass of ``layer_norm``; returns ``(dx, dweight, dbias)``.
 
     ``dy``: the gradient of its output, ``x``: its input.  ``dweight`` and
-    ``dbias`` are float32 [hidden], and None where ``weight`` is None.
+    ``dbias`` are float32 [hidden], or None without ``param_grads``, which
+    defaults to whether there is a ``weight``: pass True for the gradient of a
+    bias alone, False where the weight gets none.
     ``out`` receives dx (a new tensor by default); ``out=dy`` works in place.
     ``workspace``: at least ``layer_norm_backward_workspace_size`` bytes;
     allocated here on the launch stream when None and needed.
@@ -719,8 +721,10 @@ def layer_norm_backward(dy, x, weight=None, *, out=None, eps: float = 1e-6, work
     if weight is not None and weight.shape != (hidden,):
         raise ValueError("weight must be [%d]" % hidden)
     rows = x.numel() // hidden if hidden else 0
+    if param_grads is None:
+        param_grads = weight is not None
     return _norm_backward(dy, x, weight, DIT_LN_WEIGHT, rows, hidden, max(1, rows),
-                          None if weight is None else hidden, out, eps, workspace, stream)
+                          hidden if param_grads else None, out, eps, workspace, stream)
 
 
 def fuse_scale_shift_backward(dy, x, scale, *, out=None, eps: float = 1e-6,

@@ -348,3 +348,16 @@ def test_products_of_large_values_and_gradients():
         dy = rows_of(39, 12, hidden, "bf16", 1e22)
         w = params_of(40, (hidden,), "fp32")[0]
         check_backward(dy, x, w[None], 0.0, 12, qkr.layer_norm_backward(dy, x, w))
+
+
+@pytest.mark.parametrize("rows,hidden", [(50, 1200), (3, 64), (2000, 512)])
+def test_sums_are_to_be_had_without_a_weight(rows, hidden):
+    """A layer norm with a bias alone has a bias gradient: the weight of ones' bits."""
+    x, dy = rows_of(6, rows, hidden, "bf16"), rows_of(7, rows, hidden, "bf16")
+    ones = torch.ones(hidden, device=DEV)
+    want = qkr.layer_norm_backward(dy, x, ones)
+    got = qkr.layer_norm_backward(dy, x, param_grads=True)
+    check_backward(dy, x, ones[None], 0.0, rows, got)
+    assert all(same_bits(a, b) for a, b in zip(got, want))
+    dx, dw, db = qkr.layer_norm_backward(dy, x, ones, param_grads=False)
+    assert same_bits(dx, want[0]) and dw is None and db is None
