@@ -185,13 +185,13 @@ def _torch():
     return _torch_module
 
 
-def _x_code(t) -> int:
+def _x_code(t, names: str = "q/k/qkv") -> int:
     torch = _torch()
     if t.dtype == torch.bfloat16:
         return QKR_BF16
     if t.dtype == torch.float16:
         return QKR_FP16
-    raise ValueError("q/k/qkv must be bfloat16 or float16, got %s" % t.dtype)
+    raise ValueError("%s must be bfloat16 or float16, got %s" % (names, t.dtype))
 
 
 def _table_code(t) -> int:
@@ -349,7 +349,7 @@ def dit_fuse_scale_shift_raw(x: int, y: int, rows: int, hidden: int, rows_per_ba
                                         stream or None))
 
 
-def _mod_code(t) -> int:
+def _mod_code(t, names: str = "scale/shift") -> int:
     torch = _torch()
     dtype = t.dtype
     if dtype == torch.float32:
@@ -358,7 +358,7 @@ def _mod_code(t) -> int:
         return QKR_BF16
     if dtype == torch.float16:
         return QKR_FP16
-    raise ValueError("scale/shift must be bfloat16, float16 or float32, got %s" % dtype)
+    raise ValueError("%s must be bfloat16, float16 or float32, got %s" % (names, dtype))
 
 
 def fuse_scale_shift(x, scale, shift, *, out=None, eps: float = 1e-6,
@@ -394,7 +394,7 @@ def fuse_scale_shift(x, scale, shift, *, out=None, eps: float = 1e-6,
     with ctx:
         status = dit_fuse_scale_shift_raw(_ptr(x), _ptr(out), rows, hidden, rows_per_batch,
                                           _ptr(scale), _ptr(shift), _mod_code(scale), float(eps),
-                                          _x_code(x), stream_ptr)
+                                          _x_code(x, "x"), stream_ptr)
     _check(status)
     return out
 
@@ -475,8 +475,8 @@ def group_norm_silu(x, gamma, beta, groups: int, *, out=None, eps: float = 1e-6,
     ctx, stream_ptr = _call_context(x, (out, gamma, beta, workspace), stream)
     with ctx:
         status = dit_group_norm_silu_raw(_ptr(x), _ptr(out), n, channels, spatial, groups,
-                                         _ptr(gamma), _ptr(beta), _mod_code(gamma), float(eps),
-                                         _x_code(x), _ptr(workspace), ws_bytes, stream_ptr)
+                                         _ptr(gamma), _ptr(beta), _mod_code(gamma, "gamma/beta"),
+                                         float(eps), _x_code(x, "x"), _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return out
 
@@ -514,7 +514,7 @@ def _attn_args(q, k, v, causal, kv_lengths, scale) -> AttnArgs:
     if kv_lengths is not None and (kv_lengths.dtype != torch.int32 or kv_lengths.shape != (batch,)):
         raise ValueError("kv_lengths must be int32 [batch]")
     return AttnArgs(batch, q_tokens, kv_shape[1], heads, kv_heads, head_dim, 1 if causal else 0,
-                    _x_code(q), head_dim ** -0.5 if scale is None else scale,
+                    _x_code(q, "q/k/v"), head_dim ** -0.5 if scale is None else scale,
                     None if kv_lengths is None else _ptr(kv_lengths))
 
 
@@ -560,8 +560,9 @@ def attention(q, k, v, *, causal: bool = False, kv_lengths=None, scale: float | 
     dimension contiguous, so the slices of a fused QKV buffer serve as they
     are (a dimension of one element may have any stride).  ``heads`` is a
     multiple of ``kv_heads``; consecutive query heads share a key head.
-    ``kv_lengths``: int32 [batch], the keys in use of each sample.  ``causal``: the last query sees the last key of kv_tokens, the
-    one before it one key fewer.  ``scale`` defaults to head_dim ** -0.5.
+    ``kv_lengths``: int32 [batch], the keys in use of each sample.
+    ``causal``: the last query sees the last key of kv_tokens, the one before
+    it one key fewer.  ``scale`` defaults to head_dim ** -0.5.
     ``out`` (like q, same rules for strides) and ``lse`` (float32 [batch,
     heads, tokens], the log of each row's sum of exponentials, which the
     backward pass takes) default to new tensors.  ``workspace``: a device
@@ -656,8 +657,8 @@ def layer_norm(x, weight=None, bias=None, *, out=None, eps: float = 1e-6, stream
     with ctx:
         status = load_library().dit_layer_norm(
             _ptr(x), _ptr(out), rows, hidden, _ptr(weight),
-            _ptr(bias), QKR_FP32 if one is None else _mod_code(one), float(eps), _x_code(x),
-            stream_ptr)
+            _ptr(bias), QKR_FP32 if one is None else _mod_code(one, "weight/bias"), float(eps),
+            _x_code(x, "x"), stream_ptr)
     _check(status)
     return out
 
@@ -699,8 +700,8 @@ def _norm_backward(dy, x, weight, form, rows, hidden, rows_per_batch, params_sha
     with ctx:
         status = lib.dit_layer_norm_backward(
             _ptr(dy), _ptr(x), _ptr(out), rows, hidden, rows_per_batch, _ptr(weight), form,
-            QKR_FP32 if weight is None else _mod_code(weight), _ptr(dweight), _ptr(dbias),
-            float(eps), _x_code(x), _ptr(workspace), ws_bytes, stream_ptr)
+            QKR_FP32 if weight is None else _mod_code(weight, "scale" if form else "weight"),
+            _ptr(dweight), _ptr(dbias), float(eps), _x_code(x, "x"), _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return out, dweight, dbias
 

@@ -361,3 +361,17 @@ def test_sums_are_to_be_had_without_a_weight(rows, hidden):
     assert all(same_bits(a, b) for a, b in zip(got, want))
     dx, dw, db = qkr.layer_norm_backward(dy, x, ones, param_grads=False)
     assert same_bits(dx, want[0]) and dw is None and db is None
+
+
+def test_errors_name_the_tensor_of_the_wrong_type():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(64, device=DEV)
+    for call, names in ((lambda: qkr.layer_norm(x, w.double()), "^weight/bias must"),
+                        (lambda: qkr.layer_norm(x, None, w.int()), "^weight/bias must"),
+                        (lambda: qkr.layer_norm(x.float(), w), "^x must"),
+                        (lambda: qkr.layer_norm_backward(x, x, w.double()), "^weight must"),
+                        (lambda: qkr.layer_norm_backward(x.float(), x.float(), w), "^x must"),
+                        (lambda: qkr.fuse_scale_shift_backward(x, x, w.double()), "^scale must"),
+                        (lambda: qkr.attention(*[x.float().view(1, 1, 4, 64)] * 3), "^q/k/v must")):
+        with pytest.raises(ValueError, match=names):
+            call()
