@@ -216,38 +216,35 @@ struct Stager {
         const u32x4 rsrc = {scalar((uint32_t)a), scalar((uint32_t)(a >> 32) & 0xffffu),
                             scalar((uint32_t)bytes), kRawBuffer};
         const uint32_t to = lds + (group >> 1) * block_bytes<D>() + (group & 1) * 1024;
-        dma16<0>(rsrc, off, to);
-        dma16<1>(rsrc, off, to);
-        if constexpr (D > 64) {
-            dma16<2>(rsrc, off, to);
-            dma16<3>(rsrc, off, to);
-        }
-        if constexpr (D > 128) {
-            dma16<4>(rsrc, off, to);
-            dma16<5>(rsrc, off, to);
-            dma16<6>(rsrc, off, to);
-            dma16<7>(rsrc, off, to);
-        }
+        dma_row_group(rsrc, off, to);
     }
 
-    // 64 x 16 bytes of slab C, from buffer offsets off + 64 C to LDS at `to` +
-    // C * kSlab + lane * 16 (the instruction's offset counts in both).
-    // Written in assembly because the compiler, which cannot tell the halves
-    // of a double buffer apart, would wait for these loads before the next LDS
-    // read; wait_staged() waits for them.  The no-ops are the wait states
-    // after a scalar register written by the vector unit (a new resource) and
-    // after m0.
-    template <int C>
-    static __device__ __forceinline__ void dma16(u32x4 rsrc, uint32_t off, uint32_t to)
+    // 64 x 16 bytes of each slab c, from buffer offsets off + 64 c to LDS at `to` +
+    // c * kSlab + lane * 16 (the instruction's offset counts in both, so m0 moves
+    // by the rest).  Written in assembly because the compiler, which cannot tell
+    // the halves of a double buffer apart, would wait for these loads before the
+    // next LDS read; wait_staged() waits for them.  The no-ops are the wait states
+    // after a scalar register written by the vector unit (a resource just formed,
+    // or fetched back from a lane in which the compiler kept it) and after m0.
+    // All slabs are one block of assembly: between two, the compiler might fetch
+    // a part of the resource back and would not know what the next one waits for.
+    static __device__ __forceinline__ void dma_row_group(u32x4 rsrc, uint32_t off, uint32_t to)
     {
-        const uint32_t m0 = scalar(to + C * (kSlab - 64));
-        if constexpr (C == 0)
-            __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                             : : "v"(off), "s"(rsrc), "s"(m0) : "memory");
+#define QKR_FIRST_SLAB "s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+#define QKR_NEXT_SLAB(offset) \
+    "\n\ts_add_u32 m0, m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen offset:" #offset " lds"
+#define QKR_SLABS(text) \
+    __asm__ volatile(text : : "v"(off), "s"(rsrc), "s"(scalar(to)), "i"(kSlab - 64) : "memory", "scc")
+        if constexpr (D == 64)
+            QKR_SLABS(QKR_FIRST_SLAB QKR_NEXT_SLAB(64));
+        else if constexpr (D == 128)
+            QKR_SLABS(QKR_FIRST_SLAB QKR_NEXT_SLAB(64) QKR_NEXT_SLAB(128) QKR_NEXT_SLAB(192));
         else
-            __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\t"
-                             "buffer_load_dwordx4 %0, %1, 0 offen offset:%3 lds"
-                             : : "v"(off), "s"(rsrc), "s"(m0), "i"(64 * C) : "memory");
+            QKR_SLABS(QKR_FIRST_SLAB QKR_NEXT_SLAB(64) QKR_NEXT_SLAB(128) QKR_NEXT_SLAB(192)
+                      QKR_NEXT_SLAB(256) QKR_NEXT_SLAB(320) QKR_NEXT_SLAB(384) QKR_NEXT_SLAB(448));
+#undef QKR_SLABS
+#undef QKR_NEXT_SLAB
+#undef QKR_FIRST_SLAB
     }
 };
 
