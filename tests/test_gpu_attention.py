@@ -520,3 +520,16 @@ def test_strides_of_a_dimension_of_one_do_not_count(dtype):
             assert same_bits(out, out2.contiguous()) and same_bits(lse, lse2)
             got = qkr.attention_backward(odd[3], *odd[:3], odd[4], lse, dq=odd[5], dk=odd[6], dv=odd[7])
             assert all(same_bits(a, b.contiguous()) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp16", 128), ("bf16", 256)])
+def test_keys_cut_for_dq_beside_whole_runs_of_queries(dtype, d):
+    """Few causal queries over many keys of many heads: dq's keys are cut into
+    runs that its masks leave uneven, dk's and dv's queries are not cut."""
+    check(*tensors(46, dtype, 1, 100, 3000, 12, 12, d), causal=True)
+    check(*tensors(47, dtype, 2, 130, 2100, 12, 6, d), causal=True, lengths=[2100, 1500])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_more_than_6000_tokens(causal):
+    check(*tensors(48, "bf16", 1, 6200, 6200, 2, 1, 64), causal=causal)

@@ -375,3 +375,26 @@ def test_errors_name_the_tensor_of_the_wrong_type():
                         (lambda: qkr.attention(*[x.float().view(1, 1, 4, 64)] * 3), "^q/k/v must")):
         with pytest.raises(ValueError, match=names):
             call()
+
+
+def test_rows_past_4_gib():
+    """x, dy and dx of more than 2^32 bytes: rows at either end and around the
+    border have a small call's bits, and the sums hold every row (512 rows of a
+    chunk one after another, then its chunks in 16 runs: 600 additions)."""
+    rows, hidden = 262500, 8192
+    g = torch.Generator(device=DEV).manual_seed(41)
+    x = torch.randn((rows, hidden), generator=g, device=DEV, dtype=torch.bfloat16)
+    dy = torch.randn((rows, hidden), generator=g, device=DEV, dtype=torch.bfloat16)
+    w, b = params_of(42, (hidden,), "fp32")
+    some = torch.tensor([0, 1, 262143, 262144, 262145, rows - 2, rows - 1], device=DEV)
+    assert same_bits(qkr.layer_norm(x, w, b)[some], qkr.layer_norm(x[some], w, b))
+    dx, dw, db = qkr.layer_norm_backward(dy, x, w)
+    assert same_bits(dx[some], qkr.layer_norm_backward(dy[some], x[some], w)[0])
+    del dx
+    sums = [torch.zeros(hidden, dtype=torch.float64, device=DEV) for _ in range(4)]
+    for at in range(0, rows, 8192):
+        n, _, e_n = normalised(x[at:at + 8192])
+        d = dy[at:at + 8192].double()
+        for s, v in zip(sums, (d * n, d, (d * n).abs() * 600 * F + d.abs() * e_n, d.abs() * 600 * F)):
+            s += v.sum(0)
+    assert ((dw.double() - sums[0]).abs() <= sums[2]).all() and ((db.double() - sums[1]).abs() <= sums[3]).all()

@@ -234,3 +234,34 @@ def test_products_of_large_values_and_gradients():
     x, do, gam = inputs(7, 20, 4, 128, "bf16")
     x, do = (x.double() * 1e17).to(x.dtype), (do.double() * 1e24).to(x.dtype)
     check(x, do, gam, *tables(20, 4, 128, "interleaved", "shared", "fp32"), "interleaved", "shared")
+
+
+def test_tokens_past_4_gib():
+    """A fused buffer of more than 2^32 bytes: tokens at either end and around
+    the border have a small call's bits, and dgamma holds every token (a lane's
+    35 tokens of 10 heads, then the waves, 32 parts of a run and 18 for the runs:
+    404 additions, for which the bound has 400 and what C leaves of 64)."""
+    tokens, heads, d = 139900, 40, 128
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x, do = (torch.randn((tokens, 3 * heads * d), generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    gam = inputs(9, 1, 1, d, "bf16")[2]
+    cos, sin = (torch.randn((tokens, d), generator=g, device=DEV) for _ in range(2))
+    some = torch.tensor([0, 1, 139808, 139809, 139810, 139811, tokens - 2, tokens - 1], device=DEV)
+    kw = dict(q_gamma=gam[0], k_gamma=gam[1], eps=EPS)
+    few = do[some]
+    qkr.qknorm_rope_backward(few, x[some], cos=cos[some], sin=sin[some], **kw)
+    out = torch.full_like(x, 3.0)
+    dg = qkr.qknorm_rope_backward(do, x, cos=cos, sin=sin, out=out, **kw)
+    n = 2 * heads * d
+    assert same_bits(out[some][:, :n].contiguous(), few[:, :n].contiguous()) and (out[:, n:] == 3).all()
+    del out
+    sums = torch.zeros((2, 2, d), dtype=torch.float64, device=DEV)
+    for at in range(0, tokens, 4096):
+        run = slice(at, at + 4096)
+        parts = [t[run].view(-1, 3, heads, d) for t in (x, do)]
+        for i in range(2):
+            _, _, dgamma, e_dgamma = reference(parts[0][:, i], parts[1][:, i], gam[i], cos[run], sin[run], "interleaved")
+            sums[i, 0] += dgamma
+            sums[i, 1] += e_dgamma
+    for i in range(2):
+        assert ((dg[i].double() - sums[i, 0]).abs() <= sums[i, 1]).all()
