@@ -84,7 +84,9 @@ constexpr int value_rows(int d) { return 4 * 256 / (d / 8); }
 // delta is the diagonal of out dout^T, taken on the matrix cores in the order
 // in which dout . v is summed: where out is a copy of one value (a query that
 // sees one key, or gives one all its weight) dp - delta is then exactly 0, and
-// not what two orders of summation differ by.
+// not what two orders of summation differ by.  The fragments that takes, 16 bytes
+// of a row a lane, cost time: 28 us on 4608 tokens of 48 heads of 128, where whole
+// rows summed side by side took 21 (22 at a copy's rate).
 template <int D, bool F16>
 __global__ __launch_bounds__(256)
 void row_stats_kernel(const BwdParams p)
@@ -178,12 +180,14 @@ constexpr int kWaves = 4;
 constexpr int kTileRows = 64;      // queries (dk and dv) or keys (dq) staged at a time
 constexpr int kFewRows = 32;
 
-// What bounds it: the matrix rate at the clock that its power leaves (about
-// 1030 TFLOP/s of the four products at head_dim 128, where a large library
-// product reaches 1220), with the LDS reads, one fragment a product, close
-// behind.  Tiles of 64 queries measured 6% faster than tiles of 32, and keeping
-// the phases of a block apart 3% more: left to itself the scheduler mixes two
-// blocks and has to spill.
+// What bounds it: the matrix cores together with what feeds them, at the clock
+// that the power leaves (1.7 to 1.9 of 2.4 GHz).  They are busy 58 to 60% of the
+// cycles, the LDS reads, one fragment a product, and the vector ALU a third each.
+// The four products run at 1141 TFLOP/s on 32760 tokens of 5 heads of 128 and at
+// 1094 on 4608 of 48, launched alone; a large library product, under the same
+// power, reaches 1215 on that card.  Tiles of 64 queries measured 6% faster than
+// tiles of 32, and keeping the phases of a block apart 3% more: left to itself
+// the scheduler mixes two blocks and has to spill.
 //
 // head_dim 256 takes all 512 registers of a lane: 256 accumulators, 128 of k and
 // v, 32 scores.  The barriers to the scheduler that only it has keep a phase's
@@ -191,8 +195,8 @@ constexpr int kFewRows = 32;
 //
 // DS = 2, for head_dim 256: two waves share a block of 32 keys, each with the
 // scores of all and half the columns of dk and dv.  That is 6 products for 4, but
-// twice the workgroups, for calls that leave CUs idle (8 heads of 512 tokens: 50
-// against 57 us; 16 heads of 4096, which do not: 1400 against 1140).
+// twice the workgroups, for calls that leave CUs idle (8 heads of 512 tokens: 44
+// against 55 us; 16 heads of 4096, which do not: 1409 against 1083).
 template <int D, bool F16, bool CAUSAL, bool TWO, int DS>
 __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* lds, float* tops,
                                               uint32_t bid)

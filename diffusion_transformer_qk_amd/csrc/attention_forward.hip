@@ -40,15 +40,16 @@ struct FwdParams {
     float* part_lse;                          // [splits][batch * kv_heads * rows], base 2
 };
 
-// exp2 of the scores is taken relative to 2^-kShift of the row's maximum, so
+// exp2 of the scores is taken relative to 2^-p_shift of the row's maximum, so
 // that fp16 probabilities down to 2^-21 of the largest are normal numbers; a
-// maximum is kept until the scores pass it by kSlack, so p <= 2^(kShift + kSlack).
+// maximum is kept until the scores pass it by kSlack, so p <= 2^(p_shift + kSlack).
 template <bool F16>
 constexpr float p_shift() { return F16 ? 7.0f : 0.0f; }
 constexpr float kSlack = 8.0f;
 
 // Waves a SIMD that the registers have to allow (of 4-wave workgroups): q and
-// o take 24, 96 or 192 of them a lane beside the 16 scores and the operands.
+// o take 48, 96 or 192 of them a lane beside the scores (32 at head_dim 64, 16
+// above) and the operands.
 constexpr int waves_per_simd(int d) { return d == 64 ? 4 : d == 128 ? 3 : 2; }
 
 // Keys of a tile.  head_dim 128: 64 keys, which leave two waves a SIMD, measured

@@ -1,7 +1,10 @@
 // layer_norm.hip -- layer norm forward and backward for gfx950 (see
 // layer_norm.h).
 //
-// Memory-bound: every pass reads each row once and keeps it in registers.
+// Bound by memory: every pass reads each row once and keeps it in registers.
+// Forward 5.0 TB/s on 32760 x 5120, a large copy's rate on that card, where
+// fuse_scale_shift, a wave a row, moves the same bytes at 6.0: the rest is the
+// schedule's (two rows of a workgroup in flight, two reductions through LDS a row).
 //   * a row is held by TPR threads, VPT 16-byte vectors each: one wave up to
 //     1024 columns, the four waves of a workgroup above;
 //   * a workgroup walks a run of rows of one weight row, so the weight (and in
@@ -435,15 +438,25 @@ Fn select(int hidden)
     }
 }
 
-// Workgroups that a call spreads its rows over: whole multiples of what is
-// resident at once.  Measured on 300 MB of rows, in workgroups a CU (GB/s):
-//   forward   512 columns (1 vector): 2: 3530, 3: 4240, 4: 4710
-//            4096 (2 vectors):        2: 4680, 3: 4650, 4: 5000
-//            5120 (3 vectors):        2: 4680, 3: 5000, 4: 4140
-//            8192 (4 vectors):        2: 5060, 3: 4250, 4: 5160
-//   backward 2048 columns (1 vector): 2: 3370, 3: 4120, 4: 4470
-//            4096 (2 vectors):        2: 4730, 3: 4440, 4: 4020
-//            5120 (3 vectors):        2: 4660, 3: 3900, 4: 4400
+// Workgroups that a call spreads its rows over, by the vectors a thread holds:
+// with one of them, as many as keep enough loads in flight; with more, a whole
+// multiple of what the registers let run at once, where that is 2 or 3 a CU (the
+// last round is then as full as the others).  Measured on 300 MB of rows, in
+// workgroups a CU (GB/s; * the rule's):
+//   forward   512 columns (a wave a row, 1 vector): 2: 3645, 3: 4421, 4: 5048*
+//            1024 (a wave a row, 2 vectors):        2: 4975, 3: 4706, 4: 5073*
+//            2048 (1 vector):                       2: 3000, 3: 4101, 4: 4809*
+//            4096 (2 vectors):                      2: 4780, 3: 4690, 4: 5082*
+//            5120 (3 vectors):                      2: 4717, 3: 5044*, 4: 4223
+//            6144 (3 vectors, the last one full):   2: 5014, 3: 4686*, 4: 4431
+//            8192 (4 vectors):                      2: 5163, 3: 4271, 4: 5265*
+//   backward  512 columns (a wave a row, 1 vector): 2: 4271, 3: 4569, 4: 4812*
+//            1024 (a wave a row, 2 vectors):        2: 4946*, 3: 4651, 4: 4470
+//            2048 (1 vector):                       2: 3627, 3: 4323, 4: 4610*
+//            4096 (2 vectors):                      2: 4908*, 3: 4515, 4: 4108
+//            5120 (3 vectors):                      2: 4892*, 3: 3994, 4: 4486
+//            6144 (3 vectors, the last one full):   2: 4760*, 3: 4052, 4: 4731
+//            8192 (4 vectors):                      2: 4697*, 3: 3993, 4: 4647
 int64_t target_blocks(int hidden, bool grad)
 {
     const int v = vectors_of(hidden);
