@@ -184,8 +184,14 @@ inline bool may_meet(const dit_attn_args& a, const dit_attn_tensor& x, const Ext
     }
     if (alike && !runs_meet(ahead, steps, n, a.head_dim))
         return false;
-    const int64_t ts = x.token_stride;
-    if (ts != y.token_stride || ts == 0)
+    // rows: what tokens (or, of one token each, samples) step by
+    int64_t ts = ex.tokens > 1 ? x.token_stride : y.token_stride;
+    if (ex.tokens > 1 && ey.tokens > 1 && ts != y.token_stride)
+        return true;
+    if (ex.tokens == 1 && ey.tokens == 1)
+        ts = x.batch_stride == 0 || (y.batch_stride != 0 && y.batch_stride < x.batch_stride) ? y.batch_stride
+                                                                                            : x.batch_stride;
+    if (ts == 0)
         return true;
     if (a.batch > 1 && (x.batch_stride % ts || y.batch_stride % ts))
         return true;

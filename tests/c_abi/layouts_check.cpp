@@ -70,7 +70,8 @@ int main()
         a.batch = 1 + below(3);
         a.head_dim = kDim;
         const int64_t tokens = 1 + below(5), slots = 1 + below(4), tensors = 1 + below(4);
-        int64_t size[4] = {a.batch, tokens, slots, tensors}, stride[4], order[4] = {0, 1, 2, 3}, s = kDim + 8 * below(2);
+        int64_t size[4] = {a.batch, tokens, slots, tensors}, stride[4], order[4] = {0, 1, 2, 3};
+        int64_t s = kDim + 8 * below(2);
         std::shuffle(order, order + 4, rng);
         for (int i : order) {
             stride[i] = s;
@@ -82,7 +83,8 @@ int main()
             const int64_t first = below(slots), token = below(tokens);
             e[i] = Extent{1 + below(tokens - token), (int32_t)(1 + below(slots - first))};
             // now and then a few elements off its place
-            const int64_t at = below(tensors) * stride[3] + first * stride[2] + token * stride[1] + (below(4) ? 0 : 8 * below(9));
+            const int64_t at = below(tensors) * stride[3] + first * stride[2] + token * stride[1] +
+                               (below(4) ? 0 : 8 * below(9));
             t[i] = dit_attn_tensor{kAt + 2 * at, stride[0], stride[1], stride[2]};
         }
         const bool meet = share(runs(a, t[0], e[0]), runs(a, t[1], e[1]));
@@ -91,7 +93,22 @@ int main()
         ++(meet ? joined : apart);
     }
 
-    // any strides (odd and negative ones of single elements too), zeros and ones that fold onto themselves among them: never
+    // rows beside rows: of one token each, one of them the same for all samples
+    for (int64_t tokens : {1, 4})
+        for (int64_t single : {0, 1}) {
+            dit_attn_args a = {};
+            a.batch = 3;
+            a.head_dim = kDim;
+            const Extent ex = {single ? 1 : tokens, 2}, ey = {tokens, 3};
+            const int64_t row = 5 * kDim;
+            const dit_attn_tensor x = {kAt + 2 * row, 0, row, kDim};
+            const dit_attn_tensor y = {kAt + 2 * (2 * kDim), tokens * row, row, kDim};
+            if (said(a, x, ex, y, ey) || said(a, y, ey, x, ex))
+                return wrong("apart", a, x, ex, y, ey);
+        }
+
+    // any strides (odd and negative ones of single elements too), zeros and ones
+    // that fold onto themselves among them: never
     // apart where they share
     for (int n = 0; n < 40000; ++n) {
         dit_attn_args a = {};
