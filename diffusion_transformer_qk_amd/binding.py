@@ -4,8 +4,9 @@ Every step runs in the HIP kernels behind the C ABI declared in
 ``include/qknorm_rope.h`` (fused QK-norm + RoPE), ``include/fuse_scale_shift.h``
 (AdaLN modulation), ``include/group_norm_silu.h`` (group norm + SiLU),
 ``include/dit_attention.h`` (attention and its backward pass),
-``include/layer_norm.h`` (layer norm and its backward pass) and
-``include/qknorm_rope_backward.h``;
+``include/layer_norm.h`` (layer norm and its backward pass),
+``include/rms_norm.h`` (RMS norm with the residual and an 8-bit output, and its
+backward pass) and ``include/qknorm_rope_backward.h``;
 this module turns torch
 tensors into device pointers, sizes and enum codes and raises on a non-zero
 status.  There is no fallback: if the library is missing, loading fails
@@ -42,7 +43,8 @@ EXPORTS = ("qknorm_rope_fused", "qknorm_rope_strerror", "qknorm_rope_version",
            "dit_attention_workspace_size", "dit_attention_backward_workspace_size",
            "dit_attention", "dit_attention_backward", "dit_layer_norm",
            "dit_layer_norm_backward_workspace_size", "dit_layer_norm_backward",
-           "qknorm_rope_backward_workspace_size", "qknorm_rope_backward")
+           "qknorm_rope_backward_workspace_size", "qknorm_rope_backward", "dit_rms_norm",
+           "dit_rms_norm_backward_workspace_size", "dit_rms_norm_backward")
 MOD_DTYPES = {"bf16": QKR_BF16, "fp16": QKR_FP16, "fp32": QKR_FP32}
 
 
@@ -137,6 +139,12 @@ def load_library(path: str = LIB_PATH):
     lib.dit_layer_norm_backward.argtypes = [vp, vp, vp, i64, i32, i64, vp, i32, i32, vp, vp, f32,
                                             i32, vp, i64, vp]
     lib.dit_layer_norm_backward.restype = ctypes.c_int
+    lib.dit_rms_norm.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, i32, f32, i32, vp]
+    lib.dit_rms_norm.restype = ctypes.c_int
+    lib.dit_rms_norm_backward_workspace_size.argtypes = [i64, i32]
+    lib.dit_rms_norm_backward_workspace_size.restype = i64
+    lib.dit_rms_norm_backward.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, vp, f32, i32, vp, i64, vp]
+    lib.dit_rms_norm_backward.restype = ctypes.c_int
     grad = ctypes.POINTER(GradTensor)
     lib.qknorm_rope_backward_workspace_size.argtypes = [i64, i32]
     lib.qknorm_rope_backward_workspace_size.restype = i64
@@ -757,6 +765,143 @@ def fuse_scale_shift_backward(dy, x, scale, *, out=None, eps: float = 1e-6,
             for t in (dscale, dshift):
                 t.view(batches, hidden)[used:].zero_()
     return dx, dscale, dshift
+
+
+def _like(t, x, name: str, like: str = "x"):
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError("%s must match %s in shape and dtype" % (name, like))
+
+
+def _rms_norm(x, weight, residual, sum_out, out, scales, eps, stream):
+    lib = load_library()
+    rows = x.numel() // x.shape[-1] if x.numel() else 0
+    ctx, stream_ptr = _call_context(x, (residual, sum_out, out, scales, weight), stream)
+    with ctx:
+        status = lib.dit_rms_norm(
+            _ptr(x), _ptr(residual), _ptr(sum_out), _ptr(out), _ptr(scales), rows, x.shape[-1],
+            _ptr(weight), QKR_FP32 if weight is None else _mod_code(weight, "weight"), float(eps),
+            _x_code(x, "x"), stream_ptr)
+    _check(status)
+
+
+def _rms_norm_sum(x, weight, residual, sum_out):
+    """The checks that both forms share; sum_out, made here if there is a residual."""
+    if x.dim() < 1:
+        raise ValueError("x must be [..., hidden]")
+    if weight is not None and weight.shape != x.shape[-1:]:
+        raise ValueError("weight must be [%d]" % x.shape[-1])
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out needs a residual")
+        return None
+    _like(residual, x, "residual")
+    if sum_out is None:
+        return _torch().empty_like(x)
+    _like(sum_out, x, "sum_out")
+    return sum_out
+
+
+def rms_norm(x, weight=None, *, residual=None, sum_out=None, out=None, eps: float = 1e-6, stream=None):
+    """RMS norm over the last dimension (see ``include/rms_norm.h``); returns
+    ``out``, or ``(out, sum)`` with a residual.
+
+    ``x``: [..., hidden] bfloat16/float16; ``weight``: [hidden] of bfloat16,
+    float16 or float32, or None.  ``residual``, like x, is added first: the sum
+    is rounded to x's type, is what is normalised, and goes to ``sum_out`` (a
+    new tensor by default; ``sum_out=residual`` adds in place).  ``out``
+    defaults to a new tensor like x; it may be x or the residual itself.
+    """
+    with _launch_stream_context(x, stream):
+        sum_out = _rms_norm_sum(x, weight, residual, sum_out)
+        if out is None:
+            out = _torch().empty_like(x)
+        else:
+            _like(out, x, "out")
+    _rms_norm(x, weight, residual, sum_out, out, None, eps, stream)
+    return out if residual is None else (out, sum_out)
+
+
+def rms_norm_fp8(x, weight=None, *, residual=None, sum_out=None, out=None, scales=None,
+                 eps: float = 1e-6, stream=None):
+    """``rms_norm`` with an output in 8 bits; returns ``(out, scales)``, or
+    ``(out, scales, sum)`` with a residual.
+
+    ``out`` is float8_e4m3fn in x's shape, ``scales`` float32 in x's shape
+    without its last dimension: a row's largest value becomes 448, and the norm
+    is ``out * scales`` of the row (0 * anything for a row of zeros).  They are
+    what ``gated_feed_forward`` takes as ``x`` and ``x_scale``.  The other
+    arguments are ``rms_norm``'s.
+    """
+    torch = _torch()
+    with _launch_stream_context(x, stream):
+        sum_out = _rms_norm_sum(x, weight, residual, sum_out)
+        if out is None:
+            out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        elif out.shape != x.shape or out.dtype != torch.float8_e4m3fn:
+            raise ValueError("out must be float8_e4m3fn in x's shape")
+        if scales is None:
+            scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        elif scales.shape != x.shape[:-1] or scales.dtype != torch.float32:
+            raise ValueError("scales must be float32, one a row of x")
+    _rms_norm(x, weight, residual, sum_out, out, scales, eps, stream)
+    return (out, scales) if residual is None else (out, scales, sum_out)
+
+
+def rms_norm_backward_workspace_size(rows: int, hidden: int) -> int:
+    """Workspace bytes of ``rms_norm_backward`` (negative: a QKR_ERR_* code)."""
+    return int(load_library().dit_rms_norm_backward_workspace_size(rows, hidden))
+
+
+def rms_norm_backward(dy, x, weight=None, *, dsum=None, out=None, eps: float = 1e-6,
+                      param_grads: bool | None = None, workspace=None, stream=None):
+    """Backward pass of ``rms_norm``; returns ``(dx, dweight)``.
+
+    ``dy``: the gradient of its output, ``x``: what it normalised (the sum, if
+    there was a residual).  ``dsum``, like x, is the gradient that reaches the
+    sum past the norm, and is added: dx is then the gradient of x and of the
+    residual alike.  ``dweight`` is float32 [hidden], or None without
+    ``param_grads``, which defaults to whether there is a ``weight``.
+    ``out`` receives dx (a new tensor by default); it may be dy or dsum itself.
+    ``workspace``: at least ``rms_norm_backward_workspace_size`` bytes;
+    allocated here on the launch stream when None and needed.
+    """
+    torch = _torch()
+    lib = load_library()
+    if x.dim() < 1:
+        raise ValueError("x must be [..., hidden]")
+    hidden = x.shape[-1]
+    rows = x.numel() // hidden if x.numel() else 0
+    if weight is not None and weight.shape != (hidden,):
+        raise ValueError("weight must be [%d]" % hidden)
+    for name, t in (("dy", dy), ("dsum", dsum), ("out", out)):
+        if t is not None:
+            _like(t, x, name)
+    if param_grads is None:
+        param_grads = weight is not None
+    dweight = None
+    ws_bytes = 0
+    with _launch_stream_context(x, stream):
+        if param_grads:
+            make = torch.empty if rows else torch.zeros     # without rows the sum is empty
+            dweight = make(hidden, dtype=torch.float32, device=x.device)
+            if workspace is None:
+                ws_bytes = lib.dit_rms_norm_backward_workspace_size(rows, hidden)
+                if ws_bytes < 0:
+                    raise QkrError(ws_bytes, strerror(ws_bytes))
+                if ws_bytes > 0:
+                    workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+            else:
+                ws_bytes = workspace.numel() * workspace.element_size()
+        if out is None:
+            out = torch.empty_like(x)
+    ctx, stream_ptr = _call_context(x, (dy, dsum, out, weight, workspace), stream)
+    with ctx:
+        status = lib.dit_rms_norm_backward(
+            _ptr(dy), _ptr(x), _ptr(dsum), _ptr(out), rows, hidden, _ptr(weight),
+            QKR_FP32 if weight is None else _mod_code(weight, "weight"), _ptr(dweight), float(eps),
+            _x_code(x, "x"), _ptr(workspace), ws_bytes, stream_ptr)
+    _check(status)
+    return out, dweight
 
 
 def qknorm_rope_backward_workspace_size(tokens: int, head_dim: int) -> int:

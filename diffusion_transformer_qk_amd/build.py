@@ -17,6 +17,7 @@ SRCS = [os.path.join(PKG, "csrc", "qknorm_rope.hip"),
         os.path.join(PKG, "csrc", "fuse_scale_shift.hip"),
         os.path.join(PKG, "csrc", "group_norm_silu.hip"),
         os.path.join(PKG, "csrc", "layer_norm.hip"),
+        os.path.join(PKG, "csrc", "rms_norm.hip"),
         os.path.join(PKG, "csrc", "qknorm_rope_backward.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqknorm_rope.so")
