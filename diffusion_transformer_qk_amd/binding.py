@@ -6,7 +6,8 @@ Every step runs in the HIP kernels behind the C ABI declared in
 ``include/dit_attention.h`` (attention and its backward pass),
 ``include/layer_norm.h`` (layer norm and its backward pass),
 ``include/rms_norm.h`` (RMS norm with the residual and an 8-bit output, and its
-backward pass) and ``include/qknorm_rope_backward.h``;
+backward pass), ``include/feed_forward.h`` (the gated feed-forward projection
+and its backward pass) and ``include/qknorm_rope_backward.h``;
 this module turns torch
 tensors into device pointers, sizes and enum codes and raises on a non-zero
 status.  There is no fallback: if the library is missing, loading fails
@@ -32,6 +33,8 @@ QKR_COS_SHARED, QKR_COS_PER_HEAD = 0, 1
 QKR_ROPE_INTERLEAVED, QKR_ROPE_ROTATE_HALF = 0, 1
 QKR_TENSORS_FUSED, QKR_TENSORS_PAIR, QKR_TENSORS_ONE = 0, 1, 2
 
+DIT_FF_E4M3 = 8
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 LAYOUTS = {"shared": QKR_COS_SHARED, "per_head": QKR_COS_PER_HEAD}
 DIT_LN_WEIGHT, DIT_LN_ONE_PLUS = 0, 1
 STYLES = {"interleaved": QKR_ROPE_INTERLEAVED, "rotate_half": QKR_ROPE_ROTATE_HALF}
@@ -44,7 +47,9 @@ EXPORTS = ("qknorm_rope_fused", "qknorm_rope_strerror", "qknorm_rope_version",
            "dit_attention", "dit_attention_backward", "dit_layer_norm",
            "dit_layer_norm_backward_workspace_size", "dit_layer_norm_backward",
            "qknorm_rope_backward_workspace_size", "qknorm_rope_backward", "dit_rms_norm",
-           "dit_rms_norm_backward_workspace_size", "dit_rms_norm_backward")
+           "dit_rms_norm_backward_workspace_size", "dit_rms_norm_backward",
+           "dit_gated_feed_forward_workspace_size", "dit_gated_feed_forward",
+           "dit_gated_feed_forward_backward_workspace_size", "dit_gated_feed_forward_backward")
 MOD_DTYPES = {"bf16": QKR_BF16, "fp16": QKR_FP16, "fp32": QKR_FP32}
 
 
@@ -79,6 +84,11 @@ class AttnArgs(ctypes.Structure):
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("causal", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("kv_lengths", ctypes.c_void_p)]
+
+
+class FfArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int32), ("inner", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -145,6 +155,14 @@ def load_library(path: str = LIB_PATH):
     lib.dit_rms_norm_backward_workspace_size.restype = i64
     lib.dit_rms_norm_backward.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, vp, f32, i32, vp, i64, vp]
     lib.dit_rms_norm_backward.restype = ctypes.c_int
+    ff = ctypes.POINTER(FfArgs)
+    for name in ("dit_gated_feed_forward_workspace_size", "dit_gated_feed_forward_backward_workspace_size"):
+        getattr(lib, name).argtypes = [ff]
+        getattr(lib, name).restype = i64
+    lib.dit_gated_feed_forward.argtypes = [ff, *[vp] * 10, i64, vp]
+    lib.dit_gated_feed_forward.restype = ctypes.c_int
+    lib.dit_gated_feed_forward_backward.argtypes = [ff, *[vp] * 10, i64, vp]
+    lib.dit_gated_feed_forward_backward.restype = ctypes.c_int
     grad = ctypes.POINTER(GradTensor)
     lib.qknorm_rope_backward_workspace_size.argtypes = [i64, i32]
     lib.qknorm_rope_backward_workspace_size.restype = i64
@@ -1007,3 +1025,138 @@ def qknorm_rope_backward(dqkv=None, qkv=None, dq=None, dk=None, q=None, k=None, 
             _table_code(cos), STYLES[style], _x_code(ref), _ptr(workspace), ws_bytes, stream_ptr)
     _check(status)
     return dq_gamma, dk_gamma
+
+
+def _ff_args(x, w_gate, w_up, activation, out_dtype=None) -> FfArgs:
+    torch = _torch()
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % sorted(ACTIVATIONS))
+    if x.dim() < 1 or w_gate.dim() != 2 or w_gate.shape[1] != x.shape[-1]:
+        raise ValueError("x must be [..., hidden] and the weights [inner, hidden]")
+    if w_up.shape != w_gate.shape:
+        raise ValueError("w_gate and w_up must have one shape")
+    if w_gate.dtype != x.dtype or w_up.dtype != x.dtype:
+        raise ValueError("x, w_gate and w_up must have one dtype")
+    inner, hidden = w_gate.shape
+    if x.dtype == torch.float8_e4m3fn:
+        dtype = DIT_FF_E4M3
+        out = {None: QKR_BF16, torch.bfloat16: QKR_BF16, torch.float16: QKR_FP16}.get(out_dtype)
+        if out is None:
+            raise ValueError("out_dtype must be bfloat16 or float16, got %s" % out_dtype)
+    else:
+        dtype = out = _x_code(x, "x and the weights")
+        if out_dtype is not None and out_dtype != x.dtype:
+            raise ValueError("out_dtype must be x's dtype, unless that is float8_e4m3fn")
+    return FfArgs(x.numel() // hidden if hidden else 0, hidden, inner, ACTIVATIONS[activation], dtype, out)
+
+
+def _ff_like(t, shape, dtype, name: str):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError("%s must be %s %s" % (name, dtype, list(shape)))
+
+
+def gated_feed_forward(x, w_gate, w_up, *, activation: str = "silu", x_scale=None, gate_scale=None,
+                       up_scale=None, out_dtype=None, save: bool = False, out=None, gate=None,
+                       up=None, stream=None):
+    """``act(x @ w_gate.T) * (x @ w_up.T)`` in one kernel (see
+    ``include/feed_forward.h``); returns ``out``, or ``(out, gate, up)`` with
+    ``save``.
+
+    ``x``: [..., hidden]; ``w_gate``/``w_up``: [inner, hidden] (the halves of
+    one [2 * inner, hidden] weight serve as they are), all of bfloat16 or
+    float16, or all of float8_e4m3fn with ``x_scale`` (float32, one a row of x:
+    what ``rms_norm_fp8`` gives) and ``gate_scale``/``up_scale`` (float32
+    [inner]).  ``activation``: "silu" or "gelu_tanh".  ``out``: [..., inner] of
+    x's dtype, or for 8 bits of ``out_dtype`` (bfloat16 by default).  ``save``
+    keeps both projections in ``gate`` and ``up``, like out, for
+    ``gated_feed_forward_backward``.
+    """
+    torch = _torch()
+    lib = load_library()
+    args = _ff_args(x, w_gate, w_up, activation, out_dtype)
+    fp8 = args.dtype == DIT_FF_E4M3
+    for name, t, shape in (("x_scale", x_scale, x.shape[:-1]), ("gate_scale", gate_scale, (args.inner,)),
+                           ("up_scale", up_scale, (args.inner,))):
+        if fp8 != (t is not None):
+            raise ValueError("%s goes with float8_e4m3fn, and only with it" % name)
+        if t is not None:
+            _ff_like(t, shape, torch.float32, name)
+    if not save and (gate is not None or up is not None):
+        raise ValueError("gate and up go with save")
+    shape = (*x.shape[:-1], args.inner)
+    dtype = torch.float16 if args.out_dtype == QKR_FP16 else torch.bfloat16
+    made = []
+    with _launch_stream_context(x, stream):
+        for name, t, wanted in (("out", out, True), ("gate", gate, save), ("up", up, save)):
+            if t is not None:
+                _ff_like(t, shape, dtype, name)
+            elif wanted:
+                t = torch.empty(shape, dtype=dtype, device=x.device)
+            made.append(t)
+    out, gate, up = made
+    ctx, stream_ptr = _call_context(x, (w_gate, w_up, x_scale, gate_scale, up_scale, out, gate, up), stream)
+    with ctx:
+        status = lib.dit_gated_feed_forward(args, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(x_scale),
+                                            _ptr(gate_scale), _ptr(up_scale), _ptr(out), _ptr(gate), _ptr(up),
+                                            None, 0, stream_ptr)
+    _check(status)
+    return (out, gate, up) if save else out
+
+
+def gated_feed_forward_backward_workspace_size(rows: int, hidden: int, inner: int, *,
+                                               dtype: int = QKR_BF16) -> int:
+    """Workspace bytes of ``gated_feed_forward_backward`` (negative: a QKR_ERR_*
+    code for bad sizes)."""
+    args = FfArgs(rows, hidden, inner, 0, dtype, dtype)
+    return int(load_library().dit_gated_feed_forward_backward_workspace_size(args))
+
+
+def gated_feed_forward_backward(dh, x, w_gate, w_up, gate, up, *, activation: str = "silu", dx=None,
+                                dw_gate=None, dw_up=None, input_grad: bool = True,
+                                weight_grads: bool = True, workspace=None, stream=None):
+    """Backward pass of ``gated_feed_forward``; returns ``(dx, dw_gate, dw_up)``.
+
+    ``dh`` is the gradient of its output, ``gate`` and ``up`` what it saved; the
+    rest is the forward call's, of bfloat16 or float16.  Gradients are of that
+    dtype, written (not added to), and default to new tensors; dx is None
+    without ``input_grad``, the other two are without ``weight_grads``.
+    ``workspace``: at least ``gated_feed_forward_backward_workspace_size`` bytes
+    (4 bytes an element of dh); allocated here on the launch stream when None.
+    """
+    torch = _torch()
+    lib = load_library()
+    args = _ff_args(x, w_gate, w_up, activation)
+    if args.dtype == DIT_FF_E4M3:
+        raise ValueError("the backward pass takes bfloat16 or float16")
+    shape = (*x.shape[:-1], args.inner)
+    for name, t in (("dh", dh), ("gate", gate), ("up", up)):
+        _ff_like(t, shape, x.dtype, name)
+    for name, t, wanted in (("dx", dx, input_grad), ("dw_gate", dw_gate, weight_grads), ("dw_up", dw_up, weight_grads)):
+        if t is not None and not wanted:
+            raise ValueError("%s was not asked for" % name)
+    made = []
+    with _launch_stream_context(x, stream):
+        for name, t, like, wanted in (("dx", dx, x, input_grad), ("dw_gate", dw_gate, w_gate, weight_grads),
+                                      ("dw_up", dw_up, w_up, weight_grads)):
+            if t is not None:
+                _ff_like(t, like.shape, like.dtype, name)
+            elif wanted:
+                t = torch.empty(like.shape, dtype=like.dtype, device=x.device)
+            made.append(t)
+        ws_bytes = 0
+        if workspace is None:
+            ws_bytes = int(lib.dit_gated_feed_forward_backward_workspace_size(args))
+            if ws_bytes < 0:
+                raise QkrError(ws_bytes, strerror(ws_bytes))
+            if ws_bytes > 0:
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
+    dx, dw_gate, dw_up = made
+    ctx, stream_ptr = _call_context(x, (dh, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace), stream)
+    with ctx:
+        status = lib.dit_gated_feed_forward_backward(
+            args, _ptr(dh), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up), _ptr(dx), _ptr(dw_gate),
+            _ptr(dw_up), _ptr(workspace), ws_bytes, stream_ptr)
+    _check(status)
+    return dx, dw_gate, dw_up

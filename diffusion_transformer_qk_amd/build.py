@@ -21,13 +21,16 @@ SRCS = [os.path.join(PKG, "csrc", "qknorm_rope.hip"),
         os.path.join(PKG, "csrc", "qknorm_rope_backward.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqknorm_rope.so")
-# The attention kernels: a library of their own, because every kernel of
-# libqknorm_rope.so is memory-bound work without matrix instructions and the
-# tests hold its whole code to that.  libqknorm_rope.so names it as a
+# The matrix-core kernels (attention, the gated feed-forward projection): a
+# library of their own, because every kernel of libqknorm_rope.so is
+# memory-bound work without matrix instructions and the tests hold its whole
+# code to that.  libqknorm_rope.so names it as a
 # dependency beside itself, so loading the one brings the other along (a C
-# program that calls attention links both).
+# program that calls them links both).
 ATTN_SRCS = [os.path.join(PKG, "csrc", "attention_forward.hip"),
-             os.path.join(PKG, "csrc", "attention_backward.hip")]
+             os.path.join(PKG, "csrc", "attention_backward.hip"),
+             os.path.join(PKG, "csrc", "gated_feed_forward.hip"),
+             os.path.join(PKG, "csrc", "gated_feed_forward_backward.hip")]
 ATTN_LIB = os.path.join(PKG, "libdit_attention.so")
 # bench.py's data-movement probe: its own library, outside libqknorm_rope.so
 FLOOR_SRC = os.path.join(ROOT, "bench_floor.hip")

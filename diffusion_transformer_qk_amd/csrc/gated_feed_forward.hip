@@ -1,0 +1,233 @@
+// gated_feed_forward.hip -- h = act(x W_gate^T) * (x W_up^T) for gfx950 (see
+// feed_forward.h).
+//
+// One product with the rows of both weights as one operand: a wave holds the same
+// rows of W_gate and of W_up (feed_forward_common.h), so that gate and up of an
+// element end in the same place of two accumulators, and the activation and the
+// product are its epilogue.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "feed_forward.h"
+#include "feed_forward_common.h"
+#include "feed_forward_host.h"
+
+namespace {
+
+using namespace qkr_ff;
+
+struct FwdParams {
+    const char *x, *w_gate, *w_up;
+    const float *x_scale, *gate_scale, *up_scale;
+    uint16_t *h, *gate, *up;
+    int64_t rows;
+    int32_t inner;
+    int32_t k_bytes;                  // of a row of x and of the weights
+    uint32_t row_tiles, inner_tiles;  // of the grid
+};
+
+// The epilogue of one block: rows r (this lane's), columns i0 .. i0 + 31.
+template <int T, bool F16, int ACT>
+__device__ __forceinline__ void finish(const FwdParams& p, f32x16 gate, f32x16 up, int64_t r, int i0, int g)
+{
+    const bool valid = r < p.rows;
+    const int left = p.inner - i0;
+    if constexpr (T == kFp8) {
+        const float s = valid ? p.x_scale[r] : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (8 * q + 4 * g < left) {
+                const float* gs = p.gate_scale + i0 + 8 * q + 4 * g;
+                const float* us = p.up_scale + i0 + 8 * q + 4 * g;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    gate[4 * q + k] *= s * gs[k];
+                    up[4 * q + k] *= s * us[k];
+                }
+            }
+        }
+    }
+    const int64_t at = r * p.inner + i0;
+    if (p.gate) {
+        store_block<F16>(p.gate + at, gate, g, valid, left);
+        store_block<F16>(p.up + at, up, g, valid, left);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        gate[k] = activated<ACT>(gate[k]) * up[k];
+    store_block<F16>(p.h + at, gate, g, valid, left);
+}
+
+// Tiles of kRowsB rows of x and kRowsA / 2 columns of h.
+template <int T, bool F16, int ACT, int NA, int NB>
+__global__ __launch_bounds__(256, NA * NB > 4 ? 1 : 2)
+void gated_feed_forward_kernel(const FwdParams p)
+{
+    using P = Product<T, kRows, kRows, true, NA, NB, 2, 2>;
+    __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const TileOf tile(blockIdx.x, p.row_tiles, p.inner_tiles, 8);
+    const int64_t r0 = (int64_t)tile.row * P::kRowsB;
+    constexpr int kColumnsOf = P::kRowsA / 2;
+    const int i0 = tile.column * kColumnsOf;
+    const int64_t rows_left = p.rows - r0;
+    const int of_up = wave >> 1;                 // waves 0 and 1 load W_gate's rows
+    const Matrix w = {(of_up ? p.w_up : p.w_gate) + (int64_t)i0 * p.k_bytes, p.k_bytes,
+                      p.inner - i0 < kColumnsOf ? p.inner - i0 : kColumnsOf};
+    const Matrix x = {p.x + r0 * p.k_bytes, p.k_bytes, rows_left < P::kRowsB ? (int)rows_left : P::kRowsB};
+    typename P::LoadA la(w, (wave & 1) * P::kLoadsA, p.k_bytes, lane);
+    typename P::LoadB lb(x, wave * P::kLoadsB, p.k_bytes, lane);
+    P c;
+    c.clear();
+    c.add(la, lb, (p.k_bytes + kStageBytes - 1) / kStageBytes, lds_address(lds), wave, lane);
+    const int n = lane & 31, g = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < NA / 2; ++i) {
+            const f32x16 gate = c.block(i, j), up = c.block(i + NA / 2, j);
+            finish<T, F16, ACT>(p, gate, up, r0 + (P::first_b(wave) + j) * 32 + n,
+                                i0 + (P::first_a(wave) + i) * 32, g);
+        }
+}
+
+// Up to 32 rows of x: the call waits for the weights.  A workgroup takes 32 columns
+// of h, its waves a quarter of k each, through rings of their own (no barriers),
+// and the first wave adds the four sums in order.
+constexpr int kFewRows = 32, kFewColumns = 32;
+
+template <int T, bool F16, int ACT>
+__global__ __launch_bounds__(256, 2)
+void gated_feed_forward_few_kernel(const FwdParams p)
+{
+    using P = Product<T, kRows, kRows, true, 2, 1, 1, 1, 3>;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * P::kLds];
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int i0 = (int)blockIdx.x * kFewColumns;
+    const int stages = (p.k_bytes + kStageBytes - 1) / kStageBytes, each = (stages + 3) / 4;
+    const int k0 = wave * each * kStageBytes;
+    const int k_left = p.k_bytes - k0 < each * kStageBytes ? p.k_bytes - k0 : each * kStageBytes;
+    const int columns = p.inner - i0 < kFewColumns ? p.inner - i0 : kFewColumns;
+    const int64_t w0 = (int64_t)i0 * p.k_bytes + k0;
+    const uint32_t ring = lds_address(lds) + wave * P::kLds;
+    P c;
+    c.clear();
+    if (k_left > 0) {
+        // one load of 32 rows of W_gate, one of W_up
+        typename P::LoadA la(Matrix{p.w_gate + w0, p.k_bytes, columns}, Matrix{p.w_up + w0, p.k_bytes, columns}, k_left,
+                             lane);
+        typename P::LoadB lb(Matrix{p.x + k0, p.k_bytes, (int)p.rows}, 0, k_left, lane);
+        c.add(la, lb, (k_left + kStageBytes - 1) / kStageBytes, ring, 0, lane);
+    }
+    const int n = lane & 31, g = lane >> 5;
+    f32x4* sums = reinterpret_cast<f32x4*>(lds) + wave * (P::kLds / 16);
+    if (wave > 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                sums[(i * 4 + q) * 64 + lane] = f32x4{c.c[i][0][4 * q], c.c[i][0][4 * q + 1], c.c[i][0][4 * q + 2],
+                                                      c.c[i][0][4 * q + 3]};
+    }
+    __syncthreads();
+    if (wave > 0)
+        return;
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4 v = sums[w * (P::kLds / 16) + (i * 4 + q) * 64 + lane];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    c.c[i][0][4 * q + k] += v[k];
+            }
+    finish<T, F16, ACT>(p, c.c[0][0], c.c[1][0], n, i0, g);
+}
+
+using Fn = void (*)(FwdParams);
+
+template <int T, bool F16, int NA, int NB>
+Fn select(int activation)
+{
+    if constexpr (NA == 0)
+        return activation == DIT_FF_SILU ? gated_feed_forward_few_kernel<T, F16, 0>
+                                         : gated_feed_forward_few_kernel<T, F16, 1>;
+    else
+        return activation == DIT_FF_SILU ? gated_feed_forward_kernel<T, F16, 0, NA, NB>
+                                         : gated_feed_forward_kernel<T, F16, 1, NA, NB>;
+}
+
+// NA, NB: blocks of a wave's tile, or 0 for few rows.
+template <int NA, int NB>
+Fn select(int dtype, int out_dtype, int activation)
+{
+    if (dtype == DIT_FF_E4M3)
+        return out_dtype == QKR_FP16 ? select<kFp8, true, NA, NB>(activation) : select<kFp8, false, NA, NB>(activation);
+    return dtype == QKR_FP16 ? select<kFp16, true, NA, NB>(activation) : select<kBf16, false, NA, NB>(activation);
+}
+
+}  // namespace
+
+extern "C" int64_t dit_gated_feed_forward_workspace_size(const dit_ff_args* args)
+{
+    return qkr_ff_host::check_args(args, true);
+}
+
+extern "C" int dit_gated_feed_forward(const dit_ff_args* args, const void* x, const void* w_gate,
+                                      const void* w_up, const float* x_scale, const float* gate_scale,
+                                      const float* up_scale, void* h, void* gate, void* up,
+                                      void* workspace, int64_t workspace_bytes, void* stream)
+{
+    using namespace qkr_ff_host;
+    (void)workspace;
+    (void)workspace_bytes;
+    const int rc = check_args(args, true);
+    if (rc != QKR_OK)
+        return rc;
+    const dit_ff_args& a = *args;
+    const bool fp8 = a.dtype == DIT_FF_E4M3;
+    if (a.rows == 0)
+        return QKR_OK;
+    if (!x || !w_gate || !w_up || !h || !gate != !up || (fp8 && (!x_scale || !gate_scale || !up_scale)))
+        return QKR_ERR_NULL;
+    if (!fp8 && (x_scale || gate_scale || up_scale))
+        return QKR_ERR_ARG;
+    const uint64_t size = fp8 ? 1 : 2, hidden = a.hidden, inner = a.inner, rows = a.rows;
+    const Buffer in[] = {{x, rows * hidden * size, 16}, {w_gate, inner * hidden * size, 16},
+                         {w_up, inner * hidden * size, 16}, {x_scale, x_scale ? rows * 4 : 0, 4},
+                         {gate_scale, gate_scale ? inner * 4 : 0, 4}, {up_scale, up_scale ? inner * 4 : 0, 4}};
+    const Buffer out[] = {{h, rows * inner * 2, 16}, {gate, gate ? rows * inner * 2 : 0, 16},
+                          {up, up ? rows * inner * 2 : 0, 16}};
+    const int bad = check_buffers(in, 6, out, 3);
+    if (bad != QKR_OK)
+        return bad;
+
+    FwdParams p = {};
+    p.x = static_cast<const char*>(x);
+    p.w_gate = static_cast<const char*>(w_gate);
+    p.w_up = static_cast<const char*>(w_up);
+    p.x_scale = x_scale;
+    p.gate_scale = gate_scale;
+    p.up_scale = up_scale;
+    p.h = static_cast<uint16_t*>(h);
+    p.gate = static_cast<uint16_t*>(gate);
+    p.up = static_cast<uint16_t*>(up);
+    p.rows = a.rows;
+    p.inner = a.inner;
+    p.k_bytes = a.hidden * (int32_t)size;
+    if (a.rows <= kFewRows)
+        return launch(select<0, 0>(a.dtype, a.out_dtype, a.activation), (a.inner + kFewColumns - 1) / kFewColumns, p,
+                      stream);
+    const bool large = large_tiles(a.rows, 2 * (int64_t)a.inner);
+    const int64_t side = large ? 256 : 128;
+    p.row_tiles = (uint32_t)((a.rows + side - 1) / side);
+    p.inner_tiles = (uint32_t)((a.inner + side / 2 - 1) / (side / 2));
+    const Fn fn = large ? select<4, 4>(a.dtype, a.out_dtype, a.activation)
+                        : select<2, 2>(a.dtype, a.out_dtype, a.activation);
+    return launch(fn, (int64_t)p.row_tiles * p.inner_tiles, p, stream);
+}
