@@ -9,7 +9,8 @@ The passes run in hand-written HIP kernels behind the C ABI of
 (``libqknorm_rope.so`` and the ``libdit_attention.so`` it loads); this package is the thin Python binding over it.
 """
 from .binding import (  # noqa: F401
-    EXPORTS, LIB_PATH, QkrError, attention, attention_backward, attention_workspace_size,
+    EXPORTS, LIB_PATH, QkrError, attention, attention_backward, attention_packed,
+    attention_packed_backward, attention_packed_workspace_size, attention_workspace_size,
     dit_fuse_scale_shift_raw, dit_group_norm_silu_noalloc_raw, dit_group_norm_silu_raw,
     fuse_scale_shift, fuse_scale_shift_backward, gated_feed_forward, gated_feed_forward_backward,
     gated_feed_forward_backward_workspace_size, group_norm_silu, group_norm_silu_schedule,
@@ -24,6 +25,7 @@ __all__ = ["qknorm_rope_fused", "qknorm_rope_fused_raw", "fuse_scale_shift",
            "group_norm_silu_workspace_size",
            "dit_group_norm_silu_raw", "dit_group_norm_silu_noalloc_raw", "kernel_info",
            "attention", "attention_backward", "attention_workspace_size",
+           "attention_packed", "attention_packed_backward", "attention_packed_workspace_size",
            "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_size",
            "fuse_scale_shift_backward", "qknorm_rope_backward",
            "qknorm_rope_backward_workspace_size",

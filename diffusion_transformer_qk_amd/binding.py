@@ -3,7 +3,8 @@
 Every step runs in the HIP kernels behind the C ABI declared in
 ``include/qknorm_rope.h`` (fused QK-norm + RoPE), ``include/fuse_scale_shift.h``
 (AdaLN modulation), ``include/group_norm_silu.h`` (group norm + SiLU),
-``include/dit_attention.h`` (attention and its backward pass),
+``include/dit_attention.h`` (attention, of padded samples and of packed
+sequences, and its backward pass),
 ``include/layer_norm.h`` (layer norm and its backward pass),
 ``include/rms_norm.h`` (RMS norm with the residual and an 8-bit output, and its
 backward pass), ``include/feed_forward.h`` (the gated feed-forward projection
@@ -49,7 +50,9 @@ EXPORTS = ("qknorm_rope_fused", "qknorm_rope_strerror", "qknorm_rope_version",
            "qknorm_rope_backward_workspace_size", "qknorm_rope_backward", "dit_rms_norm",
            "dit_rms_norm_backward_workspace_size", "dit_rms_norm_backward",
            "dit_gated_feed_forward_workspace_size", "dit_gated_feed_forward",
-           "dit_gated_feed_forward_backward_workspace_size", "dit_gated_feed_forward_backward")
+           "dit_gated_feed_forward_backward_workspace_size", "dit_gated_feed_forward_backward",
+           "dit_attention_packed_workspace_size", "dit_attention_packed_backward_workspace_size",
+           "dit_attention_packed", "dit_attention_packed_backward")
 MOD_DTYPES = {"bf16": QKR_BF16, "fp16": QKR_FP16, "fp32": QKR_FP32}
 
 
@@ -84,6 +87,15 @@ class AttnArgs(ctypes.Structure):
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("causal", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("kv_lengths", ctypes.c_void_p)]
+
+
+class AttnPackedArgs(ctypes.Structure):
+    _fields_ = [("sequences", ctypes.c_int64), ("q_tokens", ctypes.c_int64),
+                ("kv_tokens", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("fill_rest", ctypes.c_int32), ("q_offsets", ctypes.c_void_p),
+                ("kv_offsets", ctypes.c_void_p)]
 
 
 class FfArgs(ctypes.Structure):
@@ -142,6 +154,14 @@ def load_library(path: str = LIB_PATH):
     lib.dit_attention.restype = ctypes.c_int
     lib.dit_attention_backward.argtypes = [args, *[tensor] * 5, vp, *[tensor] * 3, vp, i64, vp]
     lib.dit_attention_backward.restype = ctypes.c_int
+    packed = ctypes.POINTER(AttnPackedArgs)
+    for name in ("dit_attention_packed_workspace_size", "dit_attention_packed_backward_workspace_size"):
+        getattr(lib, name).argtypes = [packed]
+        getattr(lib, name).restype = i64
+    lib.dit_attention_packed.argtypes = [packed, *[tensor] * 4, vp, vp, i64, vp]
+    lib.dit_attention_packed.restype = ctypes.c_int
+    lib.dit_attention_packed_backward.argtypes = [packed, *[tensor] * 5, vp, *[tensor] * 3, vp, i64, vp]
+    lib.dit_attention_packed_backward.restype = ctypes.c_int
     lib.dit_layer_norm.argtypes = [vp, vp, i64, i32, vp, vp, i32, f32, i32, vp]
     lib.dit_layer_norm.restype = ctypes.c_int
     lib.dit_layer_norm_backward_workspace_size.argtypes = [i64, i32, i64]
@@ -651,6 +671,123 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, kv_leng
                                     stream)
     with ctx:
         status = lib.dit_attention_backward(
+            args, _attn_tensor(dout, "dout"), _attn_tensor(q, "q"), _attn_tensor(k, "k"),
+            _attn_tensor(v, "v"), _attn_tensor(out, "out"), _ptr(lse), _attn_tensor(dq, "dq"),
+            _attn_tensor(dk, "dk"), _attn_tensor(dv, "dv"), _ptr(workspace), ws_bytes, stream_ptr)
+    _check(status)
+    return dq, dk, dv
+
+
+def _packed_args(q, k, v, offsets, kv_offsets, causal, scale, fill) -> AttnPackedArgs:
+    torch = _torch()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, head_dim]")
+    q_tokens, heads, head_dim = q.shape
+    if k.shape != v.shape or k.shape[2] != head_dim:
+        raise ValueError("k and v must be [kv_tokens, kv_heads, %d]" % head_dim)
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have one dtype")
+    kv_heads = k.shape[1]
+    if kv_heads < 1 or heads % kv_heads:
+        raise ValueError("the number of query heads must be a multiple of k's and v's")
+    if kv_offsets is None and k.shape[0] != q_tokens:
+        raise ValueError("k and v of other tokens than q need kv_offsets")
+    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.dtype != torch.int32:
+        raise ValueError("offsets must be int32 [sequences + 1]")
+    if kv_offsets is not None and (kv_offsets.shape != offsets.shape or kv_offsets.dtype != torch.int32):
+        raise ValueError("kv_offsets must be int32 [sequences + 1], as offsets are")
+    return AttnPackedArgs(offsets.numel() - 1, q_tokens, k.shape[0], heads, kv_heads, head_dim,
+                          1 if causal else 0, _x_code(q, "q/k/v"),
+                          head_dim ** -0.5 if scale is None else scale, 1 if fill else 0, _ptr(offsets),
+                          None if kv_offsets is None else _ptr(kv_offsets))
+
+
+def attention_packed_workspace_size(sequences: int, q_tokens: int, kv_tokens: int, heads: int, kv_heads: int,
+                                    head_dim: int, *, causal: bool = False, dtype: int = QKR_BF16,
+                                    backward: bool = False) -> int:
+    """Workspace bytes of an ``attention_packed`` call of buffers of these rows,
+    or of its backward pass (negative: a QKR_ERR_* code for bad sizes)."""
+    lib = load_library()
+    args = AttnPackedArgs(sequences, q_tokens, kv_tokens, heads, kv_heads, head_dim, 1 if causal else 0, dtype,
+                          1.0, 0, None, None)
+    size_of = (lib.dit_attention_packed_backward_workspace_size if backward
+               else lib.dit_attention_packed_workspace_size)
+    return int(size_of(args))
+
+
+def attention_packed(q, k, v, offsets, *, kv_offsets=None, causal: bool = False, scale: float | None = None,
+                     out=None, lse=None, workspace=None, stream=None):
+    """Attention of packed sequences of different lengths (see
+    ``include/dit_attention.h``); returns ``(out, lse)``.
+
+    ``q``: [tokens, heads, head_dim], ``k``/``v``: [kv_tokens, kv_heads,
+    head_dim], sequences one after another, of the types and strides that
+    ``attention`` takes.  ``offsets``: int32 [sequences + 1] on the GPU, not
+    decreasing: sequence i has the rows offsets[i] to offsets[i + 1] - 1 of q,
+    and of k and v unless ``kv_offsets`` (like it) says which.  Each attends to
+    its own keys as a sample of ``attention`` does; ``causal``: its last query
+    sees its last key.  Rows of no sequence, before the first or behind the
+    last, are neither read nor written; where ``out`` and ``lse`` (float32
+    [heads, tokens]) are both made here, they hold 0 and -inf there.
+    ``workspace``: at least ``attention_packed_workspace_size`` bytes, allocated
+    here on the launch stream when None and one is needed.
+    """
+    torch = _torch()
+    lib = load_library()
+    args = _packed_args(q, k, v, offsets, kv_offsets, causal, scale, out is None and lse is None)
+    with _launch_stream_context(q, stream):
+        workspace, ws_bytes = _attn_workspace(lib.dit_attention_packed_workspace_size, args, workspace,
+                                              q.device)
+        if out is None:
+            out = (torch.empty if args.fill_rest else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(_lse_shape(q), dtype=torch.float32, device=q.device)
+            if not args.fill_rest:
+                lse.fill_(-float("inf"))
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must match q in shape and dtype")
+    _check_lse(lse, q)
+    ctx, stream_ptr = _call_context(q, (k, v, out, lse, offsets, kv_offsets, workspace), stream)
+    with ctx:
+        status = lib.dit_attention_packed(args, _attn_tensor(q, "q"), _attn_tensor(k, "k"),
+                                          _attn_tensor(v, "v"), _attn_tensor(out, "out"), _ptr(lse),
+                                          _ptr(workspace), ws_bytes, stream_ptr)
+    _check(status)
+    return out, lse
+
+
+def attention_packed_backward(dout, q, k, v, out, lse, offsets, *, kv_offsets=None, causal: bool = False,
+                              scale: float | None = None, dq=None, dk=None, dv=None, workspace=None,
+                              stream=None):
+    """Backward pass of ``attention_packed``; returns ``(dq, dk, dv)``.
+
+    The arguments are those of the forward call and of ``attention_backward``.
+    Rows of no sequence are left as they are in gradients that are given, and 0
+    in those made here.
+    """
+    torch = _torch()
+    lib = load_library()
+    args = _packed_args(q, k, v, offsets, kv_offsets, causal, scale, dq is None and dk is None and dv is None)
+    make = torch.empty if args.fill_rest else torch.zeros
+    with _launch_stream_context(q, stream):
+        workspace, ws_bytes = _attn_workspace(lib.dit_attention_packed_backward_workspace_size, args,
+                                              workspace, q.device)
+        if dq is None:
+            dq = make(q.shape, dtype=q.dtype, device=q.device)
+        if dk is None:
+            dk = make(k.shape, dtype=k.dtype, device=k.device)
+        if dv is None:
+            dv = make(v.shape, dtype=v.dtype, device=v.device)
+    for name, t, like in (("dout", dout, q), ("out", out, q), ("dq", dq, q), ("dk", dk, k),
+                          ("dv", dv, v)):
+        if t.shape != like.shape or t.dtype != like.dtype:
+            raise ValueError("%s must match %s in shape and dtype"
+                             % (name, {"dk": "k", "dv": "v"}.get(name, "q")))
+    _check_lse(lse, q)
+    ctx, stream_ptr = _call_context(q, (dout, k, v, out, lse, dq, dk, dv, offsets, kv_offsets, workspace),
+                                    stream)
+    with ctx:
+        status = lib.dit_attention_packed_backward(
             args, _attn_tensor(dout, "dout"), _attn_tensor(q, "q"), _attn_tensor(k, "k"),
             _attn_tensor(v, "v"), _attn_tensor(out, "out"), _ptr(lse), _attn_tensor(dq, "dq"),
             _attn_tensor(dk, "dk"), _attn_tensor(dv, "dv"), _ptr(workspace), ws_bytes, stream_ptr)

@@ -53,6 +53,36 @@ struct BwdParams {
     float* value_norms;                       // fp16: [batch][kv_heads][value_blocks] largest |v|
     float* part_kv;                           // [row_splits][pairs][kv_tokens][dk, dv][D]
     float* part_q;                            // [key_splits][pairs][rows][D]
+    Rows q_rows, kv_rows;                     // packed sequences (batch is 1, rows all of the buffer's)
+    int32_t fill_rest;
+};
+
+// Block `block` of SIZE rows (times `group`) of packed sequences.
+template <int SIZE>
+struct PackedBlock {
+    int seq, at;              // the sequence, and the block's place in it
+    int q_at, kv_at;          // the sequence's first rows
+    int q_tokens, kv_tokens;
+
+    // `of`: q_rows or kv_rows, by which the blocks are numbered
+    __device__ __forceinline__ PackedBlock(const BwdParams& p, const Rows& of, int group, int block)
+    {
+        seq = sequence_of<SIZE>(of, group, block);
+        at = __builtin_amdgcn_readfirstlane(block - first_block<SIZE>(of, group, seq));
+        const int q0 = p.q_rows.first(seq), k0 = p.kv_rows.first(seq);
+        const int q = p.q_rows.first(seq + 1) - q0, k = p.kv_rows.first(seq + 1) - k0;
+        q_at = __builtin_amdgcn_readfirstlane(q0);
+        kv_at = __builtin_amdgcn_readfirstlane(k0);
+        q_tokens = __builtin_amdgcn_readfirstlane(q < 0 ? 0 : q);
+        kv_tokens = __builtin_amdgcn_readfirstlane(k < 0 ? 0 : k);
+    }
+
+    // Whether rows `rows` (of the sequence, times the group) begin before this block and
+    // are anybody's.
+    __device__ __forceinline__ bool there(const BwdParams& p, int rows) const
+    {
+        return at >= 0 && at < (rows + SIZE - 1) / SIZE && (p.fill_rest || !p.q_rows.rest(seq));
+    }
 };
 
 template <bool F16>
@@ -87,7 +117,9 @@ constexpr int value_rows(int d) { return 4 * 256 / (d / 8); }
 // not what two orders of summation differ by.  The fragments that takes, 16 bytes
 // of a row a lane, cost time: 28 us on 4608 tokens of 48 heads of 128, where whole
 // rows summed side by side took 21 (22 at a copy's rate).
-template <int D, bool F16>
+// Packed: blocks are numbered by the sequences, those that no sequence needs have
+// no rows.
+template <int D, bool F16, bool PACKED>
 __global__ __launch_bounds__(256)
 void row_stats_kernel(const BwdParams p)
 {
@@ -98,8 +130,14 @@ void row_stats_kernel(const BwdParams p)
         const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
         const int64_t bh = blockIdx.x / p.stat_blocks, b = bh / p.heads;
         const int h = bh % p.heads;
-        const int64_t qi = (int64_t)(blockIdx.x % p.stat_blocks) * kStatRows + threadIdx.x / 64 * 32 + n;
-        const bool there = qi < p.q_tokens;
+        int64_t qi = (int64_t)(blockIdx.x % p.stat_blocks) * kStatRows + threadIdx.x / 64 * 32 + n;
+        bool there = qi < p.q_tokens;
+        if constexpr (PACKED) {
+            const PackedBlock<kStatRows> of(p, p.q_rows, 1, (int)(blockIdx.x % p.stat_blocks));
+            qi = (int64_t)of.at * kStatRows + threadIdx.x / 64 * 32 + n;
+            there = of.at >= 0 && qi < of.q_tokens && !p.q_rows.rest(of.seq);
+            qi += of.q_at;
+        }
         const uint16_t* dor = p.dout + b * p.do_bs + qi * p.do_ts + h * p.do_hs + 8 * g;
         const uint16_t* outr = p.out + b * p.o_bs + qi * p.o_ts + h * p.o_hs + 8 * g;
         u32x4 df[D / 16], of[D / 16];
@@ -144,9 +182,16 @@ void row_stats_kernel(const BwdParams p)
         if (p.kv_lengths && p.kv_lengths[b] < len)
             len = p.kv_lengths[b];
         const uint16_t* vr = p.v + b * p.v_bs + bh % p.kv_heads * p.v_hs + d0;
+        int64_t first = at % p.value_blocks * value_rows(D);
+        if constexpr (PACKED) {
+            const PackedBlock<value_rows(D)> of(p, p.kv_rows, 1, (int)(at % p.value_blocks));
+            first = of.at < 0 ? 0 : (int64_t)of.at * value_rows(D);
+            len = of.at < 0 || p.q_rows.rest(of.seq) ? 0 : of.kv_tokens;
+            vr += of.kv_at * p.v_ts;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t j = at % p.value_blocks * value_rows(D) + i * R + row0;
+            const int64_t j = first + i * R + row0;
             float x[8], sq = 0.0f;
             unpack8<true>(j < len ? load16<false>(vr + j * p.v_ts) : u32x4{0, 0, 0, 0}, x);
 #pragma unroll
@@ -174,6 +219,20 @@ __device__ __forceinline__ float largest(const float* v, int n, float* slot)
     return block_max<4>(top, slot);
 }
 
+// The largest of what row_stats_kernel left of blocks of SIZE rows for a sequence
+// of packed ones, of `heads` heads from `head` on (of `blocks` values each).
+template <int SIZE>
+__device__ __forceinline__ float largest_packed(const float* v, int64_t head, int heads, int blocks,
+                                                const Rows& rows, int seq, int tokens, float* slot)
+{
+    const int first = first_block<SIZE>(rows, 1, seq), n = (tokens + SIZE - 1) / SIZE;
+    float top = 0.0f;
+    for (int h = 0; h < heads; ++h)
+        for (int i = threadIdx.x; i < n; i += 256)
+            top = fmaxf(top, v[(head + h) * blocks + first + i]);
+    return block_max<4>(top, slot);
+}
+
 // ---------------------------------------------------------------- dk and dv
 
 constexpr int kWaves = 4;
@@ -197,7 +256,7 @@ constexpr int kFewRows = 32;
 // scores of all and half the columns of dk and dv.  That is 6 products for 4, but
 // twice the workgroups, for calls that leave CUs idle (8 heads of 512 tokens: 44
 // against 55 us; 16 heads of 4096, which do not: 1409 against 1083).
-template <int D, bool F16, bool CAUSAL, bool TWO, int DS>
+template <int D, bool F16, bool CAUSAL, bool TWO, int DS, bool PACKED>
 __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* lds, float* tops,
                                               uint32_t bid)
 {
@@ -211,16 +270,29 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     // causal: the first key blocks are seen by most queries; turning the order
     // from split to split keeps them from meeting on the same CUs
     const int split = block.part / p.key_blocks;
-    const int kb = (block.part + (CAUSAL ? split : 0)) % p.key_blocks;
+    int kb = (block.part + (CAUSAL ? split : 0)) % p.key_blocks;
     const uint32_t bh = block.pair;
     const int64_t b = bh / (uint32_t)p.kv_heads;
     const int hk = bh % (uint32_t)p.kv_heads;
-    int len = p.kv_tokens;
-    if (p.kv_lengths) {
+    int len = p.kv_tokens, seq = 0;
+    int q_tokens = p.q_tokens, kv_tokens = p.kv_tokens;
+    int64_t q_at = 0, kv_at = 0;           // the sequence's first rows
+    if constexpr (PACKED) {
+        const PackedBlock<BK> of(p, p.kv_rows, 1, kb);
+        if (!of.there(p, of.kv_tokens))
+            return;
+        seq = of.seq;
+        kb = of.at;
+        q_at = of.q_at;
+        kv_at = of.kv_at;
+        kv_tokens = of.kv_tokens;
+        q_tokens = p.q_rows.rest(seq) ? 0 : of.q_tokens;
+        len = q_tokens ? kv_tokens : 0;
+    } else if (p.kv_lengths) {
         const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
         len = given < 0 ? 0 : given < len ? given : len;
     }
-    const int shift = p.kv_tokens - p.q_tokens;
+    const int shift = kv_tokens - q_tokens;
     const int k0 = kb * BK + wave / DS * 32;              // the wave's first key
     const int key = k0 + n;                               // this lane's
     const int db0 = DS == 1 ? 0 : wave % DS * DB;         // the wave's first column block
@@ -230,7 +302,7 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
         const int i = kb * BK - shift;
         first = i > 0 ? i / BQ : 0;
     }
-    const int tiles = (p.q_tokens + BQ - 1) / BQ;
+    const int tiles = (q_tokens + BQ - 1) / BQ;
     const int per = tiles > first ? tiles - first : 0;    // tiles of one query head
     const int all = kb * BK < len ? per * p.group : 0;
     const int each = (all + p.row_splits - 1) / p.row_splits;
@@ -247,7 +319,7 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     const bool stages_q = wave < 2;
     const int64_t stage_ts = stages_q ? p.q_ts : p.do_ts;
     const int64_t stage_hs = stages_q ? p.q_hs : p.do_hs;
-    const uint16_t* stage_base = stages_q ? p.q + b * p.q_bs : p.dout + b * p.do_bs;
+    const uint16_t* stage_base = (stages_q ? p.q + b * p.q_bs : p.dout + b * p.do_bs) + q_at * stage_ts;
     const Stager<D> rows(lane, stage_ts);
     const uint32_t lds0 = lds_address(lds);
     uint32_t fill = lds0;
@@ -257,21 +329,21 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     // h and next_q: the next one to be staged
     int h = hk * p.group + (per ? t0 / per : 0), next_q = (first + (per ? t0 % per : 0)) * BQ;
     const auto stage = [&](int buf) {
-        const int left = p.q_tokens - next_q;
+        const int left = q_tokens - next_q;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             rows.load(stage_base + (int64_t)next_q * stage_ts + h * stage_hs, stage_ts, left,
                       fill + (stages_q ? 0 : kTile), (wave & 1) * 2 + i);
         if (wave < 2) {           // lse2 and delta: zero past the last query, as are its rows
             const uint64_t a = reinterpret_cast<uint64_t>(
-                p.stats + ((b * p.heads + h) * p.q_tokens + next_q) * 2);
+                p.stats + ((b * p.heads + h) * p.q_tokens + q_at + next_q) * 2);
             const u32x4 rsrc = {scalar((uint32_t)a), scalar((uint32_t)(a >> 32) & 0xffffu),
                                 scalar((left < BQ ? left : BQ) * 8), kRawBuffer};
             dma4(rsrc, wave * 256 + lane * 4, lds0 + 4 * kTile + buf * BQ * 8 + wave * 256);
         }
         fill ^= 2 * kTile;
         next_q += BQ;
-        if (next_q >= p.q_tokens) {
+        if (next_q >= q_tokens) {
             next_q = first * BQ;
             ++h;
         }
@@ -282,8 +354,8 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
         stage(0);                 // before k and v: the waits run together
     u32x4 kf[D / 16], vf[D / 16];
     {
-        const uint16_t* kr = p.k + b * p.k_bs + (int64_t)key * p.k_ts + hk * p.k_hs + 8 * g;
-        const uint16_t* vr = p.v + b * p.v_bs + (int64_t)key * p.v_ts + hk * p.v_hs + 8 * g;
+        const uint16_t* kr = p.k + b * p.k_bs + (kv_at + key) * p.k_ts + hk * p.k_hs + 8 * g;
+        const uint16_t* vr = p.v + b * p.v_bs + (kv_at + key) * p.v_ts + hk * p.v_hs + 8 * g;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             kf[kk] = key < len ? load16<false>(kr + 16 * kk) : u32x4{0, 0, 0, 0};
@@ -294,9 +366,15 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     int e = 0;
     if constexpr (F16) {
         const int n = p.group * p.stat_blocks;
-        e = __builtin_amdgcn_readfirstlane(
-                bound_exponent(largest(p.row_norms + bh * n, n, tops) *
-                               largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops + 4))) + 1;
+        float bound;
+        if constexpr (PACKED)
+            bound = largest_packed<kStatRows>(p.row_norms, (int64_t)hk * p.group, p.group, p.stat_blocks, p.q_rows, seq,
+                                              q_tokens, tops) *
+                    largest_packed<value_rows(D)>(p.value_norms, hk, 1, p.value_blocks, p.kv_rows, seq, len, tops + 4);
+        else
+            bound = largest(p.row_norms + bh * n, n, tops) *
+                    largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops + 4);
+        e = __builtin_amdgcn_readfirstlane(bound_exponent(bound)) + 1;
         down = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
 #pragma unroll
@@ -385,8 +463,8 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
         __asm__ volatile("" : "+v"(lane_now));
     }
     const int gs = lane_now >> 5, ks = k0 + (lane_now & 31);
-    const bool valid = ks < p.kv_tokens;
-    const int64_t to = valid ? ks : p.kv_tokens - 1;
+    const bool valid = ks < kv_tokens;
+    const int64_t to = kv_at + (valid ? ks : kv_tokens - 1);
     const float fv = F16 ? 0x1p-15f : 1.0f;
     const float fk = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
     const bool seen = ks < len;   // the scores of a padding key are no scores
@@ -414,7 +492,7 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
 
 // ---------------------------------------------------------------- dq
 
-template <int D, bool F16, bool CAUSAL, bool TWO>
+template <int D, bool F16, bool CAUSAL, bool TWO, bool PACKED>
 __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* lds, float* tops,
                                                 uint32_t bid)
 {
@@ -429,19 +507,32 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
     const uint32_t bh = block.pair;
     const int64_t b = bh / (uint32_t)p.kv_heads;
     const int hk = bh % (uint32_t)p.kv_heads;
-    const int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;
-    int len = p.kv_tokens;
-    if (p.kv_lengths) {
+    int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;
+    int len = p.kv_tokens, seq = 0, rows = p.rows;
+    int q_tokens = p.q_tokens, kv_tokens = p.kv_tokens;
+    int64_t q_at = 0, kv_at = 0;           // the sequence's first rows
+    if constexpr (PACKED) {
+        const PackedBlock<BM> of(p, p.q_rows, p.group, mb_raw);
+        seq = of.seq;
+        q_tokens = of.q_tokens;
+        rows = q_tokens * p.group;
+        if (!of.there(p, rows))
+            return;
+        mb = CAUSAL ? (rows + BM - 1) / BM - 1 - of.at : of.at;
+        kv_tokens = len = p.q_rows.rest(seq) ? 0 : of.kv_tokens;
+        q_at = of.q_at;
+        kv_at = of.kv_at;
+    } else if (p.kv_lengths) {
         const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
         len = given < 0 ? 0 : given < len ? given : len;
     }
     const int r0 = mb * BM + wave * 32;
-    const int r = r0 + n < p.rows ? r0 + n : p.rows - 1;
+    const int r = r0 + n < rows ? r0 + n : rows - 1;
     const int qi = r / p.group, head = hk * p.group + r % p.group;
-    const int shift = p.kv_tokens - p.q_tokens;
+    const int shift = kv_tokens - q_tokens;
     int end = len;
     if (CAUSAL) {
-        const int last = (mb * BM + BM < p.rows ? mb * BM + BM : p.rows) - 1;
+        const int last = (mb * BM + BM < rows ? mb * BM + BM : rows) - 1;
         const int sees = last / p.group + shift + 1;
         end = sees < end ? (sees < 0 ? 0 : sees) : end;
     }
@@ -451,7 +542,7 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
     const int tiles = all < t0 + each ? all : t0 + each;
     int open = len;
     if (CAUSAL) {
-        const int s = (r0 < p.rows ? r0 : p.rows - 1) / p.group + shift + 1;
+        const int s = (r0 < rows ? r0 : rows - 1) / p.group + shift + 1;
         open = s < open ? s : open;
     }
 
@@ -461,8 +552,8 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
         dq[i] = f32x16{};
 
     const Stager<D> ks(lane, p.k_ts), vs(lane, p.v_ts);
-    const uint16_t* kbase = p.k + b * p.k_bs + hk * p.k_hs;
-    const uint16_t* vbase = p.v + b * p.v_bs + hk * p.v_hs;
+    const uint16_t* kbase = p.k + b * p.k_bs + kv_at * p.k_ts + hk * p.k_hs;
+    const uint16_t* vbase = p.v + b * p.v_bs + kv_at * p.v_ts + hk * p.v_hs;
     uint32_t fill = lds_address(lds);
     TileAt at(fill, lane);
     const auto stage = [&](int t) {
@@ -478,15 +569,15 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
         stage(t0);                // before q and dout: the waits run together
     u32x4 qf[D / 16], df[D / 16];
     {
-        const uint16_t* qr = p.q + b * p.q_bs + qi * p.q_ts + head * p.q_hs + 8 * g;
-        const uint16_t* dr = p.dout + b * p.do_bs + qi * p.do_ts + head * p.do_hs + 8 * g;
+        const uint16_t* qr = p.q + b * p.q_bs + (q_at + qi) * p.q_ts + head * p.q_hs + 8 * g;
+        const uint16_t* dr = p.dout + b * p.do_bs + (q_at + qi) * p.do_ts + head * p.do_hs + 8 * g;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             qf[kk] = load16<false>(qr + 16 * kk);
             df[kk] = load16<false>(dr + 16 * kk);
         }
     }
-    const f32x2 st = reinterpret_cast<const f32x2*>(p.stats)[(b * p.heads + head) * p.q_tokens + qi];
+    const f32x2 st = reinterpret_cast<const f32x2*>(p.stats)[(b * p.heads + head) * p.q_tokens + q_at + qi];
     const float delta = st.y;
     int e = 0;
     if constexpr (F16) {
@@ -499,8 +590,12 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
             for (int i = 0; i < 8; ++i)
                 sq = __builtin_fmaf(x[i], x[i], sq);
         }
-        e = bound_exponent(sqrtf(half_sum(sq)) *
-                           largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops)) + 1;
+        float top;
+        if constexpr (PACKED)
+            top = largest_packed<value_rows(D)>(p.value_norms, hk, 1, p.value_blocks, p.kv_rows, seq, len, tops);
+        else
+            top = largest(p.value_norms + bh * p.value_blocks, p.value_blocks, tops);
+        e = bound_exponent(sqrtf(half_sum(sq)) * top) + 1;
     }
     // ds alone is needed here, so its power of two goes into the exponent of p
     const float lse2 = st.x + (float)e;
@@ -554,15 +649,15 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
         at.flip(2 * kTile);
     }
 
-    const bool valid = r0 + n < p.rows;
+    const bool valid = r0 + n < rows;
     const float f = F16 ? __builtin_amdgcn_ldexpf(p.scale, e - 15) : p.scale;
     if (p.key_splits == 1) {
-        uint16_t* row = p.dq + b * p.dq_bs + qi * p.dq_ts + head * p.dq_hs;
+        uint16_t* row = p.dq + b * p.dq_bs + (q_at + qi) * p.dq_ts + head * p.dq_hs;
 #pragma unroll
         for (int i = 0; i < DB; ++i)
             store_column<F16>(row + 32 * i, dq[i], f, g, valid);
     } else {
-        float* row = p.part_q + ((split * (int64_t)p.pairs + bh) * p.rows + r) * D;
+        float* row = p.part_q + ((split * (int64_t)p.pairs + bh) * p.rows + q_at * p.group + r) * D;
 #pragma unroll
         for (int i = 0; i < DB; ++i)
             store_column_f32(row + 32 * i, dq[i], f, g, valid);
@@ -595,15 +690,30 @@ void attention_backward_kernel(const BwdParams p)
     const uint32_t first = p.pairs * (uint32_t)(p.key_blocks * p.row_splits);
     if (blockIdx.x < first) {
         if (D == 256 && p.column_waves == 2)
-            key_gradients<D, F16, CAUSAL, TWO, D == 256 ? 2 : 1>(p, lds, tops, blockIdx.x);
+            key_gradients<D, F16, CAUSAL, TWO, D == 256 ? 2 : 1, false>(p, lds, tops, blockIdx.x);
         else
-            key_gradients<D, F16, CAUSAL, TWO, 1>(p, lds, tops, blockIdx.x);
+            key_gradients<D, F16, CAUSAL, TWO, 1, false>(p, lds, tops, blockIdx.x);
     } else
-        query_gradients<D, F16, CAUSAL, TWO>(p, lds, tops, blockIdx.x - first);
+        query_gradients<D, F16, CAUSAL, TWO, false>(p, lds, tops, blockIdx.x - first);
+}
+
+// The same of packed sequences, with one term of p and ds and whole blocks of keys.
+template <int D, bool F16, bool CAUSAL>
+__global__ __launch_bounds__(kWaves * 64, backward_waves(D, F16, false))
+void packed_backward_kernel(const BwdParams p)
+{
+    constexpr int kTiles = 4 * kTileRows * D * 2;
+    __shared__ __attribute__((aligned(kTiles))) char lds[kTiles + 2 * kTileRows * 8];
+    __shared__ float tops[8];
+    const uint32_t first = p.pairs * (uint32_t)(p.key_blocks * p.row_splits);
+    if (blockIdx.x < first)
+        key_gradients<D, F16, CAUSAL, false, 1, true>(p, lds, tops, blockIdx.x);
+    else
+        query_gradients<D, F16, CAUSAL, false, true>(p, lds, tops, blockIdx.x - first);
 }
 
 // Adds the splits' dk and dv, or dq, in order: D / 8 threads a row.
-template <int D, bool F16, bool KV>
+template <int D, bool F16, bool KV, bool PACKED>
 __global__ __launch_bounds__(256)
 void attention_sum_kernel(const BwdParams p)
 {
@@ -612,6 +722,12 @@ void attention_sum_kernel(const BwdParams p)
     const int64_t at = (int64_t)blockIdx.x * R + threadIdx.x / L;
     if (at >= rows)
         return;
+    if constexpr (PACKED) {                // rows of no sequence may have to be left alone
+        const Rows& of = KV ? p.kv_rows : p.q_rows;
+        const int64_t token = KV ? at / 2 % p.kv_tokens : at % p.rows / p.group;
+        if (!p.fill_rest && (token < of.first(1) || token >= of.first(of.sequences + 1)))
+            return;
+    }
     const int d0 = threadIdx.x % L * 8;
     const float* part = (KV ? p.part_kv : p.part_q) + at * D + d0;
     const int splits = KV ? p.row_splits : p.key_splits;
@@ -659,28 +775,33 @@ int64_t splits_of(int64_t blocks, int64_t resident, int64_t tiles, int64_t least
     return fill < most ? fill : most;
 }
 
-Shape shape_of(const dit_attn_args& a)
+// Packed sequences (`packed`; a's sizes are the buffers') are cut as one sequence of
+// all rows would be: a workgroup divides what its own sequence leaves.
+Shape shape_of(const dit_attn_args& a, const dit_attn_packed_args* packed)
 {
     Shape s;
     const int64_t group = a.heads / a.kv_heads, rows = a.q_tokens * group;
     const int64_t pairs = a.batch * a.kv_heads;
     constexpr int64_t per = 32 * kWaves;
-    s.row_blocks = (rows + per - 1) / per;
+    const auto blocks_of = [&](int64_t n, int64_t size) {
+        return packed ? qkr_attn_host::blocks_of(n, packed->sequences, size) : (n + size - 1) / size;
+    };
+    s.row_blocks = blocks_of(rows, per);
     // workgroups resident at once (head_dim 64 would hold 3 a CU, but its sums of
     // more parts cost what that gains: 33 us with 2 as with 3 on 12 x 8 blocks)
     const int64_t resident = 256 * (a.head_dim == 256 ? 1 : 2);
     s.key_splits = splits_of(pairs * s.row_blocks, resident, (a.kv_tokens + 63) / 64, 8);
     // head_dim 256: two waves to a block of keys if all workgroups still run at once
-    for (s.column_waves = a.head_dim == 256 ? 2 : 1;; s.column_waves = 1) {
+    for (s.column_waves = a.head_dim == 256 && !packed ? 2 : 1;; s.column_waves = 1) {
         const int64_t keys = per / s.column_waves;
-        s.key_blocks = (a.kv_tokens + keys - 1) / keys;
+        s.key_blocks = blocks_of(a.kv_tokens, keys);
         s.row_splits = splits_of(pairs * s.key_blocks, resident, (a.q_tokens + 63) / 64 * group, 8);
         if (s.column_waves == 1 ||
             pairs * (s.key_blocks * s.row_splits + s.row_blocks * s.key_splits) <= resident)
             break;
     }
-    s.stat_blocks = (a.q_tokens + kStatRows - 1) / kStatRows;
-    s.value_blocks = (a.kv_tokens + value_rows(a.head_dim) - 1) / value_rows(a.head_dim);
+    s.stat_blocks = blocks_of(a.q_tokens, kStatRows);
+    s.value_blocks = blocks_of(a.kv_tokens, value_rows(a.head_dim));
     const auto whole = [](int64_t n) { return (n + 3) / 4 * 4; };
     s.row_norms = whole(a.batch * a.heads * a.q_tokens * 2);
     s.value_norms = s.row_norms + whole(a.batch * a.heads * s.stat_blocks);
@@ -690,7 +811,7 @@ Shape shape_of(const dit_attn_args& a)
     return s;
 }
 
-template <int D, bool F16, bool CAUSAL>
+template <int D, bool F16, bool CAUSAL, bool PACKED>
 hipError_t launch(BwdParams p, hipStream_t st)
 {
     constexpr int R = 256 / (D / 8);
@@ -702,47 +823,40 @@ hipError_t launch(BwdParams p, hipStream_t st)
             err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)blocks), dim3(256),
                                   argv, 0, st);
     };
-    go(row_stats_kernel<D, F16>, p.batch * p.heads * p.stat_blocks + (F16 ? pairs * p.value_blocks : 0));
-    go(p.rows <= kFewRows ? attention_backward_kernel<D, F16, CAUSAL, true>
-                          : attention_backward_kernel<D, F16, CAUSAL, false>,
+    go(row_stats_kernel<D, F16, PACKED>, p.batch * p.heads * p.stat_blocks + (F16 ? pairs * p.value_blocks : 0));
+    go(PACKED                ? packed_backward_kernel<D, F16, CAUSAL>
+       : p.rows <= kFewRows ? attention_backward_kernel<D, F16, CAUSAL, true>
+                            : attention_backward_kernel<D, F16, CAUSAL, false>,
        pairs * ((int64_t)p.key_blocks * p.row_splits + (int64_t)p.row_blocks * p.key_splits));
     if (p.row_splits > 1)
-        go(attention_sum_kernel<D, F16, true>, (pairs * 2 * p.kv_tokens + R - 1) / R);
+        go(attention_sum_kernel<D, F16, true, PACKED>, (pairs * 2 * p.kv_tokens + R - 1) / R);
     if (p.key_splits > 1)
-        go(attention_sum_kernel<D, F16, false>, (pairs * p.rows + R - 1) / R);
+        go(attention_sum_kernel<D, F16, false, PACKED>, (pairs * p.rows + R - 1) / R);
     return err;
 }
 
-template <int D>
+template <int D, bool PACKED>
 hipError_t launch(const BwdParams& p, bool f16, bool causal, hipStream_t st)
 {
     if (f16)
-        return causal ? launch<D, true, true>(p, st) : launch<D, true, false>(p, st);
-    return causal ? launch<D, false, true>(p, st) : launch<D, false, false>(p, st);
+        return causal ? launch<D, true, true, PACKED>(p, st) : launch<D, true, false, PACKED>(p, st);
+    return causal ? launch<D, false, true, PACKED>(p, st) : launch<D, false, false, PACKED>(p, st);
 }
 
-}  // namespace
-
-extern "C" int64_t dit_attention_backward_workspace_size(const dit_attn_args* args)
+template <int D>
+hipError_t launch(const BwdParams& p, bool f16, bool causal, bool packed, hipStream_t st)
 {
-    const int rc = qkr_attn_host::check_args(args);
-    return rc != QKR_OK ? rc : shape_of(*args).floats * 4;
+    return packed ? launch<D, true>(p, f16, causal, st) : launch<D, false>(p, f16, causal, st);
 }
 
-extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_tensor* dout,
-                                      const dit_attn_tensor* q, const dit_attn_tensor* k,
-                                      const dit_attn_tensor* v, const dit_attn_tensor* out,
-                                      const float* lse, const dit_attn_tensor* dq,
-                                      const dit_attn_tensor* dk, const dit_attn_tensor* dv,
-                                      void* workspace, int64_t workspace_bytes, void* stream)
+// Both entry points, after the checks of their sizes.
+int backward(const dit_attn_args& a, const dit_attn_packed_args* packed, const dit_attn_tensor* dout,
+             const dit_attn_tensor* q, const dit_attn_tensor* k, const dit_attn_tensor* v,
+             const dit_attn_tensor* out, const float* lse, const dit_attn_tensor* dq, const dit_attn_tensor* dk,
+             const dit_attn_tensor* dv, void* workspace, int64_t workspace_bytes, void* stream)
 {
     using namespace qkr_attn_host;
-    int rc = check_args(args);
-    if (rc != QKR_OK)
-        return rc;
-    const dit_attn_args& a = *args;
-    if (a.batch == 0 || (a.q_tokens == 0 && a.kv_tokens == 0))
-        return QKR_OK;
+    int rc;
     const Extent eq = {a.q_tokens, a.heads}, ekv = {a.kv_tokens, a.kv_heads};
     const struct { dit_attn_tensor t; Extent e; } all[] = {
         {plain(a, dout, eq), eq}, {plain(a, q, eq), eq}, {plain(a, k, ekv), ekv}, {plain(a, v, ekv), ekv},
@@ -752,17 +866,17 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
             return rc;
     if (a.q_tokens && !lse)
         return QKR_ERR_NULL;
-    if (reinterpret_cast<uintptr_t>(lse) & 3u || reinterpret_cast<uintptr_t>(a.kv_lengths) & 3u)
+    const Lengths lengths(a, packed);
+    if (reinterpret_cast<uintptr_t>(lse) & 3u || !lengths.aligned())
         return QKR_ERR_ALIGN;
-    const int64_t need = dit_attention_backward_workspace_size(args);
+    const int64_t need = shape_of(a, packed).floats * 4;
     if (need && (!workspace || workspace_bytes < need))
         return QKR_ERR_WORKSPACE;
     if (!qkr_host::aligned16(workspace))
         return QKR_ERR_ALIGN;
     const Range lse_r = {lse, (uint64_t)a.batch * a.heads * a.q_tokens * 4};
     const Range ws_r = {workspace, (uint64_t)need};
-    const Range len_r = {a.kv_lengths, a.kv_lengths ? (uint64_t)a.batch * 4 : 0};
-    if (meet(ws_r, lse_r) || meet(ws_r, len_r))
+    if (meet(ws_r, lse_r) || meet(ws_r, lengths.range[0]) || meet(ws_r, lengths.range[1]))
         return QKR_ERR_ARG;
     for (int i = 0; i < 8; ++i) {
         const Range x = range(a, all[i].t, all[i].e);
@@ -770,7 +884,7 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
             return QKR_ERR_ARG;
         if (i < 5)
             continue;
-        if (meet(x, lse_r) || meet(x, len_r))
+        if (meet(x, lse_r) || meet(x, lengths.range[0]) || meet(x, lengths.range[1]))
             return QKR_ERR_ARG;
         for (int j = 0; j < i; ++j)
             if (may_meet(a, all[i].t, all[i].e, all[j].t, all[j].e))
@@ -788,6 +902,12 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     unpack(all[7].t, p.dv, p.dv_bs, p.dv_ts, p.dv_hs);
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
+    if (packed) {
+        p.q_rows = Rows{packed->q_offsets, (int32_t)packed->sequences, (int32_t)a.q_tokens};
+        p.kv_rows = Rows{packed->kv_offsets ? packed->kv_offsets : packed->q_offsets, (int32_t)packed->sequences,
+                         (int32_t)a.kv_tokens};
+        p.fill_rest = packed->fill_rest;
+    }
     p.batch = a.batch;
     p.pairs = (uint32_t)(a.batch * a.kv_heads);
     p.q_tokens = (int32_t)a.q_tokens;
@@ -799,7 +919,7 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     p.scale = a.scale;
     p.c = a.scale * kLog2e;
     p.stats = static_cast<float*>(workspace);
-    const Shape shape = shape_of(a);
+    const Shape shape = shape_of(a, packed);
     p.row_blocks = (int32_t)shape.row_blocks;
     p.key_blocks = (int32_t)shape.key_blocks;
     p.column_waves = (int32_t)shape.column_waves;
@@ -813,8 +933,52 @@ extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_
     p.part_q = p.stats + shape.part_q;
     const bool f16 = a.dtype == QKR_FP16, causal = a.causal != 0;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const hipError_t err = a.head_dim == 64    ? launch<64>(p, f16, causal, st)
-                           : a.head_dim == 128 ? launch<128>(p, f16, causal, st)
-                                               : launch<256>(p, f16, causal, st);
+    const hipError_t err = a.head_dim == 64    ? launch<64>(p, f16, causal, packed, st)
+                           : a.head_dim == 128 ? launch<128>(p, f16, causal, packed, st)
+                                               : launch<256>(p, f16, causal, packed, st);
     return err == hipSuccess ? QKR_OK : QKR_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" int64_t dit_attention_backward_workspace_size(const dit_attn_args* args)
+{
+    const int rc = qkr_attn_host::check_args(args);
+    return rc != QKR_OK ? rc : shape_of(*args, nullptr).floats * 4;
+}
+
+extern "C" int dit_attention_backward(const dit_attn_args* args, const dit_attn_tensor* dout,
+                                      const dit_attn_tensor* q, const dit_attn_tensor* k,
+                                      const dit_attn_tensor* v, const dit_attn_tensor* out,
+                                      const float* lse, const dit_attn_tensor* dq,
+                                      const dit_attn_tensor* dk, const dit_attn_tensor* dv,
+                                      void* workspace, int64_t workspace_bytes, void* stream)
+{
+    const int rc = qkr_attn_host::check_args(args);
+    if (rc != QKR_OK || args->batch == 0 || (args->q_tokens == 0 && args->kv_tokens == 0))
+        return rc;
+    return backward(*args, nullptr, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes, stream);
+}
+
+extern "C" int64_t dit_attention_packed_backward_workspace_size(const dit_attn_packed_args* args)
+{
+    dit_attn_args a;
+    const int rc = qkr_attn_host::check_packed(args, a);
+    return rc != QKR_OK ? rc : shape_of(a, args).floats * 4;
+}
+
+extern "C" int dit_attention_packed_backward(const dit_attn_packed_args* args, const dit_attn_tensor* dout,
+                                             const dit_attn_tensor* q, const dit_attn_tensor* k,
+                                             const dit_attn_tensor* v, const dit_attn_tensor* out,
+                                             const float* lse, const dit_attn_tensor* dq,
+                                             const dit_attn_tensor* dk, const dit_attn_tensor* dv,
+                                             void* workspace, int64_t workspace_bytes, void* stream)
+{
+    dit_attn_args a;
+    const int rc = qkr_attn_host::check_packed(args, a);
+    if (rc != QKR_OK || (a.q_tokens == 0 && a.kv_tokens == 0))
+        return rc;
+    if (!args->q_offsets)
+        return QKR_ERR_NULL;
+    return backward(a, args, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes, stream);
 }

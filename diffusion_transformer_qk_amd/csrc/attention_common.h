@@ -67,6 +67,56 @@ struct BlockOf {
     }
 };
 
+// Packed sequences: sequence i of `sequences` has rows offsets[i] .. offsets[i + 1]
+// - 1 of a buffer of `total` rows.  The buffer's rows before the first and behind
+// the last are counted as sequences 0 and sequences + 1 here (the others are one
+// further), which have no keys.  Offsets are clamped to the buffer, so that none,
+// whatever it holds, leads out of it.
+struct Rows {
+    const int32_t* offsets;
+    int32_t sequences, total;
+
+    __device__ __forceinline__ int first(int seq) const
+    {
+        if (seq == 0)
+            return 0;
+        if (seq > sequences + 1)
+            return total;
+        const int at = offsets[seq - 1];
+        return at < 0 ? 0 : at > total ? total : at;
+    }
+
+    __device__ __forceinline__ bool rest(int seq) const { return seq == 0 || seq > sequences; }
+};
+
+// Rows are dealt to workgroups in blocks of SIZE rows (times `group`) of one
+// sequence: sequence i has the blocks from first(i) * group / SIZE + i on, which
+// leaves each as many as it can need, so that block numbers follow from the
+// offsets without a sum over the sequences before.
+template <int SIZE>
+__device__ __forceinline__ int first_block(const Rows& r, int group, int seq)
+{
+    return r.first(seq) * group / SIZE + seq;
+}
+
+// The sequence of block `block`: 64 of them are looked at a time, by the lanes of
+// a wave, which all get the answer.
+template <int SIZE>
+__device__ __forceinline__ int sequence_of(const Rows& r, int group, int block)
+{
+    const int lane = threadIdx.x % kWave;
+    int low = 0, count = r.sequences + 2;
+    while (count > 1) {
+        const int step = (count + kWave - 1) / kWave, i = lane * step;
+        const bool before = i < count && first_block<SIZE>(r, group, low + i) <= block;
+        const int n = __builtin_popcountll(__ballot(before));      // a run from lane 0 on
+        const int skip = n > 0 ? (n - 1) * step : 0;
+        low += skip;
+        count = count - skip < step ? count - skip : step;
+    }
+    return __builtin_amdgcn_readfirstlane(low);
+}
+
 template <bool F16>
 __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
 {

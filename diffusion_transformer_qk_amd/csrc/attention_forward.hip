@@ -38,6 +38,8 @@ struct FwdParams {
     float c;                                  // scale * log2(e)
     float* part_o;                            // [splits][batch * kv_heads * rows][D]
     float* part_lse;                          // [splits][batch * kv_heads * rows], base 2
+    Rows q_rows, kv_rows;                     // packed sequences (batch is 1, rows all of the buffer's)
+    int32_t fill_rest;
 };
 
 // exp2 of the scores is taken relative to 2^-p_shift of the row's maximum, so
@@ -58,9 +60,11 @@ constexpr int waves_per_simd(int d) { return d == 64 ? 4 : d == 128 ? 3 : 2; }
 // and the waves stay four: 32 heads of 4096 take 158 us with 64 keys, 168 with 32.
 constexpr int tile_keys(int d, int waves) { return d == 64 && waves == 4 ? 64 : 32; }
 
-template <int D, bool F16, bool CAUSAL, int NW>
-__global__ __launch_bounds__(NW * 64, NW == 4 ? waves_per_simd(D) : D == 256 ? 1 : 2)
-void attention_forward_kernel(const FwdParams p)
+// Bytes of LDS: [buffer][K, V].
+constexpr int lds_bytes(int d, int waves) { return 4 * tile_keys(d, waves) * d * 2; }
+
+template <int D, bool F16, bool CAUSAL, int NW, bool PACKED>
+__device__ __forceinline__ void forward_block(const FwdParams& p, char* lds)
 {
     constexpr int BM = NW * 32, BN = tile_keys(D, NW), KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
@@ -68,7 +72,6 @@ void attention_forward_kernel(const FwdParams p)
     // what its rounding to 16 bits left: out is then off by its own rounding
     // alone.
     constexpr bool kTwoTerms = NW == 1;
-    __shared__ __attribute__((aligned(4 * kTile))) char lds[4 * kTile];   // [buffer][K, V]
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
@@ -77,20 +80,37 @@ void attention_forward_kernel(const FwdParams p)
     const uint32_t bh = block.pair;                      // sample, key head
     const int64_t b = bh / (uint32_t)p.kv_heads;
     const int hk = bh % (uint32_t)p.kv_heads;
-    const int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;   // the longest first
+    int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;         // the longest first
 
+    int q_tokens = p.q_tokens, kv_tokens = p.kv_tokens, rows = p.rows;
+    int64_t q_at = 0, kv_at = 0;           // the sequence's first rows
     int len = p.kv_tokens;
-    if (p.kv_lengths) {
+    if constexpr (PACKED) {
+        const int seq = sequence_of<BM>(p.q_rows, p.group, mb_raw);
+        const int q0 = p.q_rows.first(seq), k0 = p.kv_rows.first(seq);
+        q_tokens = p.q_rows.first(seq + 1) - q0;
+        kv_tokens = p.q_rows.rest(seq) ? 0 : p.kv_rows.first(seq + 1) - k0;
+        q_tokens = __builtin_amdgcn_readfirstlane(q_tokens < 0 ? 0 : q_tokens);
+        kv_tokens = len = __builtin_amdgcn_readfirstlane(kv_tokens < 0 ? 0 : kv_tokens);
+        q_at = __builtin_amdgcn_readfirstlane(q0);
+        kv_at = __builtin_amdgcn_readfirstlane(k0);
+        rows = q_tokens * p.group;
+        const int blocks = (rows + BM - 1) / BM, at = mb_raw - first_block<BM>(p.q_rows, p.group, seq);
+        mb = __builtin_amdgcn_readfirstlane(CAUSAL ? blocks - 1 - at : at);
+        // more blocks than the sequence needs, or rows that are left alone
+        if (at < 0 || at >= blocks || (p.q_rows.rest(seq) && !p.fill_rest))
+            return;
+    } else if (p.kv_lengths) {
         const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
         len = given < 0 ? 0 : given < len ? given : len;
     }
     const int r0 = mb * BM + wave * 32;
-    const int r = r0 + n < p.rows ? r0 + n : p.rows - 1;          // this lane's row
+    const int r = r0 + n < rows ? r0 + n : rows - 1;              // this lane's row
     const int qi = r / p.group, head = hk * p.group + r % p.group;
-    const int shift = p.kv_tokens - p.q_tokens;                   // causal: sees keys <= qi + shift
+    const int shift = kv_tokens - q_tokens;                       // causal: sees keys <= qi + shift
     int end = len;                                                // keys of the workgroup
     if (CAUSAL) {
-        const int last = (mb * BM + BM < p.rows ? mb * BM + BM : p.rows) - 1;
+        const int last = (mb * BM + BM < rows ? mb * BM + BM : rows) - 1;
         const int sees = last / p.group + shift + 1;
         end = sees < end ? (sees < 0 ? 0 : sees) : end;
     }
@@ -101,13 +121,13 @@ void attention_forward_kernel(const FwdParams p)
     // keys below this are seen by every row of the wave
     int open = len;
     if (CAUSAL) {
-        const int s = (r0 < p.rows ? r0 : p.rows - 1) / p.group + shift + 1;
+        const int s = (r0 < rows ? r0 : rows - 1) / p.group + shift + 1;
         open = s < open ? s : open;
     }
 
     u32x4 qf[D / 16];
     {
-        const uint16_t* row = p.q + b * p.q_bs + qi * p.q_ts + head * p.q_hs + 8 * g;
+        const uint16_t* row = p.q + b * p.q_bs + (q_at + qi) * p.q_ts + head * p.q_hs + 8 * g;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
             qf[kk] = load16<false>(row + 16 * kk);
@@ -119,8 +139,8 @@ void attention_forward_kernel(const FwdParams p)
     float m = -INFINITY, l = 0.0f;         // m in units of log2 (scores times c)
 
     const Stager<D> ks(lane, p.k_ts), vs(lane, p.v_ts);
-    const uint16_t* kbase = p.k + b * p.k_bs + hk * p.k_hs;
-    const uint16_t* vbase = p.v + b * p.v_bs + hk * p.v_hs;
+    const uint16_t* kbase = p.k + b * p.k_bs + kv_at * p.k_ts + hk * p.k_hs;
+    const uint16_t* vbase = p.v + b * p.v_bs + kv_at * p.v_ts + hk * p.v_hs;
     uint32_t fill = lds_address(lds);
     TileAt at(fill, lane);
     const auto stage = [&](int t) {
@@ -220,24 +240,45 @@ void attention_forward_kernel(const FwdParams p)
     }
 
     l = half_sum(l);
-    const bool valid = r0 + n < p.rows;
+    const bool valid = r0 + n < rows;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const float lse2 = l == 0.0f ? -INFINITY : m - p_shift<F16>() + __builtin_amdgcn_logf(l);
     if (p.splits == 1) {
-        uint16_t* row = p.out + b * p.o_bs + qi * p.o_ts + head * p.o_hs;
+        uint16_t* row = p.out + b * p.o_bs + (q_at + qi) * p.o_ts + head * p.o_hs;
 #pragma unroll
         for (int i = 0; i < DB; ++i)
             store_column<F16>(row + 32 * i, o[i], inv, g, valid);
         if (valid && g == 0)
-            p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + qi] = lse2 * kLn2;
+            p.lse[(b * p.kv_heads * p.group + head) * p.q_tokens + q_at + qi] = lse2 * kLn2;
     } else {
-        const int64_t slot = (split * (int64_t)p.pairs + bh) * p.rows + r;
+        const int64_t slot = (split * (int64_t)p.pairs + bh) * p.rows + q_at * p.group + r;
+        if (PACKED && t0 >= t1) {          // a split past the sequence's keys: lse alone says so
+            if (valid && g == 0)
+                p.part_lse[slot] = -INFINITY;
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < DB; ++i)
             store_column_f32(p.part_o + slot * D + 32 * i, o[i], inv, g, valid);
         if (valid && g == 0)
             p.part_lse[slot] = lse2;
     }
+}
+
+template <int D, bool F16, bool CAUSAL, int NW>
+__global__ __launch_bounds__(NW * 64, NW == 4 ? waves_per_simd(D) : D == 256 ? 1 : 2)
+void attention_forward_kernel(const FwdParams p)
+{
+    __shared__ __attribute__((aligned(lds_bytes(D, NW)))) char lds[lds_bytes(D, NW)];
+    forward_block<D, F16, CAUSAL, NW, false>(p, lds);
+}
+
+template <int D, bool F16, bool CAUSAL, int NW>
+__global__ __launch_bounds__(NW * 64, NW == 4 ? waves_per_simd(D) : D == 256 ? 1 : 2)
+void packed_forward_kernel(const FwdParams p)
+{
+    __shared__ __attribute__((aligned(lds_bytes(D, NW)))) char lds[lds_bytes(D, NW)];
+    forward_block<D, F16, CAUSAL, NW, true>(p, lds);
 }
 
 // A row of out and its lse (given in base 2).
@@ -259,7 +300,7 @@ __device__ __forceinline__ void store_joined(const FwdParams& p, int64_t at, int
 // each set takes a row of its own.
 constexpr int kManySplits = 16;
 
-template <int D, bool F16, bool MANY>
+template <int D, bool F16, bool MANY, bool PACKED>
 __global__ __launch_bounds__(256)
 void attention_join_kernel(const FwdParams p)
 {
@@ -269,13 +310,20 @@ void attention_join_kernel(const FwdParams p)
     const int64_t at = MANY ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * S + set;
     float top = -INFINITY, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    bool there = true;                     // rows of no sequence may have to be left alone
+    if constexpr (PACKED) {
+        const int64_t token = at % p.rows / p.group;
+        there = p.fill_rest || (token >= p.q_rows.first(1) && token < p.q_rows.first(p.q_rows.sequences + 1));
+        if (MANY && !there)
+            return;
+    }
     if constexpr (MANY) {
         __shared__ float tops[4];
         for (int k = threadIdx.x; k < p.splits; k += 256)
             top = fmaxf(top, p.part_lse[k * total + at]);
         top = block_max<4>(top, tops);
     } else {
-        if (at >= total)
+        if (at >= total || !there)
             return;
         for (int k = 0; k < p.splits; ++k)
             top = fmaxf(top, p.part_lse[k * total + at]);
@@ -283,7 +331,10 @@ void attention_join_kernel(const FwdParams p)
     const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
     for (int k = MANY ? set : 0; k < p.splits; k += MANY ? S : 1) {
-        const float w = __builtin_amdgcn_exp2f(p.part_lse[k * total + at] - base);
+        const float lse = p.part_lse[k * total + at];
+        if (PACKED && lse == -INFINITY)    // its part may not have been written
+            continue;
+        const float w = __builtin_amdgcn_exp2f(lse - base);
         l += w;
         o += w * *reinterpret_cast<const f32x4*>(p.part_o + (k * total + at) * D + col);
     }
@@ -316,12 +367,18 @@ struct Shape {
 // in flight.  Calls that leave CUs idle cut the keys: into as many runs as fill
 // the chip once, of at least 512 keys (128 for one wave, which waits for memory),
 // or the launch that joins them costs what they save.
-Shape shape_of(const dit_attn_args& a)
+//
+// Packed sequences (`packed`; a's sizes are the buffers'): the lengths are on the
+// device, so what is known is the means.  One wave a block where a sequence has no
+// more than 32 rows in the mean; splits as for one sequence of all keys, where
+// those past a sequence's own keys cost a row's lse each.
+Shape shape_of(const dit_attn_args& a, const dit_attn_packed_args* packed)
 {
     Shape s;
-    const int64_t rows = a.q_tokens * (a.heads / a.kv_heads);
-    s.waves = rows <= 32 ? 1 : 4;
-    s.row_blocks = (rows + 32 * s.waves - 1) / (32 * s.waves);
+    const int64_t rows = a.q_tokens * (a.heads / a.kv_heads), sequences = packed ? packed->sequences : 1;
+    s.waves = rows <= 32 * sequences ? 1 : 4;
+    s.row_blocks = packed ? qkr_attn_host::blocks_of(rows, sequences, 32 * s.waves)
+                          : (rows + 32 * s.waves - 1) / (32 * s.waves);
     const int64_t blocks = s.row_blocks * a.batch * a.kv_heads;
     const int keys = tile_keys(a.head_dim, s.waves);
     const int64_t tiles = (a.kv_tokens + keys - 1) / keys;
@@ -342,53 +399,51 @@ Shape shape_of(const dit_attn_args& a)
 using Fn = void (*)(FwdParams);
 
 template <int D, bool F16, bool CAUSAL>
-Fn select(int waves)
+Fn select(int waves, bool packed)
 {
+    if (packed)
+        return waves == 1 ? packed_forward_kernel<D, F16, CAUSAL, 1> : packed_forward_kernel<D, F16, CAUSAL, 4>;
     return waves == 1 ? attention_forward_kernel<D, F16, CAUSAL, 1>
                       : attention_forward_kernel<D, F16, CAUSAL, 4>;
 }
 
 template <int D>
-Fn select(bool f16, bool causal, int waves)
+Fn select(bool f16, bool causal, int waves, bool packed)
 {
     if (f16)
-        return causal ? select<D, true, true>(waves) : select<D, true, false>(waves);
-    return causal ? select<D, false, true>(waves) : select<D, false, false>(waves);
+        return causal ? select<D, true, true>(waves, packed) : select<D, true, false>(waves, packed);
+    return causal ? select<D, false, true>(waves, packed) : select<D, false, false>(waves, packed);
 }
 
-template <int D>
+template <int D, bool PACKED>
 Fn select_join(bool f16, bool many)
 {
     if (many)
-        return f16 ? attention_join_kernel<D, true, true> : attention_join_kernel<D, false, true>;
-    return f16 ? attention_join_kernel<D, true, false> : attention_join_kernel<D, false, false>;
+        return f16 ? attention_join_kernel<D, true, true, PACKED> : attention_join_kernel<D, false, true, PACKED>;
+    return f16 ? attention_join_kernel<D, true, false, PACKED> : attention_join_kernel<D, false, false, PACKED>;
 }
 
-}  // namespace
-
-extern "C" int64_t dit_attention_workspace_size(const dit_attn_args* args)
+template <int D>
+Fn select_join(bool f16, bool many, bool packed)
 {
-    const int rc = qkr_attn_host::check_args(args);
-    if (rc != QKR_OK)
-        return rc;
-    const Shape s = shape_of(*args);
+    return packed ? select_join<D, true>(f16, many) : select_join<D, false>(f16, many);
+}
+
+int64_t workspace_size(const dit_attn_args& a, const dit_attn_packed_args* packed)
+{
+    const Shape s = shape_of(a, packed);
     if (s.splits == 1)
         return 0;
-    return s.splits * args->batch * args->heads * args->q_tokens * (args->head_dim + 1) * 4;
+    return s.splits * a.batch * a.heads * a.q_tokens * (a.head_dim + 1) * 4;
 }
 
-extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q,
-                             const dit_attn_tensor* k, const dit_attn_tensor* v,
-                             const dit_attn_tensor* out, float* lse, void* workspace,
-                             int64_t workspace_bytes, void* stream)
+// Both entry points, after the checks of their sizes.
+int forward(const dit_attn_args& a, const dit_attn_packed_args* packed, const dit_attn_tensor* q,
+            const dit_attn_tensor* k, const dit_attn_tensor* v, const dit_attn_tensor* out, float* lse,
+            void* workspace, int64_t workspace_bytes, void* stream)
 {
     using namespace qkr_attn_host;
-    int rc = check_args(args);
-    if (rc != QKR_OK)
-        return rc;
-    const dit_attn_args& a = *args;
-    if (a.batch == 0 || a.q_tokens == 0)
-        return QKR_OK;
+    int rc;
     const Extent eq = {a.q_tokens, a.heads}, ekv = {a.kv_tokens, a.kv_heads};
     const dit_attn_tensor tq = plain(a, q, eq), tk = plain(a, k, ekv), tv = plain(a, v, ekv),
                           to = plain(a, out, eq);
@@ -398,25 +453,26 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
     const uint64_t lse_bytes = (uint64_t)a.batch * a.heads * a.q_tokens * 4;
     if (!lse)
         return QKR_ERR_NULL;
-    if (reinterpret_cast<uintptr_t>(lse) & 3u || reinterpret_cast<uintptr_t>(a.kv_lengths) & 3u)
+    const Lengths lengths(a, packed);
+    if (reinterpret_cast<uintptr_t>(lse) & 3u || !lengths.aligned())
         return QKR_ERR_ALIGN;
-    const int64_t need = dit_attention_workspace_size(args);
+    const int64_t need = workspace_size(a, packed);
     if (need && (!workspace || workspace_bytes < need))
         return QKR_ERR_WORKSPACE;
     if (!qkr_host::aligned16(workspace))
         return QKR_ERR_ALIGN;
     const Range lse_r = {lse, lse_bytes}, ws_r = {workspace, (uint64_t)need};
-    const Range len_r = {a.kv_lengths, a.kv_lengths ? (uint64_t)a.batch * 4 : 0};
-    const Range in[] = {range(a, tq, eq), range(a, tk, ekv), range(a, tv, ekv), len_r};
+    const Range in[] = {range(a, tq, eq), range(a, tk, ekv), range(a, tv, ekv), lengths.range[0], lengths.range[1]};
     const Range o = range(a, to, eq);
     for (const Range& x : in)
         if (meet(x, lse_r) || meet(x, ws_r))
             return QKR_ERR_ARG;
-    if (meet(o, lse_r) || meet(o, ws_r) || meet(lse_r, ws_r) || meet(o, len_r) ||
-        may_meet(a, to, eq, tq, eq) || may_meet(a, to, eq, tk, ekv) || may_meet(a, to, eq, tv, ekv))
+    if (meet(o, lse_r) || meet(o, ws_r) || meet(lse_r, ws_r) || meet(o, lengths.range[0]) ||
+        meet(o, lengths.range[1]) || may_meet(a, to, eq, tq, eq) || may_meet(a, to, eq, tk, ekv) ||
+        may_meet(a, to, eq, tv, ekv))
         return QKR_ERR_ARG;
 
-    const Shape s = shape_of(a);
+    const Shape s = shape_of(a, packed);
     FwdParams p = {};
     unpack(tq, p.q, p.q_bs, p.q_ts, p.q_hs);
     unpack(tk, p.k, p.k_bs, p.k_ts, p.k_hs);
@@ -424,6 +480,12 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
     unpack(to, p.out, p.o_bs, p.o_ts, p.o_hs);
     p.lse = lse;
     p.kv_lengths = a.kv_lengths;
+    if (packed) {
+        p.q_rows = Rows{packed->q_offsets, (int32_t)packed->sequences, (int32_t)a.q_tokens};
+        p.kv_rows = Rows{packed->kv_offsets ? packed->kv_offsets : packed->q_offsets, (int32_t)packed->sequences,
+                         (int32_t)a.kv_tokens};
+        p.fill_rest = packed->fill_rest;
+    }
     p.q_tokens = (int32_t)a.q_tokens;
     p.kv_tokens = (int32_t)a.kv_tokens;
     p.kv_heads = a.kv_heads;
@@ -437,9 +499,9 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = p.part_o ? p.part_o + s.splits * total * a.head_dim : nullptr;
     const bool f16 = a.dtype == QKR_FP16, causal = a.causal != 0;
-    Fn fn = a.head_dim == 64    ? select<64>(f16, causal, s.waves)
-            : a.head_dim == 128 ? select<128>(f16, causal, s.waves)
-                                : select<256>(f16, causal, s.waves);
+    Fn fn = a.head_dim == 64    ? select<64>(f16, causal, s.waves, packed)
+            : a.head_dim == 128 ? select<128>(f16, causal, s.waves, packed)
+                                : select<256>(f16, causal, s.waves, packed);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     void* argv[] = {&p};
     hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(fn),
@@ -447,12 +509,52 @@ extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q
                                      dim3(s.waves * 64), argv, 0, st);
     if (err == hipSuccess && s.splits > 1) {
         const bool many = s.splits >= kManySplits;
-        fn = a.head_dim == 64    ? select_join<64>(f16, many)
-             : a.head_dim == 128 ? select_join<128>(f16, many)
-                                 : select_join<256>(f16, many);
+        fn = a.head_dim == 64    ? select_join<64>(f16, many, packed)
+             : a.head_dim == 128 ? select_join<128>(f16, many, packed)
+                                 : select_join<256>(f16, many, packed);
         const int64_t rows = many ? 1 : 1024 / a.head_dim;
         err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)((total + rows - 1) / rows)),
                               dim3(256), argv, 0, st);
     }
     return err == hipSuccess ? QKR_OK : QKR_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" int64_t dit_attention_workspace_size(const dit_attn_args* args)
+{
+    const int rc = qkr_attn_host::check_args(args);
+    return rc != QKR_OK ? rc : workspace_size(*args, nullptr);
+}
+
+extern "C" int dit_attention(const dit_attn_args* args, const dit_attn_tensor* q,
+                             const dit_attn_tensor* k, const dit_attn_tensor* v,
+                             const dit_attn_tensor* out, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream)
+{
+    const int rc = qkr_attn_host::check_args(args);
+    if (rc != QKR_OK || args->batch == 0 || args->q_tokens == 0)
+        return rc;
+    return forward(*args, nullptr, q, k, v, out, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" int64_t dit_attention_packed_workspace_size(const dit_attn_packed_args* args)
+{
+    dit_attn_args a;
+    const int rc = qkr_attn_host::check_packed(args, a);
+    return rc != QKR_OK ? rc : workspace_size(a, args);
+}
+
+extern "C" int dit_attention_packed(const dit_attn_packed_args* args, const dit_attn_tensor* q,
+                                    const dit_attn_tensor* k, const dit_attn_tensor* v,
+                                    const dit_attn_tensor* out, float* lse, void* workspace,
+                                    int64_t workspace_bytes, void* stream)
+{
+    dit_attn_args a;
+    const int rc = qkr_attn_host::check_packed(args, a);
+    if (rc != QKR_OK || a.q_tokens == 0)
+        return rc;
+    if (!args->q_offsets)
+        return QKR_ERR_NULL;
+    return forward(a, args, q, k, v, out, lse, workspace, workspace_bytes, stream);
 }

@@ -46,6 +46,51 @@ inline int check_args(const dit_attn_args* a)
     return QKR_OK;
 }
 
+// Blocks of `size` rows that packed sequences of `rows` rows in all may need, with
+// the rows before and behind them (first_block of attention_common.h).
+inline int64_t blocks_of(int64_t rows, int64_t sequences, int64_t size) { return rows / size + sequences + 3; }
+
+// A packed call's sizes as those of one sample of all its rows.
+inline int check_packed(const dit_attn_packed_args* p, dit_attn_args& a)
+{
+    if (!p)
+        return QKR_ERR_NULL;
+    a = dit_attn_args{1, p->q_tokens, p->kv_tokens, p->heads, p->kv_heads, p->head_dim, p->causal, p->dtype,
+                      p->scale, nullptr};
+    const int rc = check_args(&a);
+    if (rc != QKR_OK)
+        return rc;
+    if (p->fill_rest != 0 && p->fill_rest != 1)
+        return QKR_ERR_ARG;
+    if (p->sequences < 0 || p->sequences >= QKR_MAX_TOKENS ||
+        p->heads * blocks_of(p->q_tokens, p->sequences, 32) >= kMaxBlocks ||
+        p->kv_heads * blocks_of(p->q_tokens * (p->heads / p->kv_heads), p->sequences, 32) >= kMaxBlocks ||
+        p->kv_heads * blocks_of(p->kv_tokens, p->sequences, 32) >= kMaxBlocks)
+        return QKR_ERR_SHAPE;
+    return QKR_OK;
+}
+
+// The device arrays that say how long sequences are: kv_lengths, or offsets.
+struct Lengths {
+    Range range[2];
+
+    Lengths(const dit_attn_args& a, const dit_attn_packed_args* p) : range{}
+    {
+        if (p) {
+            const uint64_t bytes = ((uint64_t)p->sequences + 1) * 4;
+            range[0] = {p->q_offsets, bytes};
+            range[1] = {p->kv_offsets, p->kv_offsets ? bytes : 0};
+        } else if (a.kv_lengths) {
+            range[0] = {a.kv_lengths, (uint64_t)a.batch * 4};
+        }
+    }
+
+    bool aligned() const
+    {
+        return !((reinterpret_cast<uintptr_t>(range[0].at) | reinterpret_cast<uintptr_t>(range[1].at)) & 3u);
+    }
+};
+
 // A call's tensor as the checks and kernels take it: the strides of dimensions
 // of one element, which may be anything, replaced by some that fit (0, and for a
 // token at least head_dim: what kernels stage past the last token lies outside

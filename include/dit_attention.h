@@ -115,6 +115,54 @@ int dit_attention_backward(const dit_attn_args* args, const dit_attn_tensor* dou
                            const dit_attn_tensor* dv, void* workspace, int64_t workspace_bytes,
                            void* stream);
 
+/*
+ * Packed sequences of different lengths: q, k and v are buffers of rows, one
+ * sequence after another, and each sequence attends to its own keys as one sample
+ * of dit_attention does (causal: its last query sees its last key).  Sequence i has
+ * the queries q_offsets[i] .. q_offsets[i + 1] - 1 and the keys kv_offsets[i] ..
+ * kv_offsets[i + 1] - 1; either range may be empty.
+ *
+ * Offsets are in device memory and must not decrease.  They are taken as if
+ * clamped to 0 .. the buffer's rows, so none leads out of a buffer, but with
+ * decreasing ones the results are undefined.  Rows before the first sequence and
+ * behind the last are left as they are in every output, or, with fill_rest, get
+ * out = 0, lse = -inf and zero gradients.  Rows of no sequence are not read.
+ */
+typedef struct {
+    int64_t sequences;          /* 0 .. ; see below                                   */
+    int64_t q_tokens;           /* rows of q, out and lse: 0 .. QKR_MAX_TOKENS - 1    */
+    int64_t kv_tokens;          /* rows of k and v                                    */
+    int32_t heads;              /* as in dit_attn_args, from here                     */
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t causal;
+    int32_t dtype;
+    float scale;
+    int32_t fill_rest;          /* 0 or 1                                             */
+    const int32_t* q_offsets;   /* device array [sequences + 1]                       */
+    const int32_t* kv_offsets;  /* the same, or NULL: q_offsets                       */
+} dit_attn_packed_args;
+
+/* The limits of dit_attn_args hold for one sample of all rows, and heads times
+ * sequences must stay below 2^23 with them (heads * (q_tokens / 32 + sequences + 3),
+ * kv_heads * (kv_tokens / 32 + sequences + 3)). */
+int64_t dit_attention_packed_workspace_size(const dit_attn_packed_args* args);
+int64_t dit_attention_packed_backward_workspace_size(const dit_attn_packed_args* args);
+
+/* As dit_attention and dit_attention_backward, with tensors of one sample (their
+ * batch_stride is not looked at) and lse [heads, q_tokens]. */
+int dit_attention_packed(const dit_attn_packed_args* args, const dit_attn_tensor* q,
+                         const dit_attn_tensor* k, const dit_attn_tensor* v,
+                         const dit_attn_tensor* out, float* lse, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+int dit_attention_packed_backward(const dit_attn_packed_args* args, const dit_attn_tensor* dout,
+                                  const dit_attn_tensor* q, const dit_attn_tensor* k,
+                                  const dit_attn_tensor* v, const dit_attn_tensor* out,
+                                  const float* lse, const dit_attn_tensor* dq,
+                                  const dit_attn_tensor* dk, const dit_attn_tensor* dv,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
