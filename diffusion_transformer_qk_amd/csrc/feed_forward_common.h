@@ -7,19 +7,27 @@
 // v_mfma_f32_32x32x16 (32x32x64 for 8 bits), so that a, the operand of the
 // contiguous dimension of the output, leaves 16 bytes of a row in a lane.
 //
-// An operand's matrix holds k along its rows (kRows: row a of the matrix is row
-// a of the operand) or down its rows (kColumns: column a of the matrix is row a
-// of the operand).  A stage is 64 bytes of k of kRows (32 numbers of 16 bits, 64
-// of 8), or 32 rows of kColumns, laid out in slabs of 32 rows of 64 bytes whose
-// 16-byte chunks are permuted as attention_common.h describes: row fragments of
-// kRows and transposed reads of kColumns both touch every bank evenly, and 16
-// rows of 64 bytes are one load of a wave straight into LDS.  The k of lane 32 g
-// + n in a fragment is 8 g .. 8 g + 7 of 16 for both, so that they may be mixed.
+// An operand's matrix holds k along its rows (kRows: row a of the matrix is row a
+// of the operand) or down its rows (kColumns: column a of the matrix is row a of
+// the operand).  A stage is 128 bytes of k of kRows (64 numbers of 16 bits, 128 of
+// 8), or 64 rows of k of kColumns.  In LDS both are rows of 128 bytes: the operand
+// rows of kRows, or slabs of 64 columns of the 64 rows of kColumns.  A load of a
+// wave, straight into LDS, is 8 such rows: whole lines of the L2, whose requests
+// are what bounds a tile's loads (rows of 64 bytes, twice as many requests, ran
+// 256 x 256 tiles at 1200 TFLOP/s).
 //
-// The next loads are issued into the slot of a stage when all its fragments have
-// been read (of stage s + 4, in a ring of four), and one barrier a stage says both that a slot is free
-// and that the next stage is there.  Loads past the last stage read nothing (their
-// range is empty) and keep the count of loads in flight the same for every stage.
+// 16-byte chunk c of row r is stored at c ^ f(r), where f is bits 1, 3 and 2 of r
+// from the highest: 16 rows read at one chunk, and rows r .. r + 3 and r + 8 .. r + 11
+// read at two chunks (transposed), touch every bank once.  The k of a fragment's
+// lane is a run of 8 for both forms, so that they may be mixed.
+//
+// There are two slots, and the stage after is held in registers.  A stage is several
+// steps of products; while one runs, the fragments of the next are read.  When those
+// of a stage's last step are read, one barrier says that its slot is free and that
+// the next stage is there.  (Loads straight into LDS would save the registers and the
+// stores, but came out slower: a tile of 256 x 256 then waited for loads and reads
+// of LDS together, 1320 against ... TFLOP/s.)  Loads past the last stage read nothing:
+// their range is empty.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,6 +35,7 @@
 #include <stdint.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "attention_common.h"
 
@@ -36,12 +45,15 @@ using namespace qkr_attn;
 
 typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) u32x4* LdsStore;
 
 enum Type { kBf16, kFp16, kFp8 };
 enum Form { kRows, kColumns };
 
-constexpr int kStageBytes = 64;     // of k, of a row of kRows
-constexpr int kStageRows = 32;      // of k, of kColumns
+constexpr int kStageBytes = 128;    // of k, of a row of kRows
+constexpr int kStageRows = 64;      // of k, of kColumns
+constexpr int kGroupRows = 8;       // LDS rows that a wave loads at a time
+constexpr int kSlabBytes = 64 * 128;
 constexpr uint32_t kOutside = 0x80000000u;   // a buffer offset that is out of every range
 
 // One operand's matrix as a workgroup reads it.
@@ -51,28 +63,34 @@ struct Matrix {
     int rows;             // operand rows left from the tile's first one (may be above the tile's)
 };
 
-// This lane's and wave's part of loading a tile of one operand: COUNT groups of
-// 16 rows by 64 bytes, groups first .. first + COUNT - 1 of the tile.
+// f(r) above, of r / 2.
+__device__ __forceinline__ uint32_t swizzle(uint32_t half_row)
+{
+    return (half_row & 1) << 2 | (half_row & 4) >> 1 | (half_row & 2) >> 1;
+}
+
+// This lane's and wave's part of loading a tile of one operand: COUNT groups of 8
+// LDS rows, groups first .. first + COUNT - 1 of the tile.
 template <int FORM, int COUNT>
 struct Loader {
-    uint32_t off[COUNT];
-    uint32_t chunk;       // this lane's byte in a row's 64 (kRows)
+    uint32_t off[2];      // of groups of even and odd number, less what follows from the number
+    uint32_t chunk[2];    // this lane's byte in a row's 128 (kRows)
     uint64_t at;
     uint32_t pitch, last; // last: bytes of the range up to the start of the last row (kRows), or of its columns
     int32_t k;            // bytes (kRows) or rows (kColumns) of k left
 
-    // group_rows: operand rows that the matrix's tile begins before group `first`
     __device__ __forceinline__ Loader(const Matrix& m, int first, int64_t k_size, int lane)
     {
-        chunk = ((lane & 3) ^ ((lane >> 4) & 3)) << 4;
         at = reinterpret_cast<uint64_t>(m.at);
         pitch = (uint32_t)m.pitch;
         k = (int32_t)k_size;
+        static_assert(COUNT % 2 == 0 && (FORM == kRows || COUNT == 2 || COUNT == 4 || COUNT % 8 == 0), "whole slabs");
 #pragma unroll
-        for (int i = 0; i < COUNT; ++i) {
-            const int g = first + i;
-            off[i] = chunk + (FORM == kRows ? (uint32_t)((lane >> 2) + 16 * g) * pitch
-                                            : (uint32_t)((lane >> 2) + 16 * (g & 1)) * pitch + (g >> 1) * 64);
+        for (int i = 0; i < 2; ++i) {
+            chunk[i] = ((lane & 7) ^ swizzle(4 * i + (lane >> 4))) << 4;
+            const uint32_t g = first;          // of 8 groups of a slab, slab first / 8
+            off[i] = chunk[i] + (FORM == kRows ? ((lane >> 3) + kGroupRows * g) * pitch
+                                               : ((lane >> 3) + kGroupRows * (g & 7)) * pitch + (g >> 3) * 128);
         }
         last = FORM == kRows ? (uint32_t)(m.rows - 1) * pitch : 2u * (uint32_t)m.rows;
         if (m.rows <= 0)
@@ -81,8 +99,8 @@ struct Loader {
 
     // The next stage's range, for its COUNT calls of load().
     struct Stage {
-        u32x4 rsrc;
-        uint32_t mask;
+        __amdgpu_buffer_rsrc_t rsrc;
+        uint32_t off[2];
     };
 
     __device__ __forceinline__ Stage next()
@@ -92,24 +110,28 @@ struct Loader {
         if constexpr (FORM == kRows) {
             const int left = k < kStageBytes ? k : kStageBytes;
             bytes = left > 0 ? last + left : 0;
-            s.mask = (int)chunk < left ? 0 : kOutside;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                s.off[i] = (int)chunk[i] < left ? off[i] : kOutside;
         } else {
             const int left = k < kStageRows ? k : kStageRows;
             bytes = left > 0 ? (uint32_t)(left - 1) * pitch + last : 0;
-            s.mask = 0;
+            s.off[0] = off[0];
+            s.off[1] = off[1];
         }
-        s.rsrc = u32x4{scalar((uint32_t)at), scalar((uint32_t)(at >> 32) & 0xffffu), scalar(bytes), kRawBuffer};
+        s.rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, bytes, kRawBuffer);
         at += FORM == kRows ? (uint64_t)kStageBytes : (uint64_t)kStageRows * pitch;
         k -= FORM == kRows ? kStageBytes : kStageRows;
         return s;
     }
 
-    // Issues the load of group i to LDS address `to`: assembly, and its no-ops, for
-    // the reasons that Stager::dma_row_group of attention_common.h gives.
-    __device__ __forceinline__ void load(const Stage& s, int i, uint32_t to) const
+    // This lane's 16 bytes of group i.
+    __device__ __forceinline__ u32x4 load(const Stage& s, int i) const
     {
-        __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                         : : "v"(FORM == kRows ? off[i] | s.mask : off[i]), "s"(s.rsrc), "s"(scalar(to)) : "memory");
+        // (an offset outside stays outside: the steps of a tile are below 2^31)
+        const uint32_t step = FORM == kRows ? (uint32_t)i * (kGroupRows * pitch)
+                                            : (uint32_t)(i & 7) * (kGroupRows * pitch) + (uint32_t)(i >> 3) * 128;
+        return __builtin_amdgcn_raw_buffer_load_b128(s.rsrc, s.off[i & 1] + step, 0, 0);
     }
 };
 
@@ -129,254 +151,358 @@ struct PairLoader {
 
     __device__ __forceinline__ Stage next() { return Stage{one.next(), other.next()}; }
 
-    __device__ __forceinline__ void load(const Stage& s, int i, uint32_t to) const
+    __device__ __forceinline__ u32x4 load(const Stage& s, int i) const
     {
-        if (i < COUNT / 2)
-            one.load(s.one, i, to);
-        else
-            other.load(s.other, i - COUNT / 2, to);
+        return i < COUNT / 2 ? one.load(s.one, i) : other.load(s.other, i - COUNT / 2);
     }
 };
 
-// Byte addresses of this lane's part of a tile, slot by slot of the ring.
-template <int FORM>
+// Byte addresses of this lane's part of a tile.  SIDE: operand rows of a fragment,
+// 16 (by 32 numbers of k) or, of kRows, 32 (by 64 numbers of 8 bits, in two reads).
+template <int FORM, int SIDE>
 struct FragmentAt {
-    uint32_t lane[2];
+    static_assert(SIDE == 16 || FORM == kRows, "8 bits are kRows");
+    static constexpr int kN = SIDE == 16 && FORM == kRows ? 2 : 4;
+    uint32_t lane[kN];
 
     __device__ __forceinline__ FragmentAt(uint32_t lds, int ln)
     {
-        const int n = ln & 31, g = ln >> 5, l = ln & 15;
-        if constexpr (FORM == kRows) {
-            lane[0] = lds + n * 64 + ((g ^ ((n >> 2) & 3)) << 4);
-            lane[1] = lds + n * 64 + (((2 + g) ^ ((n >> 2) & 3)) << 4);
-        } else {
-            const int r = 8 * g + (l >> 2), chunk = ((ln >> 4) & 1) * 2 + ((l & 3) >> 1);
-            lane[0] = lds + r * 64 + ((chunk ^ (2 * g)) << 4) + (l & 1) * 8;
-            lane[1] = lds + (r + 4) * 64 + ((chunk ^ (2 * g + 1)) << 4) + (l & 1) * 8;
+        const int n = ln % SIDE, g = ln / SIDE, l = ln & 15;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            if constexpr (FORM == kRows) {
+                // 16: chunks 4 i + g of step i; 32: chunks 2 i + g, two for a step
+                lane[i] = lds + n * 128 + (((i * (64 / SIDE) + g) ^ swizzle((n >> 1) & 7)) << 4);
+            } else {
+                // rows 8 g .. 8 g + 3 (+ 4 for odd i) of a step, 16 columns of blocks 2 (i / 2) + 4 m
+                const uint32_t r = 8 * g + 4 * (i & 1) + (l >> 2);
+                const uint32_t chunk = (i >> 1) * 2 + ((l & 3) >> 1);
+                lane[i] = lds + r * 128 + ((chunk ^ swizzle((r >> 1) & 7)) << 4) + (l & 1) * 8;
+            }
         }
     }
 
-    // Operand rows 32 i .. 32 i + 31 of the tile, k step kk of the stage; `off`: the
-    // slot's and the tile's offset.
-    __device__ __forceinline__ u32x4 read(uint32_t off, int i, int kk) const
+    // To the other slot, `bytes` (a power of two, to which LDS is aligned) away.
+    __device__ __forceinline__ void flip(uint32_t bytes)
+    {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            lane[i] ^= bytes;
+    }
+
+    // Operand rows SIDE i .. of the tile, chunk set `kk` of the stage.
+    __device__ __forceinline__ u32x4 read(int i, int kk) const
     {
         if constexpr (FORM == kRows) {
-            return *reinterpret_cast<LdsVec>(lane[kk] + off + i * kSlab);
+            return *reinterpret_cast<LdsVec>(lane[kk] + i * (SIDE * 128));
         } else {
-            const uint32_t o = off + i * kSlab + kk * 1024;
+            // 4 blocks of 16 columns in a slab: their chunks are 2 (i % 4) and the next
+            const uint32_t o = (i >> 2) * kSlabBytes + kk * 4096, flip = (i & 2) ? 64 : 0;
             const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                reinterpret_cast<LdsQuad>(lane[0] + o)));
+                reinterpret_cast<LdsQuad>((lane[2 * (i & 1)] ^ flip) + o)));
             const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                reinterpret_cast<LdsQuad>(lane[1] + o)));
+                reinterpret_cast<LdsQuad>((lane[2 * (i & 1) + 1] ^ flip) + o)));
             return u32x4{a[0], a[1], b[0], b[1]};
         }
     }
 };
 
-template <bool V>
+template <int V>
 struct Flag {
-    static constexpr bool value = V;
+    static constexpr int value = V;
 };
 
+// f(Flag<0>{}), f(Flag<1>{}) .. N times: a loop of that many products is more than
+// the compiler unrolls.
+template <int... I, typename F>
+__device__ __forceinline__ void unrolled(std::integer_sequence<int, I...>, F&& f)
+{
+    (f(Flag<I>{}), ...);
+}
+
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F&& f)
+{
+    unrolled(std::make_integer_sequence<int, N>{}, f);
+}
+
 template <int T>
-struct Fragment {                   // 16 numbers of 16 bits, or 64 of 8, of a row's k
+struct Fragment {                   // 16 rows by 32 numbers of 16 bits, or 32 by 64 of 8
     u32x4 v[T == kFp8 ? 2 : 1];
 };
 
 template <int T>
-__device__ __forceinline__ f32x16 product(const Fragment<T>& a, const Fragment<T>& b, f32x16 c)
+using Sums = std::conditional_t<T == kFp8, f32x16, f32x4>;
+
+// c += a b.  KEPT: c stays where only the matrix cores reach, in assembly, because the
+// compiler moves 64 such sums to and fro.  Assembly has to keep the distances itself:
+// two wait states after a vector instruction that wrote a or b (a copy, say; reads of
+// LDS are waited for), and settle_sums() before the sums are read.
+template <int T, bool KEPT>
+__device__ __forceinline__ void add_product(const Fragment<T>& a, const Fragment<T>& b, Sums<T>& c)
 {
     if constexpr (T == kFp8) {
         const i32x8 x = __builtin_bit_cast(i32x8, a), y = __builtin_bit_cast(i32x8, b);
         // both operands e4m3 (0), no block scales (all 1: 2^(127 - 127)); it aligns runs
         // of eight products to their largest (feed_forward.h), at twice the rate of 16 bits
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+    } else if constexpr (KEPT && T == kFp16) {
+        __asm__ volatile("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a.v[0]), "v"(b.v[0]));
+    } else if constexpr (KEPT) {
+        __asm__ volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a.v[0]), "v"(b.v[0]));
+    } else if constexpr (T == kFp16) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.v[0]), __builtin_bit_cast(f16x8, b.v[0]),
+                                                   c, 0, 0, 0);
     } else {
-        return mfma<T == kFp16>(a.v[0], b.v[0], c);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v[0]),
+                                                    __builtin_bit_cast(bf16x8, b.v[0]), c, 0, 0, 0);
     }
 }
+
+// The longest wait of a matrix instruction's result, of which an earlier one has passed.
+__device__ __forceinline__ void settle_sums() { __asm__ volatile("s_nop 15\n\ts_nop 7" : : : "memory"); }
 
 // What a group of WA x WB waves computes: NA x NB blocks of 32 x 32 a wave.  With
 // PAIRED the A tile is two halves, of two matrices, and so is a wave's part of it:
 // its first NA / 2 blocks are of the one, the others the same rows of the other.
 // A group is a workgroup, or one wave, which waits for no other.
-// STAGES: slots of the ring.
-template <int T, int FORM_A, int FORM_B, bool PAIRED, int NA, int NB, int WA, int WB, int STAGES = 4>
+template <int T, int FORM_A, int FORM_B, bool PAIRED, int NA, int NB, int WA, int WB>
 struct Product {
-    static constexpr int kStages = STAGES;
     static constexpr int kWaves = WA * WB;
     static constexpr int kRowsA = 32 * NA * WA, kRowsB = 32 * NB * WB;
-    static constexpr int kLoadsA = kRowsA / 16 / kWaves, kLoadsB = kRowsB / 16 / kWaves;
-    static constexpr int kTileA = kRowsA * 64, kSlot = (kRowsA + kRowsB) * 64;
-    static constexpr int kLds = kStages * kSlot;
-    static_assert(kLoadsA * kWaves * 16 == kRowsA && kLoadsB * kWaves * 16 == kRowsB, "whole groups a wave");
+    static constexpr int kLoadsA = kRowsA / kGroupRows / kWaves, kLoadsB = kRowsB / kGroupRows / kWaves;
+    static constexpr int kTileA = kRowsA * 128;
+    // the slots' distance: a power of two
+    static constexpr int kSlot = kTileA + kRowsB * 128 <= 16384 ? 16384
+                                 : kTileA + kRowsB * 128 <= 32768 ? 32768 : 65536;
+    static constexpr int kLds = kSlot + kTileA + kRowsB * 128;
+    static_assert(kLoadsA * kWaves * kGroupRows == kRowsA && kLoadsB * kWaves * kGroupRows == kRowsB,
+                  "whole groups a wave");
     static_assert(!PAIRED || NA % 2 == 0, "a pair of blocks");
     // one wave loads both halves of a pair
     using LoadA = std::conditional_t<PAIRED && kWaves == 1, PairLoader<FORM_A, kLoadsA>, Loader<FORM_A, kLoadsA>>;
     using LoadB = Loader<FORM_B, kLoadsB>;
 
-    f32x16 c[NA][NB];
+    static constexpr int kSide = T == kFp8 ? 32 : 16;      // of a product's operands
+    static constexpr int kTilesA = 32 * NA / kSide, kTilesB = 32 * NB / kSide;
 
-    struct Fragments {
-        Fragment<T> a[NA], b[NB];
-    };
+    static constexpr bool kKept = NA * NB >= 16;    // the sums take half of a lane's registers
+    Sums<T> c[kTilesA][kTilesB];
 
-    // The block of a wave's ith, from the wave's first one.
-    static constexpr int block_a(int i) { return PAIRED && i >= NA / 2 ? i - NA / 2 + NA * WA / 2 : i; }
+    // Fragments of A are read this many rows of products ahead, into a ring.
+    static constexpr int kAhead = kTilesA < 4 ? kTilesA - 1 : 3, kRing = kAhead + 1;
+    static_assert(kTilesA % kRing == 0, "a fragment's place does not change from step to step");
+
+    // The operand rows (in kSide) of a wave's ith fragment, from the wave's first one.
+    static constexpr int tile_a(int i)
+    {
+        return PAIRED && i >= kTilesA / 2 ? i - kTilesA / 2 + kTilesA * WA / 2 : i;
+    }
+    // A wave's first blocks of 32.
     static constexpr int first_a(int wave) { return wave % WA * (PAIRED ? NA / 2 : NA); }
     static constexpr int first_b(int wave) { return wave / WA * NB; }
+    // ... in bytes of LDS (kColumns: slabs of two blocks, so a wave's first is even)
+    static constexpr int bytes_of(int form, int block) { return form == kRows ? block * 4096 : block / 2 * kSlabBytes; }
+    static_assert(FORM_A == kRows || (NA % 2 == 0 && !PAIRED), "whole slabs a wave");
+    static_assert(FORM_B == kRows || NB % 2 == 0, "whole slabs a wave");
 
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
-        for (int i = 0; i < NA; ++i)
+        for (int i = 0; i < kTilesA; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-                c[i][j] = f32x16{};
+            for (int j = 0; j < kTilesB; ++j)
+                c[i][j] = Sums<T>{};
     }
 
-    // Block (i, j), fetched from where the sums are kept when it is asked for.
-    __device__ __forceinline__ f32x16 block(int i, int j)
+    // The sums leave in pieces of 8: piece (i, p), of block i of 32 columns (rows of A)
+    // and p of 2 NB, holds for this lane two runs of 4 columns of one row (of B).
+    // 16 bits: p is 16 rows; 8 bits: half of the columns of 32 rows.
+    static constexpr int kPieces = 2 * NB;
+    static __device__ __forceinline__ int piece_row(int p, int lane)
+    {
+        return T == kFp8 ? p / 2 * 32 + lane % 32 : p * 16 + lane % 16;
+    }
+    static __device__ __forceinline__ int piece_column(int p, int lane, int run)
+    {
+        return T == kFp8 ? p % 2 * 16 + run * 8 + lane / 32 * 4 : run * 16 + lane / 16 * 4;
+    }
+
+    // Fetched from where the sums are kept when it is asked for, and not before.
+    template <int i, int p>
+    __device__ __forceinline__ void piece(float (&v)[8])
     {
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (NA * NB >= 16)
-            __asm__ volatile("" : "+a"(c[i][j]));
-        return c[i][j];
-    }
-
-    // N of this wave's loads may be in flight, its LDS reads are done, and all waves are here.
-    template <int N>
-    static __device__ __forceinline__ void wait()
-    {
-        if constexpr (kWaves > 1)
-            __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
-        else
-            __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
-    }
-
-    // Adds `stages` (1 or more) stages of the two loaders' matrices.  The kLds bytes at `lds` are
-    // free at the start and at the end.
-    __device__ __forceinline__ void add(LoadA& la, LoadB& lb, int stages, uint32_t lds, int wave, int lane)
-    {
-        const FragmentAt<FORM_A> fa(lds + first_a(wave) * kSlab, lane);
-        const FragmentAt<FORM_B> fb(lds + kTileA + first_b(wave) * kSlab, lane);
-        const uint32_t to_a = lds + wave * kLoadsA * 1024, to_b = lds + kTileA + wave * kLoadsB * 1024;
-        uint32_t fill = 0, slot = 0;
-        constexpr int kLoads = kLoadsA + kLoadsB, kReads = NA + NB, kProducts = NA * NB;
-        const auto after = [](uint32_t at) { return at == kLds - kSlot ? 0 : at + kSlot; };
-        const auto read = [&](Fragments& f, int r, int kk) {       // b's after a's first: the order of use
-            Fragment<T>& to = r == 0 ? f.a[0] : r <= NB ? f.b[r - 1] : f.a[r - NB];
-#pragma unroll
-            for (int h = 0; h < (T == kFp8 ? 2 : 1); ++h) {
-                const int step = T == kFp8 ? h : kk;
-                to.v[h] = r == 0 ? fa.read(slot, block_a(0), step)
-                          : r <= NB ? fb.read(slot, r - 1, step)
-                                    : fa.read(slot, block_a(r - NB), step);
-            }
-        };
-        // The products of f, under which the fragments of the next step are read and,
-        // with LOADS, the next stage's loads issued; in this order, a few between two
-        // products, which take 32 cycles each (64 in 8 bits) and run on by themselves.
-        const auto multiply = [&](const Fragments& f, Fragments& next, int kk, auto loads) {
-            constexpr bool LOADS = decltype(loads)::value;
-            typename LoadA::Stage sa;
-            typename LoadB::Stage sb;
-            if constexpr (LOADS) {
-                sa = la.next();
-                sb = lb.next();
-            }
-#pragma unroll
-            for (int t = 0; t < kProducts; ++t) {
-#pragma unroll
-                for (int r = t * kReads / kProducts; r < (t + 1) * kReads / kProducts; ++r)
-                    read(next, r, kk);
-                if constexpr (LOADS) {
-#pragma unroll
-                    for (int q = t * kLoads / kProducts; q < (t + 1) * kLoads / kProducts; ++q) {
-                        if (q < kLoadsA)
-                            la.load(sa, q, to_a + fill + q * 1024);
-                        else
-                            lb.load(sb, q - kLoadsA, to_b + fill + (q - kLoadsA) * 1024);
-                    }
-                }
-                c[t / NB][t % NB] = product<T>(f.a[t / NB], f.b[t % NB], c[t / NB][t % NB]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if constexpr (LOADS)
-                fill = after(fill);
-        };
-        // The sums of the large tiles take half of a lane's registers, the half that
-        // only the matrix cores reach: said here, or some are spilled.
-        const auto keep = [&] {
-            if constexpr (kProducts >= 16) {
-#pragma unroll
-                for (int t = 0; t < kProducts; ++t)
-                    __asm__ volatile("" : "+a"(c[t / NB][t % NB]));
-            }
-        };
-        const auto turn = [&] {          // the next stage is there, and the present slot free
-            wait<(kStages - 2) * kLoads>();
-            slot = after(slot);
-        };
-        Fragments f0, f1;
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-            const auto sa = la.next();
-            const auto sb = lb.next();
-#pragma unroll
-            for (int q = 0; q < kLoadsA; ++q)
-                la.load(sa, q, to_a + fill + q * 1024);
-#pragma unroll
-            for (int q = 0; q < kLoadsB; ++q)
-                lb.load(sb, q, to_b + fill + q * 1024);
-            fill = after(fill);
-        }
-        wait<(kStages - 1) * kLoads>();
-#pragma unroll
-        for (int r = 0; r < kReads; ++r)
-            read(f0, r, 0);
-        int s = 0;
         if constexpr (T == kFp8) {
-            do {                                         // a stage of zeros at the end of an odd number
-                turn();
-                multiply(f0, f1, 0, Flag<true>{});
-                turn();
-                multiply(f1, f0, 0, Flag<true>{});
-                keep();
-                s += 2;
-            } while (s < stages);
-        } else {
-            do {
-                multiply(f0, f1, 1, Flag<false>{});
-                turn();
-                multiply(f1, f0, 0, Flag<true>{});
-                keep();
-            } while (++s < stages);
-        }
-        wait<0>();
-    }
-};
-
-// Stores a C block's lane (row b, columns a0 .. a0 + 31 of the output at `row`),
-// of which `left` columns are there.
-template <bool F16>
-__device__ __forceinline__ void store_block(uint16_t* row, const f32x16& c, int g, bool valid, int left)
-{
+            if constexpr (kKept)
+                __asm__ volatile("" : "+a"(c[i][p / 2]));
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
+            for (int k = 0; k < 8; ++k)
+                v[k] = c[i][p / 2][8 * (p % 2) + k];
+        } else {
+            if constexpr (kKept)
+                __asm__ volatile("" : "+a"(c[2 * i][p]), "+a"(c[2 * i + 1][p]));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = c[2 * i + k / 4][p][k % 4];
+        }
+    }
+
+    // Stores a piece: `row` is block i's first column in the lane's output row, of which
+    // `left` columns are there.  The lanes that hold neighbouring runs trade them, so that
+    // each stores 16 bytes.
+    template <bool F16>
+    static __device__ __forceinline__ void store_piece(uint16_t* row, const float (&v)[8], int p, int lane, bool valid,
+                                                       int left)
+    {
         u32x4 w;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint32_t a = pack2<F16>(c[4 * i + 2 * j], c[4 * i + 2 * j + 1]);
-            const uint32_t b = pack2<F16>(c[4 * i + 4 + 2 * j], c[4 * i + 4 + 2 * j + 1]);
-            const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-            w[j] = r[0];
-            w[2 + j] = r[1];
+            const uint32_t x = pack2<F16>(v[2 * j], v[2 * j + 1]), y = pack2<F16>(v[4 + 2 * j], v[5 + 2 * j]);
+            if constexpr (T == kFp8) {
+                const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+                w[j] = r[0];
+                w[2 + j] = r[1];
+            } else {
+                const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+                w[j] = r[0];
+                w[2 + j] = r[1];
+            }
         }
-        if (valid && 8 * (i + g) < left)
-            store16<false>(row + 8 * (i + g), w);
+        const int at = T == kFp8 ? p % 2 * 16 + lane / 32 * 8 : (lane >> 4 & 1) * 16 + (lane >> 5) * 8;
+        if (valid && at < left)
+            store16<false>(row + at, w);
     }
-}
+
+    // This wave's LDS reads and writes are done, and all waves are here.
+    static __device__ __forceinline__ void meet()
+    {
+        if constexpr (kWaves > 1)
+            __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+        else
+            __asm__ volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    }
+
+    // Adds `stages` (1 or more) stages of the two loaders' matrices.  The kLds bytes at
+    // `lds`, which is aligned to two slots, are free at the start and at the end.
+    __device__ __forceinline__ void add(LoadA& la, LoadB& lb, int stages, uint32_t lds, int wave, int lane)
+    {
+        FragmentAt<FORM_A, kSide> fa(lds + bytes_of(FORM_A, first_a(wave)), lane);
+        FragmentAt<FORM_B, kSide> fb(lds + kTileA + bytes_of(FORM_B, first_b(wave)), lane);
+        constexpr int kLoads = kLoadsA + kLoadsB, kProducts = kTilesA * kTilesB;
+        constexpr int kSteps = 2;             // of a stage: 32 numbers of k, or 64 of 8 bits
+        Fragment<T> a[kRing], b[kSteps][kTilesB];
+        const auto read_a = [&](int i, int step) {
+#pragma unroll
+            for (int h = 0; h < (T == kFp8 ? 2 : 1); ++h)
+                a[i % kRing].v[h] = fa.read(tile_a(i), T == kFp8 ? 2 * step + h : step);
+        };
+        const auto read_b = [&](int j, int step) {
+#pragma unroll
+            for (int h = 0; h < (T == kFp8 ? 2 : 1); ++h)
+                b[step][j].v[h] = fb.read(j, T == kFp8 ? 2 * step + h : step);
+        };
+        u32x4 held[kLoads];                   // the stage after the one that is in LDS
+        typename LoadA::Stage sa;
+        typename LoadB::Stage sb;
+        uint32_t fill_a = lds + wave * kLoadsA * 1024 + lane * 16, fill_b = fill_a + kTileA + wave * (kLoadsB - kLoadsA) * 1024;
+        const auto load = [&](int q) { held[q] = q < kLoadsA ? la.load(sa, q) : lb.load(sb, q - kLoadsA); };
+        const auto store = [&](int q) {
+            *reinterpret_cast<LdsStore>(q < kLoadsA ? fill_a + q * 1024 : fill_b + (q - kLoadsA) * 1024) = held[q];
+        };
+        // A step's products, row by row of A's fragments, and between them, a few
+        // instructions under each (16 cycles, 64 in 8 bits), in this order:
+        //   A    the fragment of the row kAhead further (in the last rows, of the next step);
+        //   B    the next step's, early;
+        //   the held loads, one after another, go to the free slot, each followed by the load
+        //        that takes its registers, which has a whole stage's products to arrive;
+        //   in a stage's last step, before the first read of the next stage, and once this
+        //        wave's reads and stores are done, the barrier that says so of all waves.
+        constexpr int kTurn = (kTilesA - kAhead) * kTilesB;
+        // the held loads that go before the first step, in it, and in the last one up to the barrier
+        constexpr int kEarly = kLoads * (kProducts - kTurn) / (2 * kProducts), kMiddle = kLoads / 2;
+        const auto pass = [&](int q) {
+            store(q);
+            load(q);
+        };
+        const auto turn = [&] {
+            meet();
+            fa.flip(kSlot);
+            fb.flip(kSlot);
+            fill_a ^= kSlot;
+            fill_b ^= kSlot;
+            sa = la.next();
+            sb = lb.next();
+        };
+        const auto step = [&](auto which) {
+            constexpr int kStep = decltype(which)::value;
+            constexpr bool LAST = kStep == kSteps - 1;
+            constexpr int kFrom = LAST ? kTurn : 0, kSpan = (kProducts - kFrom) / 2 > 0 ? (kProducts - kFrom) / 2 : 1;
+            unrolled<kProducts>([&](auto number) __attribute__((always_inline)) {
+                constexpr int t = decltype(number)::value, i = t / kTilesB, j = t % kTilesB;
+                if constexpr (LAST && t == kTurn)
+                    turn();
+                if constexpr (j == 0)
+                    read_a((i + kAhead) % kTilesA, i + kAhead < kTilesA ? kStep : (kStep + 1) % kSteps);
+                if constexpr (t >= kFrom && t < kFrom + kSpan) {
+#pragma unroll
+                    for (int r = (t - kFrom) * kTilesB / kSpan; r < (t - kFrom + 1) * kTilesB / kSpan; ++r)
+                        read_b(r, (kStep + 1) % kSteps);
+                }
+                // the share of the held loads that falls to this product
+                constexpr int kLate = kLoads - kEarly - kMiddle;
+                constexpr int kOf = !LAST ? kMiddle : t < kTurn ? kLate : kEarly;
+                constexpr int kIn = !LAST ? kProducts : t < kTurn ? kTurn : kProducts - kTurn;
+                constexpr int kAt = LAST && t >= kTurn ? t - kTurn : t;
+                constexpr int kFirst = !LAST ? kEarly : t < kTurn ? kEarly + kMiddle : 0;
+#pragma unroll
+                for (int q = kAt * kOf / kIn; q < (kAt + 1) * kOf / kIn; ++q)
+                    pass(kFirst + q);
+                add_product<T, kKept>(a[i % kRing], b[kStep][j], c[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        sa = la.next();
+        sb = lb.next();
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+            load(q);
+        sa = la.next();
+        sb = lb.next();
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+            pass(q);
+        fill_a ^= kSlot;
+        fill_b ^= kSlot;
+        sa = la.next();
+        sb = lb.next();
+#pragma unroll
+        for (int q = 0; q < kEarly; ++q)
+            pass(q);
+        meet();
+#pragma unroll
+        for (int j = 0; j < kTilesB; ++j)
+            read_b(j, 0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            read_a(i, 0);
+        int s = 0;
+        do {
+            step(Flag<0>{});
+            step(Flag<1>{});
+            if constexpr (kKept && T == kFp8) {
+#pragma unroll
+                for (int i = 0; i < kTilesA; ++i)
+#pragma unroll
+                    for (int j = 0; j < kTilesB; ++j)
+                        __asm__ volatile("" : "+a"(c[i][j]));     // or some are spilled
+            }
+        } while (++s < stages);
+        meet();
+        if constexpr (kKept && T != kFp8)
+            settle_sums();
+    }
+};
 
 // The (row of tiles, column of tiles) of hardware block `bid` of rows x columns
 // tiles: each die walks one run of them, in bands of `band` rows of tiles, column

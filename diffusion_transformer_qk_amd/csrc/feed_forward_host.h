@@ -69,10 +69,10 @@ inline bool large_tiles(int64_t rows, int64_t columns)
 }
 
 template <typename Params>
-inline int launch(void (*fn)(Params), int64_t blocks, Params& p, void* stream)
+inline int launch(void (*fn)(Params), int64_t blocks, Params& p, void* stream, unsigned threads = 256)
 {
     void* args[] = {&p};
-    return hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)blocks), dim3(256), args, 0,
+    return hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)blocks), dim3(threads), args, 0,
                            static_cast<hipStream_t>(stream)) == hipSuccess
                ? QKR_OK
                : QKR_ERR_HIP;

@@ -17,6 +17,8 @@ namespace {
 
 using namespace qkr_ff;
 
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
 struct FwdParams {
     const char *x, *w_gate, *w_up;
     const float *x_scale, *gate_scale, *up_scale;
@@ -27,36 +29,44 @@ struct FwdParams {
     uint32_t row_tiles, inner_tiles;  // of the grid
 };
 
-// The epilogue of one block: rows r (this lane's), columns i0 .. i0 + 31.
-template <int T, bool F16, int ACT>
-__device__ __forceinline__ void finish(const FwdParams& p, f32x16 gate, f32x16 up, int64_t r, int i0, int g)
+// The epilogue of a wave's sums: rows from r0 on, columns from i0 on.
+template <int T, bool F16, int ACT, int BLOCKS, typename P>
+__device__ __forceinline__ void finish(const FwdParams& p, P& c, int64_t r0, int i0, int lane)
 {
-    const bool valid = r < p.rows;
-    const int left = p.inner - i0;
-    if constexpr (T == kFp8) {
-        const float s = valid ? p.x_scale[r] : 0.0f;
+    unrolled<P::kPieces * BLOCKS>([&](auto number) __attribute__((always_inline)) {
+        constexpr int q = decltype(number)::value / BLOCKS, i = decltype(number)::value % BLOCKS;
+        const int64_t r = r0 + P::piece_row(q, lane);
+        const bool valid = r < p.rows;
+        const int a0 = i0 + 32 * i, left = p.inner - a0;
+        float gate[8], up[8];
+        c.template piece<i, q>(gate);
+        c.template piece<i + BLOCKS, q>(up);
+        if constexpr (T == kFp8) {
+            const float s = valid ? p.x_scale[r] : 0.0f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (8 * q + 4 * g < left) {
-                const float* gs = p.gate_scale + i0 + 8 * q + 4 * g;
-                const float* us = p.up_scale + i0 + 8 * q + 4 * g;
+            for (int run = 0; run < 2; ++run) {
+                const int a = P::piece_column(q, lane, run);
+                if (a < left) {
+                    const f32x4 gs = *reinterpret_cast<const f32x4u*>(p.gate_scale + a0 + a);
+                    const f32x4 us = *reinterpret_cast<const f32x4u*>(p.up_scale + a0 + a);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    gate[4 * q + k] *= s * gs[k];
-                    up[4 * q + k] *= s * us[k];
+                    for (int k = 0; k < 4; ++k) {
+                        gate[4 * run + k] *= s * gs[k];
+                        up[4 * run + k] *= s * us[k];
+                    }
                 }
             }
         }
-    }
-    const int64_t at = r * p.inner + i0;
-    if (p.gate) {
-        store_block<F16>(p.gate + at, gate, g, valid, left);
-        store_block<F16>(p.up + at, up, g, valid, left);
-    }
+        const int64_t at = r * p.inner + a0;
+        if (p.gate) {
+            P::template store_piece<F16>(p.gate + at, gate, q, lane, valid, left);
+            P::template store_piece<F16>(p.up + at, up, q, lane, valid, left);
+        }
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-        gate[k] = activated<ACT>(gate[k]) * up[k];
-    store_block<F16>(p.h + at, gate, g, valid, left);
+        for (int k = 0; k < 8; ++k)
+            gate[k] = activated<ACT>(gate[k]) * up[k];
+        P::template store_piece<F16>(p.h + at, gate, q, lane, valid, left);
+    });
 }
 
 // Tiles of kRowsB rows of x and kRowsA / 2 columns of h.
@@ -65,7 +75,7 @@ __global__ __launch_bounds__(256, NA * NB > 4 ? 1 : 2)
 void gated_feed_forward_kernel(const FwdParams p)
 {
     using P = Product<T, kRows, kRows, true, NA, NB, 2, 2>;
-    __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
+    __shared__ __attribute__((aligned(2 * P::kSlot))) char lds[P::kLds];
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const TileOf tile(blockIdx.x, p.row_tiles, p.inner_tiles, 8);
@@ -82,37 +92,30 @@ void gated_feed_forward_kernel(const FwdParams p)
     P c;
     c.clear();
     c.add(la, lb, (p.k_bytes + kStageBytes - 1) / kStageBytes, lds_address(lds), wave, lane);
-    const int n = lane & 31, g = lane >> 5;
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int i = 0; i < NA / 2; ++i) {
-            const f32x16 gate = c.block(i, j), up = c.block(i + NA / 2, j);
-            finish<T, F16, ACT>(p, gate, up, r0 + (P::first_b(wave) + j) * 32 + n,
-                                i0 + (P::first_a(wave) + i) * 32, g);
-        }
+    finish<T, F16, ACT, NA / 2>(p, c, r0 + 32 * P::first_b(wave), i0 + 32 * P::first_a(wave), lane);
 }
 
 // Up to 32 rows of x: the call waits for the weights.  A workgroup takes 32 columns
-// of h, its waves a quarter of k each, through rings of their own (no barriers),
-// and the first wave adds the four sums in order.
-constexpr int kFewRows = 32, kFewColumns = 32;
+// of h, its waves a share of k each, through slots of their own (no barriers), and
+// the first wave adds their sums in order.
+constexpr int kFewRows = 32, kFewColumns = 32, kFewWaves = 2;
 
 template <int T, bool F16, int ACT>
-__global__ __launch_bounds__(256, 2)
+__global__ __launch_bounds__(64 * kFewWaves, 2)
 void gated_feed_forward_few_kernel(const FwdParams p)
 {
-    using P = Product<T, kRows, kRows, true, 2, 1, 1, 1, 3>;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * P::kLds];
+    using P = Product<T, kRows, kRows, true, 2, 1, 1, 1>;
+    constexpr int kRing = 2 * P::kSlot;
+    __shared__ __attribute__((aligned(kRing))) char lds[kFewWaves * kRing];
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int i0 = (int)blockIdx.x * kFewColumns;
-    const int stages = (p.k_bytes + kStageBytes - 1) / kStageBytes, each = (stages + 3) / 4;
+    const int stages = (p.k_bytes + kStageBytes - 1) / kStageBytes, each = (stages + kFewWaves - 1) / kFewWaves;
     const int k0 = wave * each * kStageBytes;
     const int k_left = p.k_bytes - k0 < each * kStageBytes ? p.k_bytes - k0 : each * kStageBytes;
     const int columns = p.inner - i0 < kFewColumns ? p.inner - i0 : kFewColumns;
     const int64_t w0 = (int64_t)i0 * p.k_bytes + k0;
-    const uint32_t ring = lds_address(lds) + wave * P::kLds;
+    const uint32_t ring = lds_address(lds) + wave * kRing;
     P c;
     c.clear();
     if (k_left > 0) {
@@ -122,31 +125,26 @@ void gated_feed_forward_few_kernel(const FwdParams p)
         typename P::LoadB lb(Matrix{p.x + k0, p.k_bytes, (int)p.rows}, 0, k_left, lane);
         c.add(la, lb, (k_left + kStageBytes - 1) / kStageBytes, ring, 0, lane);
     }
-    const int n = lane & 31, g = lane >> 5;
-    f32x4* sums = reinterpret_cast<f32x4*>(lds) + wave * (P::kLds / 16);
+    // (a wave's slots are free for its sums)
+    float* sums = reinterpret_cast<float*>(lds + wave * kRing) + lane;
+    constexpr int kEach = P::kSide * P::kSide / 64;
+    const auto sum = [&](int n) __attribute__((always_inline)) -> auto& {
+        return c.c[n / kEach / P::kTilesB][n / kEach % P::kTilesB];
+    };
     if (wave > 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                sums[(i * 4 + q) * 64 + lane] = f32x4{c.c[i][0][4 * q], c.c[i][0][4 * q + 1], c.c[i][0][4 * q + 2],
-                                                      c.c[i][0][4 * q + 3]};
+        for (int n = 0; n < 32; ++n)
+            sums[64 * n] = sum(n)[n % kEach];
     }
     __syncthreads();
     if (wave > 0)
         return;
 #pragma unroll
-    for (int w = 1; w < 4; ++w)
+    for (int w = 1; w < kFewWaves; ++w)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const f32x4 v = sums[w * (P::kLds / 16) + (i * 4 + q) * 64 + lane];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    c.c[i][0][4 * q + k] += v[k];
-            }
-    finish<T, F16, ACT>(p, c.c[0][0], c.c[1][0], n, i0, g);
+        for (int n = 0; n < 32; ++n)
+            sum(n)[n % kEach] += sums[w * (kRing / 4) + 64 * n];
+    finish<T, F16, ACT, 1>(p, c, 0, i0, lane);
 }
 
 using Fn = void (*)(FwdParams);
@@ -222,7 +220,7 @@ extern "C" int dit_gated_feed_forward(const dit_ff_args* args, const void* x, co
     p.k_bytes = a.hidden * (int32_t)size;
     if (a.rows <= kFewRows)
         return launch(select<0, 0>(a.dtype, a.out_dtype, a.activation), (a.inner + kFewColumns - 1) / kFewColumns, p,
-                      stream);
+                      stream, 64 * kFewWaves);
     const bool large = large_tiles(a.rows, 2 * (int64_t)a.inner);
     const int64_t side = large ? 256 : 128;
     p.row_tiles = (uint32_t)((a.rows + side - 1) / side);

@@ -113,13 +113,35 @@ void feed_forward_gradients_kernel(const BwdParams p)
     }
 }
 
+// A wave's sums times 2^e, to rows from r0 on (of `rows`) and columns from a0 on of
+// [rows, columns] at `out`.
+template <bool F16, typename P>
+__device__ __forceinline__ void store(P& c, uint16_t* out, int64_t r0, int64_t rows, int a0, int columns, int e,
+                                      int lane)
+{
+    constexpr int kBlocks = P::kTilesA * P::kSide / 32;
+    unrolled<P::kPieces * kBlocks>([&](auto number) __attribute__((always_inline)) {
+        constexpr int q = decltype(number)::value / kBlocks, i = decltype(number)::value % kBlocks;
+        const int64_t r = r0 + P::piece_row(q, lane);
+        float v[8];
+        c.template piece<i, q>(v);
+        if constexpr (F16) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = __builtin_amdgcn_ldexpf(v[k], e);
+        }
+        const int a = a0 + 32 * i;
+        P::template store_piece<F16>(out + r * columns + a, v, q, lane, r < rows, columns - a);
+    });
+}
+
 // Tiles of kRowsB rows and kRowsA columns of dx.
 template <bool F16, int N>
 __global__ __launch_bounds__(256, N == 4 ? 1 : 2)
 void feed_forward_dx_kernel(const BwdParams p)
 {
     using P = Product<F16 ? kFp16 : kBf16, kColumns, kRows, false, N, N, 2, 2>;
-    __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
+    __shared__ __attribute__((aligned(2 * P::kSlot))) char lds[P::kLds];
     __shared__ float slot[4];
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -141,20 +163,7 @@ void feed_forward_dx_kernel(const BwdParams p)
     int e = 0;
     if constexpr (F16)
         e = stored_exponent(p, slot);
-    const int n = lane & 31, g = lane >> 5;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            f32x16 v = c.block(i, j);
-            if constexpr (F16)
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    v[k] = __builtin_amdgcn_ldexpf(v[k], e);
-            const int64_t r = r0 + (P::first_b(wave) + j) * 32 + n;
-            const int a0 = h0 + (P::first_a(wave) + i) * 32;
-            store_block<F16>(p.dx + r * p.hidden + a0, v, g, r < p.rows, p.hidden - a0);
-        }
+    store<F16>(c, p.dx, r0 + 32 * P::first_b(wave), p.rows, h0 + 32 * P::first_a(wave), p.hidden, e, lane);
 }
 
 // Tiles of kRowsB rows (of one weight) and kRowsA columns of dw_gate and dw_up;
@@ -164,7 +173,7 @@ __global__ __launch_bounds__(256, N == 4 ? 1 : 2)
 void feed_forward_dw_kernel(const BwdParams p)
 {
     using P = Product<F16 ? kFp16 : kBf16, kColumns, kColumns, false, N, N, 2, 2>;
-    __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
+    __shared__ __attribute__((aligned(2 * P::kSlot))) char lds[P::kLds];
     __shared__ float slot[4];
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -184,20 +193,7 @@ void feed_forward_dw_kernel(const BwdParams p)
     if constexpr (F16)
         e = p.rows ? stored_exponent(p, slot) : 0;
     uint16_t* out = of_up ? p.dw_up : p.dw_gate;
-    const int n = lane & 31, g = lane >> 5;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            f32x16 v = c.block(i, j);
-            if constexpr (F16)
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    v[k] = __builtin_amdgcn_ldexpf(v[k], e);
-            const int64_t r = i0 + (P::first_b(wave) + j) * 32 + n;
-            const int a0 = h0 + (P::first_a(wave) + i) * 32;
-            store_block<F16>(out + r * p.hidden + a0, v, g, r < p.inner, p.hidden - a0);
-        }
+    store<F16>(c, out, i0 + 32 * P::first_b(wave), p.inner, h0 + 32 * P::first_a(wave), p.hidden, e, lane);
 }
 
 // ---------------------------------------------------------------- launches
