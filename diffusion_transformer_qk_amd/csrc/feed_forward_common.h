@@ -16,18 +16,19 @@
 // are what bounds a tile's loads (rows of 64 bytes, twice as many requests, ran
 // 256 x 256 tiles at 1200 TFLOP/s).
 //
-// 16-byte chunk c of row r is stored at c ^ f(r), where f is bits 1, 3 and 2 of r
-// from the highest: 16 rows read at one chunk, and rows r .. r + 3 and r + 8 .. r + 11
-// read at two chunks (transposed), touch every bank once.  The k of a fragment's
-// lane is a run of 8 for both forms, so that they may be mixed.
+// 16-byte chunk c of row r is stored at c ^ f(r), where f has 4 for bit 1 of r, 3 for
+// bit 2 and 2 for bit 3, exclusively or.  Of a read of 16 bytes a lane, lanes 0-3,
+// 12-15 and 20-27 (and so on) are served together: f(6) = 1 lets rows 0-3 and 12-15
+// of one chunk and rows 4-11 of the next touch every bank once.  So do rows r .. r + 3
+// and r + 8 .. r + 11 of two chunks, which a transposed read takes.  The k of a
+// fragment's lane is a run of 8 for both forms, so that they may be mixed.
 //
-// There are two slots, and the stage after is held in registers.  A stage is several
-// steps of products; while one runs, the fragments of the next are read.  When those
-// of a stage's last step are read, one barrier says that its slot is free and that
-// the next stage is there.  (Loads straight into LDS would save the registers and the
-// stores, but came out slower: a tile of 256 x 256 then waited for loads and reads
-// of LDS together, 1320 against ... TFLOP/s.)  Loads past the last stage read nothing:
-// their range is empty.
+// A stage is two steps of products; while one runs, the fragments of the next are
+// read.  LDS is a ring of five slots of a tile, for A and B of a stage in turn: two
+// stages and A of a third.  When the fragments of a stage's last step are read, one
+// barrier says that its slots are free and that the next stage is there.  Loads past
+// the last stage read nothing: their range is empty.  (Loads that go through registers
+// and stores of LDS have longer to arrive, but the stores cost more than that gains.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -45,7 +46,6 @@ using namespace qkr_attn;
 
 typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) u32x4* LdsStore;
 
 enum Type { kBf16, kFp16, kFp8 };
 enum Form { kRows, kColumns };
@@ -66,7 +66,7 @@ struct Matrix {
 // f(r) above, of r / 2.
 __device__ __forceinline__ uint32_t swizzle(uint32_t half_row)
 {
-    return (half_row & 1) << 2 | (half_row & 4) >> 1 | (half_row & 2) >> 1;
+    return (half_row & 1 ? 4 : 0) ^ (half_row & 2 ? 3 : 0) ^ (half_row & 4 ? 2 : 0);
 }
 
 // This lane's and wave's part of loading a tile of one operand: COUNT groups of 8
@@ -99,7 +99,7 @@ struct Loader {
 
     // The next stage's range, for its COUNT calls of load().
     struct Stage {
-        __amdgpu_buffer_rsrc_t rsrc;
+        u32x4 rsrc;
         uint32_t off[2];
     };
 
@@ -119,19 +119,21 @@ struct Loader {
             s.off[0] = off[0];
             s.off[1] = off[1];
         }
-        s.rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, bytes, kRawBuffer);
+        s.rsrc = u32x4{scalar((uint32_t)at), scalar((uint32_t)(at >> 32) & 0xffffu), scalar(bytes), kRawBuffer};
         at += FORM == kRows ? (uint64_t)kStageBytes : (uint64_t)kStageRows * pitch;
         k -= FORM == kRows ? kStageBytes : kStageRows;
         return s;
     }
 
-    // This lane's 16 bytes of group i.
-    __device__ __forceinline__ u32x4 load(const Stage& s, int i) const
+    // Issues the load of group i to LDS address `to`: assembly, and its no-ops, for
+    // the reasons that Stager::dma_row_group of attention_common.h gives.
+    __device__ __forceinline__ void load(const Stage& s, int i, uint32_t to) const
     {
         // (an offset outside stays outside: the steps of a tile are below 2^31)
         const uint32_t step = FORM == kRows ? (uint32_t)i * (kGroupRows * pitch)
                                             : (uint32_t)(i & 7) * (kGroupRows * pitch) + (uint32_t)(i >> 3) * 128;
-        return __builtin_amdgcn_raw_buffer_load_b128(s.rsrc, s.off[i & 1] + step, 0, 0);
+        __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                         : : "v"(s.off[i & 1] + step), "s"(s.rsrc), "s"(scalar(to)) : "memory");
     }
 };
 
@@ -151,9 +153,12 @@ struct PairLoader {
 
     __device__ __forceinline__ Stage next() { return Stage{one.next(), other.next()}; }
 
-    __device__ __forceinline__ u32x4 load(const Stage& s, int i) const
+    __device__ __forceinline__ void load(const Stage& s, int i, uint32_t to) const
     {
-        return i < COUNT / 2 ? one.load(s.one, i) : other.load(s.other, i - COUNT / 2);
+        if (i < COUNT / 2)
+            one.load(s.one, i, to);
+        else
+            other.load(s.other, i - COUNT / 2, to);
     }
 };
 
@@ -163,7 +168,7 @@ template <int FORM, int SIDE>
 struct FragmentAt {
     static_assert(SIDE == 16 || FORM == kRows, "8 bits are kRows");
     static constexpr int kN = SIDE == 16 && FORM == kRows ? 2 : 4;
-    uint32_t lane[kN];
+    uint32_t own[kN], lane[kN];     // in any slot, and in the present one
 
     __device__ __forceinline__ FragmentAt(uint32_t lds, int ln)
     {
@@ -172,22 +177,21 @@ struct FragmentAt {
         for (int i = 0; i < kN; ++i) {
             if constexpr (FORM == kRows) {
                 // 16: chunks 4 i + g of step i; 32: chunks 2 i + g, two for a step
-                lane[i] = lds + n * 128 + (((i * (64 / SIDE) + g) ^ swizzle((n >> 1) & 7)) << 4);
+                own[i] = lds + n * 128 + (((i * (64 / SIDE) + g) ^ swizzle((n >> 1) & 7)) << 4);
             } else {
                 // rows 8 g .. 8 g + 3 (+ 4 for odd i) of a step, 16 columns of blocks 2 (i / 2) + 4 m
                 const uint32_t r = 8 * g + 4 * (i & 1) + (l >> 2);
                 const uint32_t chunk = (i >> 1) * 2 + ((l & 3) >> 1);
-                lane[i] = lds + r * 128 + ((chunk ^ swizzle((r >> 1) & 7)) << 4) + (l & 1) * 8;
+                own[i] = lds + r * 128 + ((chunk ^ swizzle((r >> 1) & 7)) << 4) + (l & 1) * 8;
             }
         }
     }
 
-    // To the other slot, `bytes` (a power of two, to which LDS is aligned) away.
-    __device__ __forceinline__ void flip(uint32_t bytes)
+    __device__ __forceinline__ void to(uint32_t slot)
     {
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-            lane[i] ^= bytes;
+            lane[i] = own[i] + slot;
     }
 
     // Operand rows SIDE i .. of the tile, chunk set `kk` of the stage.
@@ -271,11 +275,8 @@ struct Product {
     static constexpr int kWaves = WA * WB;
     static constexpr int kRowsA = 32 * NA * WA, kRowsB = 32 * NB * WB;
     static constexpr int kLoadsA = kRowsA / kGroupRows / kWaves, kLoadsB = kRowsB / kGroupRows / kWaves;
-    static constexpr int kTileA = kRowsA * 128;
-    // the slots' distance: a power of two
-    static constexpr int kSlot = kTileA + kRowsB * 128 <= 16384 ? 16384
-                                 : kTileA + kRowsB * 128 <= 32768 ? 32768 : 65536;
-    static constexpr int kLds = kSlot + kTileA + kRowsB * 128;
+    // LDS: a ring of 5 slots of a tile, for A and B of a stage in turn
+    static constexpr int kSlot = 128 * (kRowsA > kRowsB ? kRowsA : kRowsB), kLds = 5 * kSlot;
     static_assert(kLoadsA * kWaves * kGroupRows == kRowsA && kLoadsB * kWaves * kGroupRows == kRowsB,
                   "whole groups a wave");
     static_assert(!PAIRED || NA % 2 == 0, "a pair of blocks");
@@ -286,7 +287,7 @@ struct Product {
     static constexpr int kSide = T == kFp8 ? 32 : 16;      // of a product's operands
     static constexpr int kTilesA = 32 * NA / kSide, kTilesB = 32 * NB / kSide;
 
-    static constexpr bool kKept = NA * NB >= 16;    // the sums take half of a lane's registers
+    static constexpr bool kKept = NA * NB >= 8;     // the sums take half of a lane's registers
     Sums<T> c[kTilesA][kTilesB];
 
     // Fragments of A are read this many rows of products ahead, into a ring.
@@ -374,21 +375,25 @@ struct Product {
             store16<false>(row + at, w);
     }
 
-    // This wave's LDS reads and writes are done, and all waves are here.
+    // All but N of this wave's loads and all of its LDS reads are done, and all waves are here.
+    template <int N>
     static __device__ __forceinline__ void meet()
     {
         if constexpr (kWaves > 1)
-            __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+            __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
         else
-            __asm__ volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+            __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
     }
 
     // Adds `stages` (1 or more) stages of the two loaders' matrices.  The kLds bytes at
-    // `lds`, which is aligned to two slots, are free at the start and at the end.
+    // `lds` are free at the start and at the end.
     __device__ __forceinline__ void add(LoadA& la, LoadB& lb, int stages, uint32_t lds, int wave, int lane)
     {
         FragmentAt<FORM_A, kSide> fa(lds + bytes_of(FORM_A, first_a(wave)), lane);
-        FragmentAt<FORM_B, kSide> fb(lds + kTileA + bytes_of(FORM_B, first_b(wave)), lane);
+        FragmentAt<FORM_B, kSide> fb(lds + bytes_of(FORM_B, first_b(wave)), lane);
+        uint32_t slot_a = 0, slot_b = kSlot;                  // of the present stage
+        uint32_t fill_b = 3 * kSlot, fill_a = 4 * kSlot;      // of the loads that are issued now
+        const auto advance = [](uint32_t slot) { return slot >= 3 * kSlot ? slot - 3 * kSlot : slot + 2 * kSlot; };
         constexpr int kLoads = kLoadsA + kLoadsB, kProducts = kTilesA * kTilesB;
         constexpr int kSteps = 2;             // of a stage: 32 numbers of k, or 64 of 8 bits
         Fragment<T> a[kRing], b[kSteps][kTilesB];
@@ -402,38 +407,43 @@ struct Product {
             for (int h = 0; h < (T == kFp8 ? 2 : 1); ++h)
                 b[step][j].v[h] = fb.read(j, T == kFp8 ? 2 * step + h : step);
         };
-        u32x4 held[kLoads];                   // the stage after the one that is in LDS
         typename LoadA::Stage sa;
         typename LoadB::Stage sb;
-        uint32_t fill_a = lds + wave * kLoadsA * 1024 + lane * 16, fill_b = fill_a + kTileA + wave * (kLoadsB - kLoadsA) * 1024;
-        const auto load = [&](int q) { held[q] = q < kLoadsA ? la.load(sa, q) : lb.load(sb, q - kLoadsA); };
-        const auto store = [&](int q) {
-            *reinterpret_cast<LdsStore>(q < kLoadsA ? fill_a + q * 1024 : fill_b + (q - kLoadsA) * 1024) = held[q];
+        const uint32_t to_a = lds + wave * kLoadsA * 1024, to_b = lds + wave * kLoadsB * 1024;
+        // loads 0 .. kLoadsB - 1 of a stage's turn are B's, the others A's of the stage after
+        const auto load = [&](int q) __attribute__((always_inline)) {
+            if (q == 0)
+                sb = lb.next();
+            if (q == kLoadsB)
+                sa = la.next();
+            if (q < kLoadsB)
+                lb.load(sb, q, fill_b + to_b + q * 1024);
+            else
+                la.load(sa, q - kLoadsB, fill_a + to_a + (q - kLoadsB) * 1024);
         };
         // A step's products, row by row of A's fragments, and between them, a few
         // instructions under each (16 cycles, 64 in 8 bits), in this order:
         //   A    the fragment of the row kAhead further (in the last rows, of the next step);
         //   B    the next step's, early;
-        //   the held loads, one after another, go to the free slot, each followed by the load
-        //        that takes its registers, which has a whole stage's products to arrive;
         //   in a stage's last step, before the first read of the next stage, and once this
-        //        wave's reads and stores are done, the barrier that says so of all waves.
+        //        wave's reads are done and the next stage is there, the barrier that says so of
+        //        all waves;
+        //   from there to the next one, at even distances, the loads into the two slots that
+        //        this freed: B of the stage after the next, then A of the one after that.  (A
+        //        wave waits while its load is taken, so loads in a row hold up its products: all
+        //        at once measured 1170 TFLOP/s, over half of a stage 1310.)
         constexpr int kTurn = (kTilesA - kAhead) * kTilesB;
-        // the held loads that go before the first step, in it, and in the last one up to the barrier
-        constexpr int kEarly = kLoads * (kProducts - kTurn) / (2 * kProducts), kMiddle = kLoads / 2;
-        const auto pass = [&](int q) {
-            store(q);
-            load(q);
+        const auto turn = [&]() __attribute__((always_inline)) {
+            meet<kLoadsA>();
+            fill_b = slot_a;
+            fill_a = slot_b;
+            slot_a = advance(slot_a);
+            slot_b = advance(slot_b);
+            fa.to(slot_a);
+            fb.to(slot_b);
         };
-        const auto turn = [&] {
-            meet();
-            fa.flip(kSlot);
-            fb.flip(kSlot);
-            fill_a ^= kSlot;
-            fill_b ^= kSlot;
-            sa = la.next();
-            sb = lb.next();
-        };
+        // loads of products 0 .. t - 1 after a turn
+        const auto loads_by = [](int t) { return (t * kLoads + 2 * kProducts - 1) / (2 * kProducts); };
         const auto step = [&](auto which) {
             constexpr int kStep = decltype(which)::value;
             constexpr bool LAST = kStep == kSteps - 1;
@@ -449,37 +459,35 @@ struct Product {
                     for (int r = (t - kFrom) * kTilesB / kSpan; r < (t - kFrom + 1) * kTilesB / kSpan; ++r)
                         read_b(r, (kStep + 1) % kSteps);
                 }
-                // the share of the held loads that falls to this product
-                constexpr int kLate = kLoads - kEarly - kMiddle;
-                constexpr int kOf = !LAST ? kMiddle : t < kTurn ? kLate : kEarly;
-                constexpr int kIn = !LAST ? kProducts : t < kTurn ? kTurn : kProducts - kTurn;
-                constexpr int kAt = LAST && t >= kTurn ? t - kTurn : t;
-                constexpr int kFirst = !LAST ? kEarly : t < kTurn ? kEarly + kMiddle : 0;
+                constexpr int kSince = LAST ? (t >= kTurn ? t - kTurn : t + 2 * kProducts - kTurn)
+                                            : t + kProducts - kTurn;
 #pragma unroll
-                for (int q = kAt * kOf / kIn; q < (kAt + 1) * kOf / kIn; ++q)
-                    pass(kFirst + q);
+                for (int q = loads_by(kSince); q < loads_by(kSince + 1); ++q)
+                    load(q);
                 add_product<T, kKept>(a[i % kRing], b[kStep][j], c[i][j]);
                 __builtin_amdgcn_sched_barrier(0);
             });
         };
-        sa = la.next();
+        // A and B of the first stage, A of the second, and what would follow a turn before it
+        const auto load_a = [&](uint32_t slot) __attribute__((always_inline)) {
+            sa = la.next();
+#pragma unroll
+            for (int q = 0; q < kLoadsA; ++q)
+                la.load(sa, q, slot + to_a + q * 1024);
+        };
+        constexpr int kBefore = loads_by(kProducts - kTurn);
+        load_a(0);
         sb = lb.next();
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q)
+        for (int q = 0; q < kLoadsB; ++q)
+            lb.load(sb, q, kSlot + to_b + q * 1024);
+        load_a(2 * kSlot);
+#pragma unroll
+        for (int q = 0; q < kBefore; ++q)
             load(q);
-        sa = la.next();
-        sb = lb.next();
-#pragma unroll
-        for (int q = 0; q < kLoads; ++q)
-            pass(q);
-        fill_a ^= kSlot;
-        fill_b ^= kSlot;
-        sa = la.next();
-        sb = lb.next();
-#pragma unroll
-        for (int q = 0; q < kEarly; ++q)
-            pass(q);
-        meet();
+        meet<kLoadsA + kBefore>();
+        fa.to(slot_a);
+        fb.to(slot_b);
 #pragma unroll
         for (int j = 0; j < kTilesB; ++j)
             read_b(j, 0);
@@ -498,7 +506,7 @@ struct Product {
                         __asm__ volatile("" : "+a"(c[i][j]));     // or some are spilled
             }
         } while (++s < stages);
-        meet();
+        meet<0>();
         if constexpr (kKept && T != kFp8)
             settle_sums();
     }

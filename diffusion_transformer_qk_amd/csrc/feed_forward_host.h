@@ -61,11 +61,44 @@ inline int check_buffers(const Buffer* in, int ins, const Buffer* out, int outs)
     return QKR_OK;
 }
 
-// Whether a product of `rows` x `columns` outputs is cut into 256 x 256 tiles
-// (one workgroup a CU) rather than 128 x 128 (two a CU).
-inline bool large_tiles(int64_t rows, int64_t columns)
+// How a product of rows x columns outputs and `stages` stages of k is cut: tiles of
+// 256 x 256 (a workgroup a CU) or of 128 x 128 (two a CU), and k into splits whose
+// sums are added by a launch of their own.  The cheapest by what a stage of a round
+// of workgroups takes, as measured: 1.5 us of the large tiles, 0.95 of the small ones
+// and 0.6 where they have a CU each.  (x of 5120, W of 13824: 512 rows 125 us with
+// large tiles, 156 with small ones; 256 rows 106 and 91.  dx of one row 242 us without
+// splits and 52 with the 12 that this gives, of 256 rows 263 and 115; dw of 16384 rows,
+// 512 x 2048, 188 and 116.)
+struct Cut {
+    bool large;
+    int64_t splits;
+    int64_t row_tiles, column_tiles;
+};
+
+inline Cut cut_of(int64_t rows, int64_t columns, int64_t stages, bool may_split)
 {
-    return (rows + 255) / 256 * ((columns + 255) / 256) >= 256;
+    Cut best = {};
+    double least = 0.0;
+    for (int large = 0; large < 2; ++large) {
+        const int64_t side = large ? 256 : 128;
+        const int64_t row_tiles = (rows + side - 1) / side, column_tiles = (columns + side - 1) / side;
+        const int64_t tiles = row_tiles * column_tiles;
+        for (int64_t splits = 1; splits <= 32; ++splits) {
+            if (splits > 1 && (!may_split || stages / splits < 8 || tiles * splits > 512))
+                break;
+            const int64_t blocks = tiles * splits, at_once = large ? 256 : 512;
+            const int64_t rounds = (blocks + at_once - 1) / at_once, each = (stages + splits - 1) / splits;
+            const double stage = large ? 1.5 : blocks <= 256 ? 0.6 : 0.95;
+            // the launch that adds the splits, and their way through memory
+            const double join = splits > 1 ? 5.0 + 8e-6 * (double)(splits * rows * columns) / 4.0 : 0.0;
+            const double time = (double)rounds * (double)each * stage + join;
+            if (best.row_tiles == 0 || time < least) {
+                best = Cut{large != 0, splits, row_tiles, column_tiles};
+                least = time;
+            }
+        }
+    }
+    return best;
 }
 
 template <typename Params>

@@ -70,24 +70,25 @@ __device__ __forceinline__ void finish(const FwdParams& p, P& c, int64_t r0, int
 }
 
 // Tiles of kRowsB rows of x and kRowsA / 2 columns of h.
-template <int T, bool F16, int ACT, int NA, int NB>
-__global__ __launch_bounds__(256, NA * NB > 4 ? 1 : 2)
+template <int T, bool F16, int ACT, int NA, int NB, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB, 2)
 void gated_feed_forward_kernel(const FwdParams p)
 {
-    using P = Product<T, kRows, kRows, true, NA, NB, 2, 2>;
-    __shared__ __attribute__((aligned(2 * P::kSlot))) char lds[P::kLds];
+    using P = Product<T, kRows, kRows, true, NA, NB, WA, WB>;
+    __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const TileOf tile(blockIdx.x, p.row_tiles, p.inner_tiles, 8);
+    const TileOf tile(blockIdx.x, p.row_tiles, p.inner_tiles, 4);
     const int64_t r0 = (int64_t)tile.row * P::kRowsB;
     constexpr int kColumnsOf = P::kRowsA / 2;
     const int i0 = tile.column * kColumnsOf;
     const int64_t rows_left = p.rows - r0;
-    const int of_up = wave >> 1;                 // waves 0 and 1 load W_gate's rows
+    constexpr int kHalf = WA * WB / 2;
+    const int of_up = wave >= kHalf;             // the first half of the waves load W_gate's rows
     const Matrix w = {(of_up ? p.w_up : p.w_gate) + (int64_t)i0 * p.k_bytes, p.k_bytes,
                       p.inner - i0 < kColumnsOf ? p.inner - i0 : kColumnsOf};
     const Matrix x = {p.x + r0 * p.k_bytes, p.k_bytes, rows_left < P::kRowsB ? (int)rows_left : P::kRowsB};
-    typename P::LoadA la(w, (wave & 1) * P::kLoadsA, p.k_bytes, lane);
+    typename P::LoadA la(w, (wave - of_up * kHalf) * P::kLoadsA, p.k_bytes, lane);
     typename P::LoadB lb(x, wave * P::kLoadsB, p.k_bytes, lane);
     P c;
     c.clear();
@@ -101,12 +102,12 @@ void gated_feed_forward_kernel(const FwdParams p)
 constexpr int kFewRows = 32, kFewColumns = 32, kFewWaves = 2;
 
 template <int T, bool F16, int ACT>
-__global__ __launch_bounds__(64 * kFewWaves, 2)
+__global__ __launch_bounds__(64 * kFewWaves, 1)
 void gated_feed_forward_few_kernel(const FwdParams p)
 {
     using P = Product<T, kRows, kRows, true, 2, 1, 1, 1>;
-    constexpr int kRing = 2 * P::kSlot;
-    __shared__ __attribute__((aligned(kRing))) char lds[kFewWaves * kRing];
+    constexpr int kRing = P::kLds;
+    __shared__ __attribute__((aligned(1024))) char lds[kFewWaves * kRing];
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int i0 = (int)blockIdx.x * kFewColumns;
@@ -156,8 +157,8 @@ Fn select(int activation)
         return activation == DIT_FF_SILU ? gated_feed_forward_few_kernel<T, F16, 0>
                                          : gated_feed_forward_few_kernel<T, F16, 1>;
     else
-        return activation == DIT_FF_SILU ? gated_feed_forward_kernel<T, F16, 0, NA, NB>
-                                         : gated_feed_forward_kernel<T, F16, 1, NA, NB>;
+        return activation == DIT_FF_SILU ? gated_feed_forward_kernel<T, F16, 0, NA, NB, 2, NA>
+                                         : gated_feed_forward_kernel<T, F16, 1, NA, NB, 2, NA>;
 }
 
 // NA, NB: blocks of a wave's tile, or 0 for few rows.
@@ -221,11 +222,10 @@ extern "C" int dit_gated_feed_forward(const dit_ff_args* args, const void* x, co
     if (a.rows <= kFewRows)
         return launch(select<0, 0>(a.dtype, a.out_dtype, a.activation), (a.inner + kFewColumns - 1) / kFewColumns, p,
                       stream, 64 * kFewWaves);
-    const bool large = large_tiles(a.rows, 2 * (int64_t)a.inner);
-    const int64_t side = large ? 256 : 128;
-    p.row_tiles = (uint32_t)((a.rows + side - 1) / side);
-    p.inner_tiles = (uint32_t)((a.inner + side / 2 - 1) / (side / 2));
-    const Fn fn = large ? select<4, 4>(a.dtype, a.out_dtype, a.activation)
+    const Cut cut = cut_of(a.rows, 2 * (int64_t)a.inner, (p.k_bytes + 127) / 128, false);
+    p.row_tiles = (uint32_t)cut.row_tiles;
+    p.inner_tiles = (uint32_t)((a.inner + (cut.large ? 127 : 63)) / (cut.large ? 128 : 64));
+    const Fn fn = cut.large ? select<4, 2>(a.dtype, a.out_dtype, a.activation)
                         : select<2, 2>(a.dtype, a.out_dtype, a.activation);
-    return launch(fn, (int64_t)p.row_tiles * p.inner_tiles, p, stream);
+    return launch(fn, (int64_t)p.row_tiles * p.inner_tiles, p, stream, cut.large ? 512 : 256);
 }

@@ -34,17 +34,20 @@ struct BwdParams {
     int64_t rows;
     int32_t hidden, inner;
     uint32_t row_tiles, column_tiles;   // of the grid
+    int32_t splits;           // of k
+    float* parts;             // [splits][rows][hidden] of dx, or [splits][2 inner][hidden] of dw, when splits > 1
 };
 
 constexpr int kThreads = 256;
 
 // The power of two that dgate and dup are divided by: the largest becomes 2^14 .. 2^15.
+template <int THREADS>
 __device__ __forceinline__ int stored_exponent(const BwdParams& p, float* slot)
 {
     float top = 0.0f;
-    for (uint32_t i = threadIdx.x; i < p.largest_blocks; i += kThreads)
+    for (uint32_t i = threadIdx.x; i < p.largest_blocks; i += THREADS)
         top = fmaxf(top, p.largest[i]);
-    top = block_max<4>(top, slot);
+    top = block_max<THREADS / 64>(top, slot);
     return top > 0.0f ? __builtin_amdgcn_frexp_expf(top) - 15 : 0;
 }
 
@@ -96,7 +99,7 @@ void feed_forward_gradients_kernel(const BwdParams p)
     const int64_t n = p.rows * p.inner;
     int e = 0;
     if constexpr (F16)
-        e = stored_exponent(p, slot);
+        e = stored_exponent<kThreads>(p, slot);
     for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kVec; i < n;
          i += (int64_t)gridDim.x * kThreads * kVec) {
         float a[8], b[8];
@@ -113,11 +116,11 @@ void feed_forward_gradients_kernel(const BwdParams p)
     }
 }
 
-// A wave's sums times 2^e, to rows from r0 on (of `rows`) and columns from a0 on of
-// [rows, columns] at `out`.
+// A wave's sums to rows from r0 on (of `rows`) and columns from a0 on of [rows,
+// columns]: times 2^e to `out`, or as they are to a split's part.
 template <bool F16, typename P>
-__device__ __forceinline__ void store(P& c, uint16_t* out, int64_t r0, int64_t rows, int a0, int columns, int e,
-                                      int lane)
+__device__ __forceinline__ void store(P& c, uint16_t* out, float* part, int64_t r0, int64_t rows, int a0,
+                                      int columns, int e, int lane)
 {
     constexpr int kBlocks = P::kTilesA * P::kSide / 32;
     unrolled<P::kPieces * kBlocks>([&](auto number) __attribute__((always_inline)) {
@@ -125,75 +128,136 @@ __device__ __forceinline__ void store(P& c, uint16_t* out, int64_t r0, int64_t r
         const int64_t r = r0 + P::piece_row(q, lane);
         float v[8];
         c.template piece<i, q>(v);
+        const int a = a0 + 32 * i;
+        if (part) {
+#pragma unroll
+            for (int run = 0; run < 2; ++run) {
+                const int at = a + P::piece_column(q, lane, run);
+                if (r < rows && at < columns)
+                    *reinterpret_cast<f32x4*>(part + r * columns + at) =
+                        f32x4{v[4 * run], v[4 * run + 1], v[4 * run + 2], v[4 * run + 3]};
+            }
+            return;
+        }
         if constexpr (F16) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 v[k] = __builtin_amdgcn_ldexpf(v[k], e);
         }
-        const int a = a0 + 32 * i;
         P::template store_piece<F16>(out + r * columns + a, v, q, lane, r < rows, columns - a);
     });
 }
 
 // Tiles of kRowsB rows and kRowsA columns of dx.
 template <bool F16, int N>
-__global__ __launch_bounds__(256, N == 4 ? 1 : 2)
+__global__ __launch_bounds__(128 * N, 2)
 void feed_forward_dx_kernel(const BwdParams p)
 {
-    using P = Product<F16 ? kFp16 : kBf16, kColumns, kRows, false, N, N, 2, 2>;
-    __shared__ __attribute__((aligned(2 * P::kSlot))) char lds[P::kLds];
-    __shared__ float slot[4];
+    using P = Product<F16 ? kFp16 : kBf16, kColumns, kRows, false, N, 2, 2, N>;
+    __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const TileOf tile(blockIdx.x, p.row_tiles, p.column_tiles, 8);
+    const uint32_t tiles = p.row_tiles * p.column_tiles;
+    const TileOf tile(blockIdx.x % tiles, p.row_tiles, p.column_tiles, 4);
+    const int split = blockIdx.x / tiles;
     const int64_t r0 = (int64_t)tile.row * P::kRowsB, rows_left = p.rows - r0;
     const int h0 = tile.column * P::kRowsA;
     const int rows = rows_left < P::kRowsB ? (int)rows_left : P::kRowsB;
     const int columns = p.hidden - h0 < P::kRowsA ? p.hidden - h0 : P::kRowsA;
     P c;
     c.clear();
+    // the split's stages of both halves' together
+    const int stages = (p.inner + kStageRows - 1) / kStageRows, each = (2 * stages + p.splits - 1) / p.splits;
+    const int from = split * each, to = from + each < 2 * stages ? from + each : 2 * stages;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-        const Matrix w = {reinterpret_cast<const char*>((half ? p.w_up : p.w_gate) + h0), (int64_t)p.hidden * 2, columns};
-        const Matrix d = {reinterpret_cast<const char*>(p.d + (half * p.rows + r0) * p.inner), (int64_t)p.inner * 2, rows};
-        typename P::LoadA la(w, wave * P::kLoadsA, p.inner, lane);
-        typename P::LoadB lb(d, wave * P::kLoadsB, (int64_t)p.inner * 2, lane);
-        c.add(la, lb, (p.inner + kStageRows - 1) / kStageRows, lds_address(lds), wave, lane);
+        const int low = (from > half * stages ? from : half * stages) - half * stages;
+        const int high = (to < (half + 1) * stages ? to : (half + 1) * stages) - half * stages;
+        if (low >= high)
+            continue;
+        const int k0 = low * kStageRows, k = (high * kStageRows < p.inner ? high * kStageRows : p.inner) - k0;
+        const Matrix w = {reinterpret_cast<const char*>((half ? p.w_up : p.w_gate) + (int64_t)k0 * p.hidden + h0),
+                          (int64_t)p.hidden * 2, columns};
+        const Matrix d = {reinterpret_cast<const char*>(p.d + (half * p.rows + r0) * p.inner + k0),
+                          (int64_t)p.inner * 2, rows};
+        typename P::LoadA la(w, wave * P::kLoadsA, k, lane);
+        typename P::LoadB lb(d, wave * P::kLoadsB, (int64_t)k * 2, lane);
+        c.add(la, lb, high - low, lds_address(lds), wave, lane);
     }
     int e = 0;
     if constexpr (F16)
-        e = stored_exponent(p, slot);
-    store<F16>(c, p.dx, r0 + 32 * P::first_b(wave), p.rows, h0 + 32 * P::first_a(wave), p.hidden, e, lane);
+        e = stored_exponent<64 * P::kWaves>(p, reinterpret_cast<float*>(lds));
+    store<F16>(c, p.dx, p.splits > 1 ? p.parts + split * p.rows * p.hidden : nullptr, r0 + 32 * P::first_b(wave),
+               p.rows, h0 + 32 * P::first_a(wave), p.hidden, e, lane);
 }
 
 // Tiles of kRowsB rows (of one weight) and kRowsA columns of dw_gate and dw_up;
 // the first half of the rows of tiles is dw_gate's.
 template <bool F16, int N>
-__global__ __launch_bounds__(256, N == 4 ? 1 : 2)
+__global__ __launch_bounds__(128 * N, 2)
 void feed_forward_dw_kernel(const BwdParams p)
 {
-    using P = Product<F16 ? kFp16 : kBf16, kColumns, kColumns, false, N, N, 2, 2>;
-    __shared__ __attribute__((aligned(2 * P::kSlot))) char lds[P::kLds];
-    __shared__ float slot[4];
+    using P = Product<F16 ? kFp16 : kBf16, kColumns, kColumns, false, N, 2, 2, N>;
+    __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const TileOf tile(blockIdx.x, p.row_tiles, p.column_tiles, 8);
-    const int each = (int)p.row_tiles / 2, of_up = tile.row >= each;
-    const int i0 = (tile.row - of_up * each) * P::kRowsB, h0 = tile.column * P::kRowsA;
+    const uint32_t tiles = p.row_tiles * p.column_tiles;
+    const TileOf tile(blockIdx.x % tiles, p.row_tiles, p.column_tiles, 4);
+    const int split = blockIdx.x / tiles;
+    const int per_weight = (int)p.row_tiles / 2, of_up = tile.row >= per_weight;
+    const int i0 = (tile.row - of_up * per_weight) * P::kRowsB, h0 = tile.column * P::kRowsA;
     const int rows = p.inner - i0 < P::kRowsB ? p.inner - i0 : P::kRowsB;
     const int columns = p.hidden - h0 < P::kRowsA ? p.hidden - h0 : P::kRowsA;
-    const Matrix x = {reinterpret_cast<const char*>(p.x + h0), (int64_t)p.hidden * 2, columns};
-    const Matrix d = {reinterpret_cast<const char*>(p.d + of_up * p.rows * p.inner + i0), (int64_t)p.inner * 2, rows};
+    const int64_t stages = (p.rows + kStageRows - 1) / kStageRows, each = (stages + p.splits - 1) / p.splits;
+    const int64_t low = split * each, high = low + each < stages ? low + each : stages;
+    const int64_t k0 = low * kStageRows, k = (high * kStageRows < p.rows ? high * kStageRows : p.rows) - k0;
     P c;
     c.clear();
-    typename P::LoadA la(x, wave * P::kLoadsA, p.rows, lane);
-    typename P::LoadB lb(d, wave * P::kLoadsB, p.rows, lane);
-    c.add(la, lb, (int)((p.rows + kStageRows - 1) / kStageRows), lds_address(lds), wave, lane);
+    if (low < high) {
+        const Matrix x = {reinterpret_cast<const char*>(p.x + k0 * p.hidden + h0), (int64_t)p.hidden * 2, columns};
+        const Matrix d = {reinterpret_cast<const char*>(p.d + (of_up * p.rows + k0) * p.inner + i0),
+                          (int64_t)p.inner * 2, rows};
+        typename P::LoadA la(x, wave * P::kLoadsA, k, lane);
+        typename P::LoadB lb(d, wave * P::kLoadsB, k, lane);
+        c.add(la, lb, (int)(high - low), lds_address(lds), wave, lane);
+    }
     int e = 0;
     if constexpr (F16)
-        e = p.rows ? stored_exponent(p, slot) : 0;
-    uint16_t* out = of_up ? p.dw_up : p.dw_gate;
-    store<F16>(c, out, i0 + 32 * P::first_b(wave), p.inner, h0 + 32 * P::first_a(wave), p.hidden, e, lane);
+        e = p.rows ? stored_exponent<64 * P::kWaves>(p, reinterpret_cast<float*>(lds)) : 0;
+    float* part = p.splits > 1 ? p.parts + ((int64_t)split * 2 + of_up) * p.inner * p.hidden : nullptr;
+    store<F16>(c, of_up ? p.dw_up : p.dw_gate, part, i0 + 32 * P::first_b(wave), p.inner,
+               h0 + 32 * P::first_a(wave), p.hidden, e, lane);
+}
+
+// Adds the splits' parts in order: `first` and `second` are the halves of what they
+// are parts of (`elements` each; no second for dx).
+template <bool F16>
+__global__ __launch_bounds__(kThreads)
+void feed_forward_join_kernel(const BwdParams p, uint16_t* first, uint16_t* second, int64_t elements)
+{
+    __shared__ float slot[4];
+    int e = 0;
+    if constexpr (F16)
+        e = stored_exponent<kThreads>(p, slot);
+    const int64_t total = second ? 2 * elements : elements;
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kVec;
+    if (i >= total)
+        return;
+    float sum[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        float v[8];
+        load_f32x8(p.parts + s * total + i, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sum[k] += v[k];
+    }
+    if constexpr (F16) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sum[k] = __builtin_amdgcn_ldexpf(sum[k], e);
+    }
+    store16<false>(i < elements ? first + i : second + (i - elements), pack8<F16>(sum));
 }
 
 // ---------------------------------------------------------------- launches
@@ -228,18 +292,44 @@ int64_t element_blocks(int64_t elements)
     return n < 1 ? 1 : n > 2048 ? 2048 : n;
 }
 
-// Bytes of the workspace up to the array of the largest values.
-int64_t largest_at(const dit_ff_args& a) { return 4 * a.rows * a.inner; }
+// How both products are cut, and where the workspace's parts begin (in bytes).
+struct Shape {
+    qkr_ff_host::Cut dx, dw;
+    int64_t largest, parts, bytes;
+};
+
+Shape shape_of(const dit_ff_args& a)
+{
+    Shape s;
+    s.dx = qkr_ff_host::cut_of(a.rows, a.hidden, 2 * (((int64_t)a.inner + kStageRows - 1) / kStageRows), true);
+    s.dw = qkr_ff_host::cut_of(2 * (int64_t)a.inner, a.hidden, (a.rows + kStageRows - 1) / kStageRows, true);
+    // tiles of one weight each
+    const int64_t side = s.dw.large ? 256 : 128;
+    s.dw.row_tiles = 2 * ((a.inner + side - 1) / side);
+    s.largest = 4 * a.rows * a.inner;
+    s.parts = s.largest + (a.dtype == QKR_FP16 ? (element_blocks(a.rows * a.inner) * 4 + 15) / 16 * 16 : 0);
+    const int64_t dx = s.dx.splits > 1 ? s.dx.splits * a.rows * a.hidden * 4 : 0;
+    const int64_t dw = s.dw.splits > 1 ? s.dw.splits * 2 * a.inner * a.hidden * 4 : 0;
+    s.bytes = a.rows == 0 ? 0 : s.parts + (dx > dw ? dx : dw);
+    return s;
+}
+
+hipError_t join(BwdParams p, uint16_t* first, uint16_t* second, int64_t elements, bool f16, void* stream)
+{
+    void* argv[] = {&p, &first, &second, &elements};
+    const int64_t total = second ? 2 * elements : elements, per = kThreads * kVec;
+    const void* fn = f16 ? reinterpret_cast<const void*>(feed_forward_join_kernel<true>)
+                         : reinterpret_cast<const void*>(feed_forward_join_kernel<false>);
+    return hipLaunchKernel(fn, dim3((unsigned)((total + per - 1) / per)), dim3(kThreads), argv, 0,
+                           static_cast<hipStream_t>(stream));
+}
 
 }  // namespace
 
 extern "C" int64_t dit_gated_feed_forward_backward_workspace_size(const dit_ff_args* args)
 {
     const int rc = qkr_ff_host::check_args(args, false);
-    if (rc != QKR_OK || args->rows == 0)
-        return rc;
-    const int64_t blocks = args->dtype == QKR_FP16 ? element_blocks(args->rows * args->inner) : 0;
-    return largest_at(*args) + (blocks * 4 + 15) / 16 * 16;
+    return rc != QKR_OK ? rc : shape_of(*args).bytes;
 }
 
 extern "C" int dit_gated_feed_forward_backward(const dit_ff_args* args, const void* dh, const void* x,
@@ -258,7 +348,8 @@ extern "C" int dit_gated_feed_forward_backward(const dit_ff_args* args, const vo
         return QKR_OK;
     if (a.rows && (!dh || !x || !gate || !up || (dx && (!w_gate || !w_up))))
         return QKR_ERR_NULL;
-    const int64_t need = dit_gated_feed_forward_backward_workspace_size(args);
+    const Shape shape = shape_of(a);
+    const int64_t need = shape.bytes;
     if (need && (!workspace || workspace_bytes < need))
         return QKR_ERR_WORKSPACE;
     const uint64_t hidden = a.hidden, inner = a.inner, rows = a.rows;
@@ -281,7 +372,8 @@ extern "C" int dit_gated_feed_forward_backward(const dit_ff_args* args, const vo
     p.dw_gate = static_cast<uint16_t*>(dw_gate);
     p.dw_up = static_cast<uint16_t*>(dw_up);
     p.d = static_cast<uint16_t*>(workspace);
-    p.largest = reinterpret_cast<float*>(static_cast<char*>(workspace) + largest_at(a));
+    p.largest = reinterpret_cast<float*>(static_cast<char*>(workspace) + shape.largest);
+    p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + shape.parts);
     p.rows = a.rows;
     p.hidden = a.hidden;
     p.inner = a.inner;
@@ -294,19 +386,17 @@ extern "C" int dit_gated_feed_forward_backward(const dit_ff_args* args, const vo
         if (rc == QKR_OK)
             rc = launch(silu ? select_gradients<0>(f16) : select_gradients<1>(f16), blocks, p, stream);
     }
-    if (rc == QKR_OK && dx && a.rows) {
-        const bool large = large_tiles(a.rows, a.hidden);
-        const int64_t side = large ? 256 : 128;
-        p.row_tiles = (uint32_t)((a.rows + side - 1) / side);
-        p.column_tiles = (uint32_t)((a.hidden + side - 1) / side);
-        rc = launch(select_dx(f16, large), (int64_t)p.row_tiles * p.column_tiles, p, stream);
-    }
-    if (rc == QKR_OK && dw_gate) {
-        const bool large = large_tiles(2 * (int64_t)a.inner, a.hidden);
-        const int64_t side = large ? 256 : 128;
-        p.row_tiles = (uint32_t)(2 * ((a.inner + side - 1) / side));
-        p.column_tiles = (uint32_t)((a.hidden + side - 1) / side);
-        rc = launch(select_dw(f16, large), (int64_t)p.row_tiles * p.column_tiles, p, stream);
-    }
+    const auto product = [&](const Cut& cut, Fn fn, uint16_t* first, uint16_t* second, int64_t elements) {
+        p.row_tiles = (uint32_t)cut.row_tiles;
+        p.column_tiles = (uint32_t)cut.column_tiles;
+        p.splits = (int32_t)cut.splits;
+        rc = launch(fn, cut.row_tiles * cut.column_tiles * cut.splits, p, stream, cut.large ? 512 : 256);
+        if (rc == QKR_OK && cut.splits > 1 && join(p, first, second, elements, f16, stream) != hipSuccess)
+            rc = QKR_ERR_HIP;
+    };
+    if (rc == QKR_OK && dx && a.rows)
+        product(shape.dx, select_dx(f16, shape.dx.large), p.dx, nullptr, a.rows * a.hidden);
+    if (rc == QKR_OK && dw_gate)
+        product(shape.dw, select_dw(f16, shape.dw.large), p.dw_gate, p.dw_up, (int64_t)a.inner * a.hidden);
     return rc;
 }

@@ -96,10 +96,15 @@ def test_outputs_must_not_share_memory():
 def test_workspaces():
     size = qkr.gated_feed_forward_backward_workspace_size
     need = size(100, 512, 1024)
-    assert need == 4 * 100 * 1024
+    assert need >= 4 * 100 * 1024 and need % 16 == 0
     assert backward(ws=0) == b.QKR_ERR_WORKSPACE and backward(ws_bytes=need - 1) == b.QKR_ERR_WORKSPACE
     assert size(0, 512, 1024) == 0 and size(-1, 8, 8) == b.QKR_ERR_SHAPE and size(1, 8, 12) == b.QKR_ERR_UNSUPPORTED
     assert need < size(100, 512, 1024, dtype=b.QKR_FP16) <= need + 4 * 2048
+    # products that fill the chip by themselves are not split
+    assert size(4608, 6144, 16384) == 4 * 4608 * 16384
+    # dx of few rows is, and dw of many rows of narrow weights: partial sums in fp32
+    assert size(16, 5120, 13824) > 4 * 16 * 13824 + 2 * 4 * 16 * 5120
+    assert size(16384, 512, 2048) > 4 * 16384 * 2048 + 2 * 4 * 2 * 2048 * 512
 
 
 def test_nothing_to_do():
@@ -143,7 +148,7 @@ C_PROGRAM = r"""
 int main(void)
 {
     dit_ff_args a = {16, 64, 128, DIT_FF_SILU, QKR_BF16, QKR_BF16};
-    if (dit_gated_feed_forward_backward_workspace_size(&a) != 4 * 16 * 128) return 1;
+    if (dit_gated_feed_forward_backward_workspace_size(&a) < 4 * 16 * 128) return 1;
     if (dit_gated_feed_forward(&a, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != QKR_ERR_NULL) return 2;
     a.dtype = DIT_FF_E4M3;
     if (dit_gated_feed_forward_backward(&a, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != QKR_ERR_UNSUPPORTED) return 3;

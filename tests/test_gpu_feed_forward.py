@@ -193,7 +193,11 @@ def check_backward(t, act):
     return {n: made[n] for n in want}
 
 
-@pytest.mark.parametrize("rows,hidden,inner", SIZES)
+# dx, dw, or both summed over splits of k, which end inside a stage or have none
+SPLITS = [(5, 512, 2048), (2500, 64, 136), (40, 264, 3080), (1100, 72, 1544), (1, 8, 4104), (3000, 520, 40)]
+
+
+@pytest.mark.parametrize("rows,hidden,inner", SIZES + SPLITS)
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_backward(rows, hidden, inner, dtype):
     for act in ("silu", "gelu_tanh"):
