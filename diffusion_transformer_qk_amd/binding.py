@@ -49,8 +49,8 @@ EXPORTS = ("qknorm_rope_fused", "qknorm_rope_strerror", "qknorm_rope_version",
            "dit_layer_norm_backward_workspace_size", "dit_layer_norm_backward",
            "qknorm_rope_backward_workspace_size", "qknorm_rope_backward", "dit_rms_norm",
            "dit_rms_norm_backward_workspace_size", "dit_rms_norm_backward",
-           "dit_gated_feed_forward_workspace_size", "dit_gated_feed_forward",
-           "dit_gated_feed_forward_backward_workspace_size", "dit_gated_feed_forward_backward",
+           "dit_gated_feed_forward", "dit_gated_feed_forward_backward_workspace_size",
+           "dit_gated_feed_forward_backward",
            "dit_attention_packed_workspace_size", "dit_attention_packed_backward_workspace_size",
            "dit_attention_packed", "dit_attention_packed_backward")
 MOD_DTYPES = {"bf16": QKR_BF16, "fp16": QKR_FP16, "fp32": QKR_FP32}
@@ -176,10 +176,9 @@ def load_library(path: str = LIB_PATH):
     lib.dit_rms_norm_backward.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, vp, f32, i32, vp, i64, vp]
     lib.dit_rms_norm_backward.restype = ctypes.c_int
     ff = ctypes.POINTER(FfArgs)
-    for name in ("dit_gated_feed_forward_workspace_size", "dit_gated_feed_forward_backward_workspace_size"):
-        getattr(lib, name).argtypes = [ff]
-        getattr(lib, name).restype = i64
-    lib.dit_gated_feed_forward.argtypes = [ff, *[vp] * 10, i64, vp]
+    lib.dit_gated_feed_forward_backward_workspace_size.argtypes = [ff]
+    lib.dit_gated_feed_forward_backward_workspace_size.restype = i64
+    lib.dit_gated_feed_forward.argtypes = [ff, *[vp] * 10]
     lib.dit_gated_feed_forward.restype = ctypes.c_int
     lib.dit_gated_feed_forward_backward.argtypes = [ff, *[vp] * 10, i64, vp]
     lib.dit_gated_feed_forward_backward.restype = ctypes.c_int
@@ -219,6 +218,7 @@ def qknorm_rope_fused_raw(qkv: int, q: int, k: int, tokens: int, heads: int, hea
 
 
 _torch_module = None
+_NO_CONTEXT = contextlib.nullcontext()      # (it may be entered any number of times)
 
 
 def _torch():
@@ -286,7 +286,7 @@ def _call_context(ref, tensors, stream):
     # switching the current device costs a few µs per call: only when needed
     if ref.is_cuda and dev.index != torch.cuda.current_device():
         return torch.cuda.device(dev), raw
-    return contextlib.nullcontext(), raw
+    return _NO_CONTEXT, raw
 
 
 def _launch_stream_context(ref, stream):
@@ -295,12 +295,12 @@ def _launch_stream_context(ref, stream):
     memory to other work only in that stream's order (memory allocated on the
     current stream and freed on return could be reused by the current stream
     while the launch stream still uses it)."""
-    torch = _torch()
     if stream is None or not ref.is_cuda:
-        return contextlib.nullcontext()
+        return _NO_CONTEXT
+    torch = _torch()
     if isinstance(stream, int):
         if stream == torch.cuda.current_stream(ref.device).cuda_stream:
-            return contextlib.nullcontext()
+            return _NO_CONTEXT
         stream = torch.cuda.ExternalStream(stream, device=ref.device)
     return torch.cuda.stream(stream)
 
@@ -739,9 +739,9 @@ def attention_packed(q, k, v, offsets, *, kv_offsets=None, causal: bool = False,
         workspace, ws_bytes = _attn_workspace(lib.dit_attention_packed_workspace_size, args, workspace,
                                               q.device)
         if out is None:
-            out = (torch.empty if args.fill_rest else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
+            out = (q.new_empty if args.fill_rest else q.new_zeros)(q.shape)
         if lse is None:
-            lse = torch.empty(_lse_shape(q), dtype=torch.float32, device=q.device)
+            lse = q.new_empty(_lse_shape(q), dtype=torch.float32)
             if not args.fill_rest:
                 lse.fill_(-float("inf"))
     if out.shape != q.shape or out.dtype != q.dtype:
@@ -765,19 +765,18 @@ def attention_packed_backward(dout, q, k, v, out, lse, offsets, *, kv_offsets=No
     Rows of no sequence are left as they are in gradients that are given, and 0
     in those made here.
     """
-    torch = _torch()
     lib = load_library()
     args = _packed_args(q, k, v, offsets, kv_offsets, causal, scale, dq is None and dk is None and dv is None)
-    make = torch.empty if args.fill_rest else torch.zeros
+    make = q.new_empty if args.fill_rest else q.new_zeros
     with _launch_stream_context(q, stream):
         workspace, ws_bytes = _attn_workspace(lib.dit_attention_packed_backward_workspace_size, args,
                                               workspace, q.device)
         if dq is None:
-            dq = make(q.shape, dtype=q.dtype, device=q.device)
+            dq = make(q.shape)
         if dk is None:
-            dk = make(k.shape, dtype=k.dtype, device=k.device)
+            dk = make(k.shape)
         if dv is None:
-            dv = make(v.shape, dtype=v.dtype, device=v.device)
+            dv = make(v.shape)
     for name, t, like in (("dout", dout, q), ("out", out, q), ("dq", dq, q), ("dk", dk, k),
                           ("dv", dv, v)):
         if t.shape != like.shape or t.dtype != like.dtype:
@@ -991,11 +990,12 @@ def rms_norm_fp8(x, weight=None, *, residual=None, sum_out=None, out=None, scale
     with _launch_stream_context(x, stream):
         sum_out = _rms_norm_sum(x, weight, residual, sum_out)
         if out is None:
-            out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+            # (contiguous whatever x's strides are; empty_like is half of empty's 2.3 us)
+            out = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
         elif out.shape != x.shape or out.dtype != torch.float8_e4m3fn:
             raise ValueError("out must be float8_e4m3fn in x's shape")
         if scales is None:
-            scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
         elif scales.shape != x.shape[:-1] or scales.dtype != torch.float32:
             raise ValueError("scales must be float32, one a row of x")
     _rms_norm(x, weight, residual, sum_out, out, scales, eps, stream)
@@ -1037,8 +1037,8 @@ def rms_norm_backward(dy, x, weight=None, *, dsum=None, out=None, eps: float = 1
     ws_bytes = 0
     with _launch_stream_context(x, stream):
         if param_grads:
-            make = torch.empty if rows else torch.zeros     # without rows the sum is empty
-            dweight = make(hidden, dtype=torch.float32, device=x.device)
+            make = x.new_empty if rows else x.new_zeros     # without rows the sum is empty
+            dweight = make(hidden, dtype=torch.float32)
             if workspace is None:
                 ws_bytes = lib.dit_rms_norm_backward_workspace_size(rows, hidden)
                 if ws_bytes < 0:
@@ -1228,14 +1228,14 @@ def gated_feed_forward(x, w_gate, w_up, *, activation: str = "silu", x_scale=Non
             if t is not None:
                 _ff_like(t, shape, dtype, name)
             elif wanted:
-                t = torch.empty(shape, dtype=dtype, device=x.device)
+                t = x.new_empty(shape, dtype=dtype)
             made.append(t)
     out, gate, up = made
     ctx, stream_ptr = _call_context(x, (w_gate, w_up, x_scale, gate_scale, up_scale, out, gate, up), stream)
     with ctx:
         status = lib.dit_gated_feed_forward(args, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(x_scale),
                                             _ptr(gate_scale), _ptr(up_scale), _ptr(out), _ptr(gate), _ptr(up),
-                                            None, 0, stream_ptr)
+                                            stream_ptr)
     _check(status)
     return (out, gate, up) if save else out
 
@@ -1278,7 +1278,7 @@ def gated_feed_forward_backward(dh, x, w_gate, w_up, gate, up, *, activation: st
             if t is not None:
                 _ff_like(t, like.shape, like.dtype, name)
             elif wanted:
-                t = torch.empty(like.shape, dtype=like.dtype, device=x.device)
+                t = like.new_empty(like.shape)
             made.append(t)
         ws_bytes = 0
         if workspace is None:
@@ -1286,7 +1286,7 @@ def gated_feed_forward_backward(dh, x, w_gate, w_up, gate, up, *, activation: st
             if ws_bytes < 0:
                 raise QkrError(ws_bytes, strerror(ws_bytes))
             if ws_bytes > 0:
-                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+                workspace = x.new_empty(ws_bytes, dtype=torch.uint8)
         else:
             ws_bytes = workspace.numel() * workspace.element_size()
     dx, dw_gate, dw_up = made

@@ -172,19 +172,12 @@ Fn select(int dtype, int out_dtype, int activation)
 
 }  // namespace
 
-extern "C" int64_t dit_gated_feed_forward_workspace_size(const dit_ff_args* args)
-{
-    return qkr_ff_host::check_args(args, true);
-}
-
 extern "C" int dit_gated_feed_forward(const dit_ff_args* args, const void* x, const void* w_gate,
                                       const void* w_up, const float* x_scale, const float* gate_scale,
                                       const float* up_scale, void* h, void* gate, void* up,
-                                      void* workspace, int64_t workspace_bytes, void* stream)
+                                      void* stream)
 {
     using namespace qkr_ff_host;
-    (void)workspace;
-    (void)workspace_bytes;
     const int rc = check_args(args, true);
     if (rc != QKR_OK)
         return rc;

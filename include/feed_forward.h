@@ -67,10 +67,9 @@ typedef struct {
                          /* unless that is e4m3                                      */
 } dit_ff_args;
 
-/* Bytes of workspace that the calls need (0: none), or a negative QKR_ERR_*
- * code.  16-byte aligned scratch, not shared by calls that may run at the same
- * time. */
-int64_t dit_gated_feed_forward_workspace_size(const dit_ff_args* args);
+/* Bytes of workspace that the backward pass needs (0: none), or a negative
+ * QKR_ERR_* code.  16-byte aligned scratch, not shared by calls that may run at
+ * the same time. */
 int64_t dit_gated_feed_forward_backward_workspace_size(const dit_ff_args* args);
 
 /*
@@ -82,8 +81,7 @@ int64_t dit_gated_feed_forward_backward_workspace_size(const dit_ff_args* args);
  */
 int dit_gated_feed_forward(const dit_ff_args* args, const void* x, const void* w_gate,
                            const void* w_up, const float* x_scale, const float* gate_scale,
-                           const float* up_scale, void* h, void* gate, void* up, void* workspace,
-                           int64_t workspace_bytes, void* stream);
+                           const float* up_scale, void* h, void* gate, void* up, void* stream);
 
 /*
  * dit_gated_feed_forward_backward -- dx, dw_gate and dw_up, of the tensors'

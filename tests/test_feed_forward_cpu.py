@@ -28,7 +28,7 @@ def forward(a=None, **over):
     v = dict(x=A, w_gate=A + FAR, w_up=A + 2 * FAR, xs=A + 3 * FAR if fp8 else 0, gs=A + 4 * FAR if fp8 else 0,
              us=A + 5 * FAR if fp8 else 0, h=A + 6 * FAR, gate=A + 7 * FAR, up=A + 8 * FAR)
     v.update(over)
-    return b.load_library().dit_gated_feed_forward(a, *v.values(), 0, 0, 0)
+    return b.load_library().dit_gated_feed_forward(a, *v.values(), 0)
 
 
 def backward(a=None, **over):
@@ -149,11 +149,11 @@ int main(void)
 {
     dit_ff_args a = {16, 64, 128, DIT_FF_SILU, QKR_BF16, QKR_BF16};
     if (dit_gated_feed_forward_backward_workspace_size(&a) < 4 * 16 * 128) return 1;
-    if (dit_gated_feed_forward(&a, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != QKR_ERR_NULL) return 2;
+    if (dit_gated_feed_forward(&a, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != QKR_ERR_NULL) return 2;
     a.dtype = DIT_FF_E4M3;
     if (dit_gated_feed_forward_backward(&a, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != QKR_ERR_UNSUPPORTED) return 3;
     a.activation = DIT_FF_GELU_TANH, a.rows = 0;
-    if (dit_gated_feed_forward(&a, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != QKR_OK) return 4;
+    if (dit_gated_feed_forward(&a, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != QKR_OK) return 4;
     if (dit_rms_norm(0, 0, 0, 0, 0, 0, DIT_RMS_MAX_HIDDEN, 0, QKR_FP32, 1e-6f, QKR_FP16, 0) != QKR_OK) return 5;
     if (dit_rms_norm_backward(0, 0, 0, 0, 1, 64, 0, QKR_FP32, 0, 1e-6f, QKR_FP16, 0, 0, 0) != QKR_ERR_NULL) return 6;
     if (dit_rms_norm_backward_workspace_size(1, 60) != QKR_ERR_UNSUPPORTED) return 7;
