@@ -266,7 +266,7 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const BlockOf block(bid, p.pairs, p.key_blocks * p.row_splits);
+    const BlockOf<> block(bid, p.pairs, p.key_blocks * p.row_splits);
     // causal: the first key blocks are seen by most queries; turning the order
     // from split to split keeps them from meeting on the same CUs
     const int split = block.part / p.key_blocks;
@@ -502,7 +502,7 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const BlockOf block(bid, p.pairs, p.row_blocks * p.key_splits);
+    const BlockOf<> block(bid, p.pairs, p.row_blocks * p.key_splits);
     const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
     const uint32_t bh = block.pair;
     const int64_t b = bh / (uint32_t)p.kv_heads;

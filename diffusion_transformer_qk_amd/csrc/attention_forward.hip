@@ -75,7 +75,7 @@ __device__ __forceinline__ void forward_block(const FwdParams& p, char* lds)
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const BlockOf block(blockIdx.x, p.pairs, p.row_blocks * p.splits);
+    const BlockOf<PACKED> block(blockIdx.x, p.pairs, p.row_blocks * p.splits);
     const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
     const uint32_t bh = block.pair;                      // sample, key head
     const int64_t b = bh / (uint32_t)p.kv_heads;
