@@ -4,8 +4,10 @@
 //
 // A workgroup computes C[a, b] = sum_k A[a, k] B[b, k] for a tile of A rows and
 // a tile of B rows, with a down the registers and b across the lanes of
-// v_mfma_f32_32x32x16 (32x32x64 for 8 bits), so that a, the operand of the
-// contiguous dimension of the output, leaves 16 bytes of a row in a lane.
+// v_mfma_f32_16x16x32 (32x32x64 for 8 bits), so that a, the operand of the
+// contiguous dimension of the output, leaves 8 bytes of a row in a lane.  (What a
+// large product may take is bounded by the card's power: on random numbers loops of
+// the 16x16x32 instruction alone reach 2040 TFLOP/s, of 32x32x16 1730.)
 //
 // An operand's matrix holds k along its rows (kRows: row a of the matrix is row a
 // of the operand) or down its rows (kColumns: column a of the matrix is row a of
@@ -349,12 +351,10 @@ struct Product {
         }
     }
 
-    // Stores a piece: `row` is block i's first column in the lane's output row, of which
-    // `left` columns are there.  The lanes that hold neighbouring runs trade them, so that
-    // each stores 16 bytes.
+    // A piece in 16 bits: the lanes that hold neighbouring runs trade them, so that each
+    // has 16 bytes of a row, from column packed_column() of the block on.
     template <bool F16>
-    static __device__ __forceinline__ void store_piece(uint16_t* row, const float (&v)[8], int p, int lane, bool valid,
-                                                       int left)
+    static __device__ __forceinline__ u32x4 packed(const float (&v)[8])
     {
         u32x4 w;
 #pragma unroll
@@ -370,7 +370,22 @@ struct Product {
                 w[2 + j] = r[1];
             }
         }
-        const int at = T == kFp8 ? p % 2 * 16 + lane / 32 * 8 : (lane >> 4 & 1) * 16 + (lane >> 5) * 8;
+        return w;
+    }
+
+    static __device__ __forceinline__ int packed_column(int p, int lane)
+    {
+        return T == kFp8 ? p % 2 * 16 + lane / 32 * 8 : (lane >> 4 & 1) * 16 + (lane >> 5) * 8;
+    }
+
+    // Stores a piece: `row` is block i's first column in the lane's output row, of which
+    // `left` columns are there.
+    template <bool F16>
+    static __device__ __forceinline__ void store_piece(uint16_t* row, const float (&v)[8], int p, int lane, bool valid,
+                                                       int left)
+    {
+        const u32x4 w = packed<F16>(v);
+        const int at = packed_column(p, lane);
         if (valid && at < left)
             store16<false>(row + at, w);
     }

@@ -29,44 +29,106 @@ struct FwdParams {
     uint32_t row_tiles, inner_tiles;  // of the grid
 };
 
-// The epilogue of a wave's sums: rows from r0 on, columns from i0 on.
+// The epilogue of a wave's sums: rows from r0 on, columns from i0 on.  Two blocks of
+// columns leave as rows of 128 bytes, whole lines, through the wave's `own` 12 KB of
+// LDS, 32 rows of each matrix at a time; one block, whose rows are half a line, leaves
+// from the registers.  (4608 rows of 6144, 16384 columns, gate and up kept: 1455 us
+// from the registers, 1412 so; of 8 bits, whose lanes hold quarters of a line, 902 and
+// 747; without gate and up within 1%.)
 template <int T, bool F16, int ACT, int BLOCKS, typename P>
-__device__ __forceinline__ void finish(const FwdParams& p, P& c, int64_t r0, int i0, int lane)
+__device__ __forceinline__ void finish(const FwdParams& p, P& c, int64_t r0, int i0, int lane, char* own)
 {
-    unrolled<P::kPieces * BLOCKS>([&](auto number) __attribute__((always_inline)) {
-        constexpr int q = decltype(number)::value / BLOCKS, i = decltype(number)::value % BLOCKS;
-        const int64_t r = r0 + P::piece_row(q, lane);
-        const bool valid = r < p.rows;
-        const int a0 = i0 + 32 * i, left = p.inner - a0;
-        float gate[8], up[8];
+    constexpr int kRowRuns = T == kFp8 ? P::kPieces / 2 : 1;         // rows of a lane that have a scale
+    // all scales at once: one wait for memory
+    float s[kRowRuns];
+    f32x4 gs[BLOCKS][2][2], us[BLOCKS][2][2];
+    if constexpr (T == kFp8) {
+#pragma unroll
+        for (int q = 0; q < kRowRuns; ++q) {
+            const int64_t r = r0 + P::piece_row(2 * q, lane);
+            s[q] = r < p.rows ? p.x_scale[r] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < BLOCKS; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int a = i0 + 32 * i + P::piece_column(k / 2, lane, k % 2);
+                gs[i][k / 2][k % 2] = us[i][k / 2][k % 2] = f32x4{};
+                if (a < p.inner) {
+                    gs[i][k / 2][k % 2] = *reinterpret_cast<const f32x4u*>(p.gate_scale + a);
+                    us[i][k / 2][k % 2] = *reinterpret_cast<const f32x4u*>(p.up_scale + a);
+                }
+            }
+    }
+    const auto projections = [&](auto block, auto piece, float (&gate)[8], float (&up)[8])
+                                 __attribute__((always_inline)) {
+        constexpr int i = decltype(block)::value, q = decltype(piece)::value;
         c.template piece<i, q>(gate);
         c.template piece<i + BLOCKS, q>(up);
         if constexpr (T == kFp8) {
-            const float s = valid ? p.x_scale[r] : 0.0f;
 #pragma unroll
-            for (int run = 0; run < 2; ++run) {
-                const int a = P::piece_column(q, lane, run);
-                if (a < left) {
-                    const f32x4 gs = *reinterpret_cast<const f32x4u*>(p.gate_scale + a0 + a);
-                    const f32x4 us = *reinterpret_cast<const f32x4u*>(p.up_scale + a0 + a);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        gate[4 * run + k] *= s * gs[k];
-                        up[4 * run + k] *= s * us[k];
-                    }
-                }
+            for (int k = 0; k < 8; ++k) {
+                gate[k] *= s[q / 2] * gs[i][q % 2][k / 4][k % 4];
+                up[k] *= s[q / 2] * us[i][q % 2][k / 4][k % 4];
             }
         }
-        const int64_t at = r * p.inner + a0;
-        if (p.gate) {
-            P::template store_piece<F16>(p.gate + at, gate, q, lane, valid, left);
-            P::template store_piece<F16>(p.up + at, up, q, lane, valid, left);
-        }
+    };
+    if constexpr (BLOCKS == 1) {
+        unrolled<P::kPieces>([&](auto number) __attribute__((always_inline)) {
+            constexpr int q = decltype(number)::value;
+            const int64_t r = r0 + P::piece_row(q, lane);
+            const bool valid = r < p.rows;
+            const int left = p.inner - i0;
+            const int64_t at = r * p.inner + i0;
+            float gate[8], up[8];
+            projections(Flag<0>{}, number, gate, up);
+            if (p.gate) {
+                P::template store_piece<F16>(p.gate + at, gate, q, lane, valid, left);
+                P::template store_piece<F16>(p.up + at, up, q, lane, valid, left);
+            }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            gate[k] = activated<ACT>(gate[k]) * up[k];
-        P::template store_piece<F16>(p.h + at, gate, q, lane, valid, left);
-    });
+            for (int k = 0; k < 8; ++k)
+                gate[k] = activated<ACT>(gate[k]) * up[k];
+            P::template store_piece<F16>(p.h + at, gate, q, lane, valid, left);
+        });
+    } else {
+        static_assert(BLOCKS == 2 && P::kPieces == 4, "64 rows of 128 bytes");
+        constexpr int kMatrix = 32 * 128;            // 32 rows of h, gate and up
+        unrolled<P::kPieces * BLOCKS>([&](auto number) __attribute__((always_inline)) {
+            constexpr int q = decltype(number)::value / BLOCKS, i = decltype(number)::value % BLOCKS;
+            float gate[8], up[8];
+            projections(Flag<i>{}, Flag<q>{}, gate, up);
+            const int row = P::piece_row(q, lane) % 32, chunk = (32 * i + P::packed_column(q, lane)) / 8;
+            u32x4* at = reinterpret_cast<u32x4*>(own + row * 128 + ((chunk ^ (row & 7)) << 4));
+            if (p.gate) {
+                at[kMatrix / 16] = P::template packed<F16>(gate);
+                at[2 * kMatrix / 16] = P::template packed<F16>(up);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                gate[k] = activated<ACT>(gate[k]) * up[k];
+            at[0] = P::template packed<F16>(gate);
+            if constexpr (q % 2 == 1 && i == BLOCKS - 1) {
+                __asm__ volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the wave's own rows only
+                const auto leave = [&](uint16_t* out, int from) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int in = 8 * k + lane / 8, c8 = lane % 8;
+                        const int64_t r = r0 + q / 2 * 32 + in;
+                        const u32x4 w = *reinterpret_cast<const u32x4*>(own + from + in * 128 + ((c8 ^ (in & 7)) << 4));
+                        if (r < p.rows && i0 + 8 * c8 < p.inner)
+                            store16<false>(out + r * p.inner + i0 + 8 * c8, w);
+                    }
+                };
+                if (p.gate) {
+                    leave(p.gate, kMatrix);
+                    leave(p.up, 2 * kMatrix);
+                }
+                leave(p.h, 0);
+                __asm__ volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // read before they are written again
+            }
+        });
+    }
 }
 
 // Tiles of kRowsB rows of x and kRowsA / 2 columns of h.
@@ -93,7 +155,8 @@ void gated_feed_forward_kernel(const FwdParams p)
     P c;
     c.clear();
     c.add(la, lb, (p.k_bytes + kStageBytes - 1) / kStageBytes, lds_address(lds), wave, lane);
-    finish<T, F16, ACT, NA / 2>(p, c, r0 + 32 * P::first_b(wave), i0 + 32 * P::first_a(wave), lane);
+    finish<T, F16, ACT, NA / 2>(p, c, r0 + 32 * P::first_b(wave), i0 + 32 * P::first_a(wave), lane,
+                                lds + wave * 12288);
 }
 
 // Up to 32 rows of x: the call waits for the weights.  A workgroup takes 32 columns
@@ -145,7 +208,7 @@ void gated_feed_forward_few_kernel(const FwdParams p)
 #pragma unroll
         for (int n = 0; n < 32; ++n)
             sum(n)[n % kEach] += sums[w * (kRing / 4) + 64 * n];
-    finish<T, F16, ACT, 1>(p, c, 0, i0, lane);
+    finish<T, F16, ACT, 1>(p, c, 0, i0, lane, lds);
 }
 
 using Fn = void (*)(FwdParams);
