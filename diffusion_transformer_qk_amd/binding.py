@@ -678,6 +678,12 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, kv_leng
     return dq, dk, dv
 
 
+def _small(what: str, *sizes):
+    """Sizes that the C interface takes in 32 bits: ctypes would cut larger ones off."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("%s must be below 2^31" % what)
+
+
 def _packed_args(q, k, v, offsets, kv_offsets, causal, scale, fill) -> AttnPackedArgs:
     torch = _torch()
     if q.dim() != 3 or k.dim() != 3:
@@ -690,6 +696,7 @@ def _packed_args(q, k, v, offsets, kv_offsets, causal, scale, fill) -> AttnPacke
     kv_heads = k.shape[1]
     if kv_heads < 1 or heads % kv_heads:
         raise ValueError("the number of query heads must be a multiple of k's and v's")
+    _small("heads and head_dim", heads, head_dim)
     if kv_offsets is None and k.shape[0] != q_tokens:
         raise ValueError("k and v of other tokens than q need kv_offsets")
     if offsets.dim() != 1 or offsets.numel() < 1 or offsets.dtype != torch.int32:
@@ -942,6 +949,7 @@ def _rms_norm_sum(x, weight, residual, sum_out):
     """The checks that both forms share; sum_out, made here if there is a residual."""
     if x.dim() < 1:
         raise ValueError("x must be [..., hidden]")
+    _small("hidden", x.shape[-1])
     if weight is not None and weight.shape != x.shape[-1:]:
         raise ValueError("weight must be [%d]" % x.shape[-1])
     if residual is None:
@@ -1025,6 +1033,7 @@ def rms_norm_backward(dy, x, weight=None, *, dsum=None, out=None, eps: float = 1
     if x.dim() < 1:
         raise ValueError("x must be [..., hidden]")
     hidden = x.shape[-1]
+    _small("hidden", hidden)
     rows = x.numel() // hidden if x.numel() else 0
     if weight is not None and weight.shape != (hidden,):
         raise ValueError("weight must be [%d]" % hidden)
@@ -1175,6 +1184,7 @@ def _ff_args(x, w_gate, w_up, activation, out_dtype=None) -> FfArgs:
     if w_gate.dtype != x.dtype or w_up.dtype != x.dtype:
         raise ValueError("x, w_gate and w_up must have one dtype")
     inner, hidden = w_gate.shape
+    _small("hidden and inner", hidden, inner)
     if x.dtype == torch.float8_e4m3fn:
         dtype = DIT_FF_E4M3
         out = {None: QKR_BF16, torch.bfloat16: QKR_BF16, torch.float16: QKR_FP16}.get(out_dtype)
