@@ -128,7 +128,7 @@ def test_forward_in_8_bits(rows, hidden, inner):
 @pytest.mark.parametrize("rows,hidden,inner", [(4200, 96, 2056), (257, 200, 16392), (5000, 104, 1800)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_large_tiles(rows, hidden, inner, dtype):
-    """Calls of 256 x 256 tiles, at sizes that end inside one."""
+    """Several rounds of tiles, at sizes that end inside one."""
     t = tensors(3, rows, hidden, inner, dtype)
     check_forward(t["x"], t["w_gate"], t["w_up"], "silu")
     t8 = tensors(4, rows, 16 * -(-hidden // 16), 16 * -(-inner // 16), "fp32")
@@ -219,6 +219,27 @@ def test_large_tiles_backward(rows, hidden, inner, dtype):
 @pytest.mark.parametrize("by", [2.0 ** -14, 1.0, 2.0 ** 10])
 def test_small_and_large_gradients_in_fp16(by):
     check_backward(backward_inputs(7, 70, 136, 200, "fp16", by), "silu")
+
+
+# These fill the chip once with 256 x 256 tiles and more than once with 128 x 128 ones, which
+# is what the larger tiles are taken for.
+@pytest.mark.parametrize("rows,hidden,inner", [(3900, 96, 1960), (300, 200, 16328), (520, 1040, 8008)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_one_round_of_large_tiles(rows, hidden, inner, dtype):
+    for act in ("silu", "gelu_tanh"):
+        t = tensors(9, rows, hidden, inner, dtype)
+        check_forward(t["x"], t["w_gate"], t["w_up"], act)
+        t8 = tensors(10, rows, 16 * -(-hidden // 16), 16 * (inner // 16), "fp32")
+        (x, xs), (wg, gs), (wu, us) = (in_8_bits(t8[n]) for n in ("x", "w_gate", "w_up"))
+        check_forward(x, wg, wu, act, (xs, gs, us), TYPES[dtype])
+
+
+# dx; dw; dw over splits of the rows; dx over splits
+@pytest.mark.parametrize("rows,hidden,inner", [(3900, 3920, 72), (136, 3920, 1960), (40000, 1480, 744),
+                                               (1480, 1480, 20000)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_one_round_of_large_tiles_backward(rows, hidden, inner, dtype):
+    check_backward(backward_inputs(11, rows, hidden, inner, dtype), "gelu_tanh")
 
 
 def test_gradients_against_differences():
