@@ -237,7 +237,6 @@ __device__ __forceinline__ float largest_packed(const float* v, int64_t head, in
 
 constexpr int kWaves = 4;
 constexpr int kTileRows = 64;      // queries (dk and dv) or keys (dq) staged at a time
-constexpr int kFewRows = 32;
 
 // What bounds it: the matrix cores together with what feeds them, at the clock
 // that the power leaves (1.7 to 1.9 of 2.4 GHz).  They are busy 58 to 60% of the
@@ -670,7 +669,7 @@ __device__ __forceinline__ void query_gradients(const BwdParams& p, const char* 
 //
 // TWO: p and ds go into the products as two 16-bit terms, the second being what
 // the rounding of the first left, so that the gradients are off by their own
-// rounding alone.  It is for calls of up to kFewRows rows a key head, which wait
+// rounding alone.  It is for calls of up to kTwoTermRows rows a key head, which wait
 // for memory and launches (16 queries over 32760 keys, 5 heads of 128: 76 us,
 // 70 with one term; 2 x 1 over 256, 24 heads of 64: 18 us with either).
 constexpr int backward_waves(int d, bool f16, bool two)
@@ -851,7 +850,7 @@ hipError_t launch(BwdParams p, hipStream_t st)
     };
     go(row_stats_kernel<D, F16, PACKED>, p.batch * p.heads * p.stat_blocks + (F16 ? pairs * p.value_blocks : 0));
     go(PACKED                ? packed_backward_kernel<D, F16, CAUSAL>
-       : p.rows <= kFewRows ? attention_backward_kernel<D, F16, CAUSAL, true>
+       : p.rows <= kTwoTermRows ? attention_backward_kernel<D, F16, CAUSAL, true>
                             : attention_backward_kernel<D, F16, CAUSAL, false>,
        pairs * ((int64_t)p.key_blocks * p.row_splits + (int64_t)p.row_blocks * p.key_splits));
     go(attention_sum_kernel<D, F16, PACKED>, sum_blocks<D, true>(p) + sum_blocks<D, false>(p));

@@ -39,6 +39,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Query rows a key head, of a sample or a packed sequence, up to which p and ds go
+// into their products in two terms (dit_attention.h).
+constexpr int kTwoTermRows = 32;
 constexpr uint32_t kRawBuffer = 0x00020000u;   // raw buffer resource, 32-bit data
 
 // The (pair, part) of hardware block `bid`, for `pairs` (sample, key head) pairs

@@ -63,47 +63,29 @@ constexpr int tile_keys(int d, int waves) { return d == 64 && waves == 4 ? 64 : 
 // Bytes of LDS: [buffer][K, V].
 constexpr int lds_bytes(int d, int waves) { return 4 * tile_keys(d, waves) * d * 2; }
 
-template <int D, bool F16, bool CAUSAL, int NW, bool PACKED>
-__device__ __forceinline__ void forward_block(const FwdParams& p, char* lds)
+// What a workgroup computes.
+struct Work {
+    uint32_t bh;                           // sample, key head
+    int split, mb;                         // of the keys; block of rows, of the sample or sequence
+    int q_tokens, kv_tokens, rows, len;    // of the sample or sequence; len: its keys that are there
+    int64_t q_at, kv_at;                   // the sequence's first rows
+};
+
+// TWO: p has a second term, what its rounding to 16 bits left: out is then off by
+// its own rounding alone.
+template <int D, bool F16, bool CAUSAL, int NW, bool PACKED, bool TWO>
+__device__ __forceinline__ void forward_rows(const FwdParams& p, const Work& w, char* lds)
 {
     constexpr int BM = NW * 32, BN = tile_keys(D, NW), KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
-    // With one wave the call waits for memory, and p can have a second term,
-    // what its rounding to 16 bits left: out is then off by its own rounding
-    // alone.
-    constexpr bool kTwoTerms = NW == 1;
     const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-
-    const BlockOf<PACKED> block(blockIdx.x, p.pairs, p.row_blocks * p.splits);
-    const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
-    const uint32_t bh = block.pair;                      // sample, key head
+    const uint32_t bh = w.bh;
     const int64_t b = bh / (uint32_t)p.kv_heads;
     const int hk = bh % (uint32_t)p.kv_heads;
-    int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;         // the longest first
-
-    int q_tokens = p.q_tokens, kv_tokens = p.kv_tokens, rows = p.rows;
-    int64_t q_at = 0, kv_at = 0;           // the sequence's first rows
-    int len = p.kv_tokens;
-    if constexpr (PACKED) {
-        const int seq = sequence_of<BM>(p.q_rows, p.group, mb_raw);
-        const int q0 = p.q_rows.first(seq), k0 = p.kv_rows.first(seq);
-        q_tokens = p.q_rows.first(seq + 1) - q0;
-        kv_tokens = p.q_rows.rest(seq) ? 0 : p.kv_rows.first(seq + 1) - k0;
-        q_tokens = __builtin_amdgcn_readfirstlane(q_tokens < 0 ? 0 : q_tokens);
-        kv_tokens = len = __builtin_amdgcn_readfirstlane(kv_tokens < 0 ? 0 : kv_tokens);
-        q_at = __builtin_amdgcn_readfirstlane(q0);
-        kv_at = __builtin_amdgcn_readfirstlane(k0);
-        rows = q_tokens * p.group;
-        const int blocks = (rows + BM - 1) / BM, at = mb_raw - first_block<BM>(p.q_rows, p.group, seq);
-        mb = __builtin_amdgcn_readfirstlane(CAUSAL ? blocks - 1 - at : at);
-        // more blocks than the sequence needs, or rows that are left alone
-        if (at < 0 || at >= blocks || (p.q_rows.rest(seq) && !p.fill_rest))
-            return;
-    } else if (p.kv_lengths) {
-        const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
-        len = given < 0 ? 0 : given < len ? given : len;
-    }
+    const int split = w.split, mb = w.mb;
+    const int q_tokens = w.q_tokens, kv_tokens = w.kv_tokens, rows = w.rows, len = w.len;
+    const int64_t q_at = w.q_at, kv_at = w.kv_at;
     const int r0 = mb * BM + wave * 32;
     const int r = r0 + n < rows ? r0 + n : rows - 1;              // this lane's row
     const int qi = r / p.group, head = hk * p.group + r % p.group;
@@ -226,13 +208,13 @@ __device__ __forceinline__ void forward_block(const FwdParams& p, char* lds)
             for (int k = 0; k < 2; ++k) {
                 const u32x4 pf = pack_b<F16>(s[j], k);
                 u32x4 rest;
-                if constexpr (kTwoTerms)
+                if constexpr (TWO)
                     rest = pack_rest<F16>(s[j], k, pf);
 #pragma unroll
                 for (int i = 0; i < DB; ++i) {
                     const u32x4 vf = tr_fragment(at, kTile + j * block_bytes<D>(), k, i);
                     o[i] = mfma<F16>(vf, pf, o[i]);
-                    if constexpr (kTwoTerms)
+                    if constexpr (TWO)
                         o[i] = mfma<F16>(vf, rest, o[i]);
                 }
             }
@@ -262,6 +244,46 @@ __device__ __forceinline__ void forward_block(const FwdParams& p, char* lds)
             store_column_f32(p.part_o + slot * D + 32 * i, o[i], inv, g, valid);
         if (valid && g == 0)
             p.part_lse[slot] = lse2;
+    }
+}
+
+// Two terms go to the samples and sequences of up to kTwoTermRows rows a key head, whose
+// calls wait for memory.  Of packed sequences each goes by its own rows, whatever the
+// others are, so both forms are in the kernel.
+template <int D, bool F16, bool CAUSAL, int NW, bool PACKED>
+__device__ __forceinline__ void forward_block(const FwdParams& p, char* lds)
+{
+    constexpr int BM = NW * 32;
+    const BlockOf<PACKED> block(blockIdx.x, p.pairs, p.row_blocks * p.splits);
+    const int mb_raw = block.part % p.row_blocks;
+    Work w = {block.pair, block.part / p.row_blocks, 0, p.q_tokens, p.kv_tokens, p.rows, p.kv_tokens, 0, 0};
+    w.mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;           // the longest first
+    if constexpr (PACKED) {
+        const int seq = sequence_of<BM>(p.q_rows, p.group, mb_raw);
+        const int q0 = p.q_rows.first(seq), k0 = p.kv_rows.first(seq);
+        const int q_tokens = p.q_rows.first(seq + 1) - q0;
+        const int kv_tokens = p.q_rows.rest(seq) ? 0 : p.kv_rows.first(seq + 1) - k0;
+        w.q_tokens = __builtin_amdgcn_readfirstlane(q_tokens < 0 ? 0 : q_tokens);
+        w.kv_tokens = w.len = __builtin_amdgcn_readfirstlane(kv_tokens < 0 ? 0 : kv_tokens);
+        w.q_at = __builtin_amdgcn_readfirstlane(q0);
+        w.kv_at = __builtin_amdgcn_readfirstlane(k0);
+        w.rows = w.q_tokens * p.group;
+        const int blocks = (w.rows + BM - 1) / BM, at = mb_raw - first_block<BM>(p.q_rows, p.group, seq);
+        w.mb = __builtin_amdgcn_readfirstlane(CAUSAL ? blocks - 1 - at : at);
+        // more blocks than the sequence needs, or rows that are left alone
+        if (at < 0 || at >= blocks || (p.q_rows.rest(seq) && !p.fill_rest))
+            return;
+        if (w.rows <= kTwoTermRows)
+            forward_rows<D, F16, CAUSAL, NW, true, true>(p, w, lds);
+        else
+            forward_rows<D, F16, CAUSAL, NW, true, false>(p, w, lds);
+    } else {
+        if (p.kv_lengths) {
+            const int64_t b = block.pair / (uint32_t)p.kv_heads;
+            const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
+            w.len = given < 0 ? 0 : given < w.len ? given : w.len;
+        }
+        forward_rows<D, F16, CAUSAL, NW, false, NW == 1>(p, w, lds);
     }
 }
 
