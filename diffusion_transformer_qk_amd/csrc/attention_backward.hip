@@ -233,10 +233,47 @@ __device__ __forceinline__ float largest_packed(const float* v, int64_t head, in
     return block_max<4>(top, slot);
 }
 
-// ---------------------------------------------------------------- dk and dv
-
 constexpr int kWaves = 4;
 constexpr int kTileRows = 64;      // queries (dk and dv) or keys (dq) staged at a time
+
+// What a workgroup computes.
+struct Work {
+    uint32_t bh;                           // sample, key head
+    int split, block, seq;                 // of the tiles; of keys or rows, of the sample or sequence
+    int q_tokens, kv_tokens, rows, len;    // of the sample or sequence; len: its keys that are there
+    int64_t q_at, kv_at;                   // the sequence's first rows
+
+    __device__ __forceinline__ Work(const BwdParams& p, uint32_t bh, int split, int block)
+        : bh(bh), split(split), block(block), seq(0), q_tokens(p.q_tokens), kv_tokens(p.kv_tokens),
+          rows(p.rows), len(p.kv_tokens), q_at(0), kv_at(0)
+    {
+    }
+
+    // `of`: the block that is `block` of all sequences' together, and there()
+    template <int SIZE>
+    __device__ __forceinline__ void in_sequence(const BwdParams& p, const PackedBlock<SIZE>& of)
+    {
+        const bool rest = p.q_rows.rest(of.seq);
+        seq = of.seq;
+        block = of.at;
+        q_at = of.q_at;
+        kv_at = of.kv_at;
+        q_tokens = of.q_tokens;
+        kv_tokens = of.kv_tokens;
+        rows = q_tokens * p.group;
+        len = rest ? 0 : kv_tokens;
+    }
+
+    __device__ __forceinline__ void in_sample(const BwdParams& p)
+    {
+        if (p.kv_lengths) {
+            const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[bh / (uint32_t)p.kv_heads]);
+            len = given < 0 ? 0 : given < len ? given : len;
+        }
+    }
+};
+
+// ---------------------------------------------------------------- dk and dv
 
 // What bounds it: the matrix cores together with what feeds them, at the clock
 // that the power leaves (1.7 to 1.9 of 2.4 GHz).  They are busy 58 to 60% of the
@@ -255,42 +292,32 @@ constexpr int kTileRows = 64;      // queries (dk and dv) or keys (dq) staged at
 // scores of all and half the columns of dk and dv.  That is 6 products for 4, but
 // twice the workgroups, for calls that leave CUs idle (8 heads of 512 tokens: 44
 // against 55 us; 16 heads of 4096, which do not: 1409 against 1083).
+//
+// PACKED: with one term and with two in one kernel, both have to fit into the same
+// registers: nothing that follows from the lane is shared, and held, by the two, and
+// barriers to the scheduler keep the operands of the last products (k = 0 and 1) apart,
+// which is also what one term runs best with (sequences of 4096 to 221, 40 heads of 128:
+// 1345 us, 1375 without; 2048, 1021, 700, 355, 13 and 1 causal, 40 heads on 8: 362 and 453).
 template <int D, bool F16, bool CAUSAL, bool TWO, int DS, bool PACKED>
-__device__ __forceinline__ void key_gradients(const BwdParams& p, const char* lds, float* tops,
-                                              uint32_t bid)
+__device__ __forceinline__ void key_gradients(const BwdParams& p, const Work& w, const char* lds, float* tops)
 {
     constexpr int NW = kWaves;
-    constexpr int BK = NW / DS * 32, BQ = kTileRows, QB = BQ / 32, DB = D / 32 / DS;
+    constexpr int BK = NW / DS * 32, BQ = kTileRows, DB = D / 32 / DS;
+    constexpr int QB = PACKED && TWO ? 1 : BQ / 32;       // a tile's rows past kTwoTermRows are nobody's
+    constexpr bool kApart = D == 256 || (PACKED && (D == 64 || !TWO));
     constexpr int kTile = BQ * D * 2;
-    const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
+    int lane = threadIdx.x % 64;
+    if constexpr (PACKED && TWO)
+        __asm__ volatile("" : "+v"(lane));
+    const int n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const BlockOf<> block(bid, p.pairs, p.key_blocks * p.row_splits);
-    // causal: the first key blocks are seen by most queries; turning the order
-    // from split to split keeps them from meeting on the same CUs
-    const int split = block.part / p.key_blocks;
-    int kb = (block.part + (CAUSAL ? split : 0)) % p.key_blocks;
-    const uint32_t bh = block.pair;
-    const int64_t b = bh / (uint32_t)p.kv_heads;
-    const int hk = bh % (uint32_t)p.kv_heads;
-    int len = p.kv_tokens, seq = 0;
-    int q_tokens = p.q_tokens, kv_tokens = p.kv_tokens;
-    int64_t q_at = 0, kv_at = 0;           // the sequence's first rows
-    if constexpr (PACKED) {
-        const PackedBlock<BK> of(p, p.kv_rows, 1, kb);
-        if (!of.there(p, of.kv_tokens))
-            return;
-        seq = of.seq;
-        kb = of.at;
-        q_at = of.q_at;
-        kv_at = of.kv_at;
-        kv_tokens = of.kv_tokens;
-        q_tokens = p.q_rows.rest(seq) ? 0 : of.q_tokens;
-        len = q_tokens ? kv_tokens : 0;
-    } else if (p.kv_lengths) {
-        const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
-        len = given < 0 ? 0 : given < len ? given : len;
-    }
+    const uint32_t bh = w.bh;
+    const int64_t b = PACKED ? 0 : bh / (uint32_t)p.kv_heads;
+    const int hk = PACKED ? bh : bh % (uint32_t)p.kv_heads;
+    const int split = w.split, kb = w.block, seq = w.seq;
+    const int q_tokens = w.q_tokens, kv_tokens = w.kv_tokens, len = w.len;
+    const int64_t q_at = w.q_at, kv_at = w.kv_at;
     const int shift = kv_tokens - q_tokens;
     const int k0 = kb * BK + wave / DS * 32;              // the wave's first key
     const int key = k0 + n;                               // this lane's
@@ -426,7 +453,7 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                if constexpr (D == 256)
+                if constexpr (kApart)
                     __builtin_amdgcn_sched_barrier(0);
                 const u32x4 pf = pack_b<F16>(s, k), sf = pack_b<F16>(dp, k);
                 u32x4 p_rest, s_rest;
@@ -455,9 +482,10 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
     }
 
     // the lane's place again: kept over the loop it would take registers that
-    // head_dim 256 does not have (nor, below, for more than one block at a time)
+    // packed sequences and head_dim 256 do not have (nor it, below, for more than one
+    // block at a time)
     int lane_now = lane;
-    if constexpr (D == 256) {
+    if constexpr (D == 256 || PACKED) {
         lane_now = threadIdx.x % 64;
         __asm__ volatile("" : "+v"(lane_now));
     }
@@ -492,39 +520,23 @@ __device__ __forceinline__ void key_gradients(const BwdParams& p, const char* ld
 // ---------------------------------------------------------------- dq
 
 template <int D, bool F16, bool CAUSAL, bool TWO, bool PACKED>
-__device__ __forceinline__ void query_gradients(const BwdParams& p, const char* lds, float* tops,
-                                                uint32_t bid)
+__device__ __forceinline__ void query_gradients(const BwdParams& p, const Work& w, const char* lds, float* tops)
 {
     constexpr int NW = kWaves, BN = kTileRows;
     constexpr int BM = NW * 32, KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
-    const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
+    int lane = threadIdx.x % 64;
+    if constexpr (PACKED)         // as in key_gradients
+        __asm__ volatile("" : "+v"(lane));
+    const int n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    const BlockOf<> block(bid, p.pairs, p.row_blocks * p.key_splits);
-    const int mb_raw = block.part % p.row_blocks, split = block.part / p.row_blocks;
-    const uint32_t bh = block.pair;
-    const int64_t b = bh / (uint32_t)p.kv_heads;
-    const int hk = bh % (uint32_t)p.kv_heads;
-    int mb = CAUSAL ? p.row_blocks - 1 - mb_raw : mb_raw;
-    int len = p.kv_tokens, seq = 0, rows = p.rows;
-    int q_tokens = p.q_tokens, kv_tokens = p.kv_tokens;
-    int64_t q_at = 0, kv_at = 0;           // the sequence's first rows
-    if constexpr (PACKED) {
-        const PackedBlock<BM> of(p, p.q_rows, p.group, mb_raw);
-        seq = of.seq;
-        q_tokens = of.q_tokens;
-        rows = q_tokens * p.group;
-        if (!of.there(p, rows))
-            return;
-        mb = CAUSAL ? (rows + BM - 1) / BM - 1 - of.at : of.at;
-        kv_tokens = len = p.q_rows.rest(seq) ? 0 : of.kv_tokens;
-        q_at = of.q_at;
-        kv_at = of.kv_at;
-    } else if (p.kv_lengths) {
-        const int given = __builtin_amdgcn_readfirstlane(p.kv_lengths[b]);
-        len = given < 0 ? 0 : given < len ? given : len;
-    }
+    const uint32_t bh = w.bh;
+    const int64_t b = PACKED ? 0 : bh / (uint32_t)p.kv_heads;
+    const int hk = PACKED ? bh : bh % (uint32_t)p.kv_heads;
+    const int split = w.split, mb = w.block, seq = w.seq;
+    const int q_tokens = w.q_tokens, kv_tokens = w.kv_tokens, rows = w.rows, len = w.len;
+    const int64_t q_at = w.q_at, kv_at = w.kv_at;
     const int r0 = mb * BM + wave * 32;
     const int r = r0 + n < rows ? r0 + n : rows - 1;
     const int qi = r / p.group, head = hk * p.group + r % p.group;
@@ -678,6 +690,25 @@ constexpr int backward_waves(int d, bool f16, bool two)
     return d == 256 || (d == 128 && f16 && two) ? 1 : 2;
 }
 
+// A workgroup's key block.  Causal: the first key blocks are seen by most queries;
+// turning the order from split to split keeps them from meeting on the same CUs.
+template <bool CAUSAL>
+__device__ __forceinline__ Work key_work(const BwdParams& p, uint32_t bid)
+{
+    const BlockOf<> block(bid, p.pairs, p.key_blocks * p.row_splits);
+    const int split = block.part / p.key_blocks;
+    return Work(p, block.pair, split, (block.part + (CAUSAL ? split : 0)) % p.key_blocks);
+}
+
+// A workgroup's row block: causal, the longest first.
+template <bool CAUSAL>
+__device__ __forceinline__ Work query_work(const BwdParams& p, uint32_t bid, bool packed)
+{
+    const BlockOf<> block(bid, p.pairs, p.row_blocks * p.key_splits);
+    const int mb = block.part % p.row_blocks;
+    return Work(p, block.pair, block.part / p.row_blocks, CAUSAL && !packed ? p.row_blocks - 1 - mb : mb);
+}
+
 template <int D, bool F16, bool CAUSAL, bool TWO>
 __global__ __launch_bounds__(kWaves * 64, backward_waves(D, F16, TWO))
 void attention_backward_kernel(const BwdParams p)
@@ -688,15 +719,22 @@ void attention_backward_kernel(const BwdParams p)
     __shared__ float tops[8];
     const uint32_t first = p.pairs * (uint32_t)(p.key_blocks * p.row_splits);
     if (blockIdx.x < first) {
+        Work w = key_work<CAUSAL>(p, blockIdx.x);
+        w.in_sample(p);
         if (D == 256 && p.column_waves == 2)
-            key_gradients<D, F16, CAUSAL, TWO, D == 256 ? 2 : 1, false>(p, lds, tops, blockIdx.x);
+            key_gradients<D, F16, CAUSAL, TWO, D == 256 ? 2 : 1, false>(p, w, lds, tops);
         else
-            key_gradients<D, F16, CAUSAL, TWO, 1, false>(p, lds, tops, blockIdx.x);
-    } else
-        query_gradients<D, F16, CAUSAL, TWO, false>(p, lds, tops, blockIdx.x - first);
+            key_gradients<D, F16, CAUSAL, TWO, 1, false>(p, w, lds, tops);
+    } else {
+        Work w = query_work<CAUSAL>(p, blockIdx.x - first, false);
+        w.in_sample(p);
+        query_gradients<D, F16, CAUSAL, TWO, false>(p, w, lds, tops);
+    }
 }
 
-// The same of packed sequences, with one term of p and ds and whole blocks of keys.
+// The same of packed sequences, with whole blocks of keys.  Each sequence's own rows
+// say how many terms p and ds have, whatever the others are, so both forms are in the
+// kernel.
 template <int D, bool F16, bool CAUSAL>
 __global__ __launch_bounds__(kWaves * 64, backward_waves(D, F16, false))
 void packed_backward_kernel(const BwdParams p)
@@ -705,10 +743,35 @@ void packed_backward_kernel(const BwdParams p)
     __shared__ __attribute__((aligned(kTiles))) char lds[kTiles + 2 * kTileRows * 8];
     __shared__ float tops[8];
     const uint32_t first = p.pairs * (uint32_t)(p.key_blocks * p.row_splits);
-    if (blockIdx.x < first)
-        key_gradients<D, F16, CAUSAL, false, 1, true>(p, lds, tops, blockIdx.x);
-    else
-        query_gradients<D, F16, CAUSAL, false, true>(p, lds, tops, blockIdx.x - first);
+    if (blockIdx.x < first) {
+        Work w = key_work<CAUSAL>(p, blockIdx.x);
+        const PackedBlock<kWaves * 32> of(p, p.kv_rows, 1, w.block);
+        if (!of.there(p, of.kv_tokens))
+            return;
+        w.in_sequence(p, of);
+        if (p.q_rows.rest(w.seq))
+            w.q_tokens = w.rows = 0;
+        if (w.q_tokens == 0)
+            w.len = 0;
+        if (w.rows <= kTwoTermRows)
+            key_gradients<D, F16, CAUSAL, true, 1, true>(p, w, lds, tops);
+        else
+            key_gradients<D, F16, CAUSAL, false, 1, true>(p, w, lds, tops);
+    } else {
+        Work w = query_work<CAUSAL>(p, blockIdx.x - first, true);
+        const PackedBlock<kWaves * 32> of(p, p.q_rows, p.group, w.block);
+        if (!of.there(p, of.q_tokens * p.group))
+            return;
+        w.in_sequence(p, of);
+        if (p.q_rows.rest(w.seq))
+            w.kv_tokens = 0;
+        if (CAUSAL)
+            w.block = (w.rows + kWaves * 32 - 1) / (kWaves * 32) - 1 - w.block;
+        if (w.rows <= kTwoTermRows)
+            query_gradients<D, F16, CAUSAL, true, true>(p, w, lds, tops);
+        else
+            query_gradients<D, F16, CAUSAL, false, true>(p, w, lds, tops);
+    }
 }
 
 // Rows that have parts to add, and the workgroups that add them.
@@ -849,9 +912,9 @@ hipError_t launch(BwdParams p, hipStream_t st)
                                   argv, 0, st);
     };
     go(row_stats_kernel<D, F16, PACKED>, p.batch * p.heads * p.stat_blocks + (F16 ? pairs * p.value_blocks : 0));
-    go(PACKED                ? packed_backward_kernel<D, F16, CAUSAL>
+    go(PACKED                   ? packed_backward_kernel<D, F16, CAUSAL>
        : p.rows <= kTwoTermRows ? attention_backward_kernel<D, F16, CAUSAL, true>
-                            : attention_backward_kernel<D, F16, CAUSAL, false>,
+                                : attention_backward_kernel<D, F16, CAUSAL, false>,
        pairs * ((int64_t)p.key_blocks * p.row_splits + (int64_t)p.row_blocks * p.key_splits));
     go(attention_sum_kernel<D, F16, PACKED>, sum_blocks<D, true>(p) + sum_blocks<D, false>(p));
     return err;

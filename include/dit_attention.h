@@ -128,7 +128,7 @@ int dit_attention_backward(const dit_attn_args* args, const dit_attn_tensor* dou
  * behind the last are left as they are in every output, or, with fill_rest, get
  * out = 0, lse = -inf and zero gradients.  Rows of no sequence are not read.
  *
- * Forward, each sequence's own query rows a key head say whether p has a second
+ * Each sequence's own query rows a key head say whether p and ds have a second
  * operand (up to 32), as in a call of its own.  The order of a sequence's sums (tiles,
  * splits of the keys) follows from the sizes of the call, so the last bit of a result
  * may differ from that of a call of its own.

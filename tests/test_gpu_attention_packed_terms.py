@@ -52,6 +52,19 @@ def test_forward(lengths, kv, causal, d, heads, kv_heads, dtype):
         assert bool(((s - r["lse"][0]).abs()[some] <= r["lse_bound"][0][some]).all()), (rows, keys)
 
 
+@pytest.mark.parametrize("lengths,kv", LENGTHS)
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,heads,kv_heads,dtype", KINDS)
+def test_backward(lengths, kv, causal, d, heads, kv_heads, dtype):
+    t, kw, out, lse = call(lengths, kv, causal, d, heads, kv_heads, dtype)
+    grads = dict(zip(("dq", "dk", "dv"), qkr.attention_packed_backward(
+        t["dout"], t["q"], t["k"], t["v"], out, lse, offsets_of(lengths, 2), **kw)))
+    for rows, keys, r in each(t, lengths, kv, causal):
+        for n, (want, bound) in ref.backward(r, t["dout"][rows][None], out[rows][None], out.dtype).items():
+            got = grads[n][rows if n == "dq" else keys].double().permute(1, 0, 2)
+            assert bool(((got - want[0]).abs() <= bound[0]).all()), (n, rows, keys)
+
+
 def test_the_bounds_tell_the_terms_apart():
     """One term of p does not meet the bound of a short sequence (by the oracle, on the CPU)."""
     g = torch.Generator().manual_seed(32)
