@@ -99,9 +99,9 @@ __device__ __forceinline__ void row_norm(const u32x4 (&x)[VPT], const RmsParams&
     ss = v[0];
 }
 
-// The binary exponent of the row's largest |x|.
+// The row's largest |x|.
 template <int TPR, int VPT, bool F16>
-__device__ __forceinline__ int row_exponent(const u32x4 (&x)[VPT], float* slot)
+__device__ __forceinline__ float row_largest(const u32x4 (&x)[VPT], float* slot)
 {
     float m = 0.0f;
 #pragma unroll
@@ -112,7 +112,71 @@ __device__ __forceinline__ int row_exponent(const u32x4 (&x)[VPT], float* slot)
         for (int k = 0; k < 8; ++k)
             m = fmaxf(m, fabsf(f[k]));
     }
-    return __builtin_amdgcn_frexp_expf(row_max<TPR>(m, slot));
+    return row_max<TPR>(m, slot);
+}
+
+__device__ __forceinline__ uint64_t fp8x8(const float (&o)[8])
+{
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[0], o[1], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[2], o[3], lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[4], o[5], 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[6], o[7], hi, true);
+    return (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo;
+}
+
+// s weight 2^-e: the product's mantissa is rounded as any product's is, whatever its
+// exponent.
+__device__ __forceinline__ float product(float s, float weight, int e)
+{
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_frexp_mantf(s) * __builtin_amdgcn_frexp_mantf(weight),
+                                   __builtin_amdgcn_frexp_expf(s) + __builtin_amdgcn_frexp_expf(weight) - e);
+}
+
+// A row to 8 bits whose largest |s weight| is too small for the products, or for 448
+// over it: the values by product(), with the exponent of the largest.  s is read
+// again, a vector at a time: held in registers it would cost the other rows theirs.
+// rstd is of s 2^-shift.
+template <int TPR, bool F16>
+__device__ __forceinline__ void small_to_8_bits(const RmsParams& p, const uint16_t* s, uint8_t* out, float* scale, int t,
+                                             float rstd, int shift, float* slot)
+{
+    const int nvec = p.hidden / kVec;
+    constexpr float kNone = -100000.0f;
+    float most = kNone, f[8], w[8];
+#pragma unroll 1
+    for (int i = t; i < nvec; i += TPR) {
+        unpack8<F16>(load16<false>(s + i * kVec), f);
+        load_weight(p, i, true, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (f[k] != 0.0f && w[k] != 0.0f)
+                most = fmaxf(most, (float)(__builtin_amdgcn_frexp_expf(f[k]) + __builtin_amdgcn_frexp_expf(w[k])));
+    }
+    most = row_max<TPR>(most, slot);
+    const int e = most == kNone ? 0 : (int)most;
+    float top = 0.0f;
+#pragma unroll 1
+    for (int i = t; i < nvec; i += TPR) {
+        unpack8<F16>(load16<false>(s + i * kVec), f);
+        load_weight(p, i, true, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            top = fmaxf(top, fabsf(product(f[k], w[k], e)));
+    }
+    top = row_max<TPR>(top, slot);
+    const float by = top > 0.0f ? kFp8Max / top : kFp8Max;
+    if (t == 0)
+        *scale = __builtin_amdgcn_ldexpf(__builtin_amdgcn_frexp_mantf(rstd) / by,
+                                         __builtin_amdgcn_frexp_expf(rstd) + e - shift);
+#pragma unroll 1
+    for (int i = t; i < nvec; i += TPR) {
+        unpack8<F16>(load16<false>(s + i * kVec), f);
+        load_weight(p, i, true, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            f[k] = product(f[k], w[k], e) * by;
+        *reinterpret_cast<uint64_t*>(out + i * kVec) = fp8x8(f);
+    }
 }
 
 template <int TPR, int VPT, bool F16, bool RES, bool FP8>
@@ -161,21 +225,28 @@ void rms_norm_kernel(const RmsParams p)
     float rstd = ss / (float)p.hidden + p.eps;
     // the same branch in every thread of the row
     if (__builtin_expect(rstd <= kMax && (ss >= kTinySum || p.eps >= kTinySum) &&
-                             (!FP8 || top == 0.0f || (top >= kTinySum && top <= kMax)), 1)) {
+                             (!FP8 || (top >= kTinySum && top <= kMax)), 1)) {
         rstd = __builtin_amdgcn_rsqf(rstd);
+    } else if (const float most = row_largest<TPR, VPT, F16>(x, slot + (RPW == 1 ? 16 : 0)); most == 0.0f) {
+        rstd = rsqrt_full_range(ss / (float)p.hidden + p.eps);        // nothing but zeros, or NaN
     } else {
-        shift = row_exponent<TPR, VPT, F16>(x, slot + (RPW == 1 ? 16 : 0));
+        shift = __builtin_amdgcn_frexp_expf(most);
         row_norm<TPR, VPT, F16, FP8, true>(x, p, t, nvec, shift, slot + (RPW == 1 ? 8 : 0), ss, top);
         const float eps = __builtin_amdgcn_ldexpf(p.eps, -2 * shift);
         // eps may be above x^2 by more than 2^128
         rstd = eps <= kMax ? rsqrt_full_range(ss / (float)p.hidden + eps)
                            : __builtin_amdgcn_ldexpf(rsqrt_full_range(p.eps), shift);
+        if constexpr (FP8) {
+            if (top < kTinySum && rstd > 0.0f) {
+                small_to_8_bits<TPR, F16>(p, (RES ? p.sum : p.x) + row, static_cast<uint8_t*>(p.out) + row,
+                                          p.scales + r, t, rstd, shift, slot + (RPW == 1 ? 16 : 0));
+                return;
+            }
+        }
     }
     float f = 0.0f;
     if constexpr (FP8) {
-        f = kFp8Max;
-        if (top > 0.0f)           // of weights below 2^-100 not all 448 steps are used
-            f = top >= kTinySum ? kFp8Max / top : 0x1p100f;
+        f = top > 0.0f ? kFp8Max / top : kFp8Max;
         if (t == 0)
             p.scales[r] = rstd / f;
     }
@@ -191,16 +262,10 @@ void rms_norm_kernel(const RmsParams p)
                 const float a = shift ? scaled(e[k], shift) : e[k];
                 o[k] = FP8 ? a * w[k] * f : a * rstd * w[k];
             }
-            if constexpr (FP8) {
-                int lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[0], o[1], 0, false);
-                lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[2], o[3], lo, true);
-                int hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[4], o[5], 0, false);
-                hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[6], o[7], hi, true);
-                *reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(p.out) + row + i * kVec) =
-                    (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo;
-            } else {
+            if constexpr (FP8)
+                *reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(p.out) + row + i * kVec) = fp8x8(o);
+            else
                 store16<true>(static_cast<uint16_t*>(p.out) + row + i * kVec, pack8<F16>(o));
-            }
         }
     }
 }
@@ -255,7 +320,7 @@ __device__ __forceinline__ RowStats row_stats(const u32x4 (&x)[VPT], const u32x4
         s.rstd = s.rstd_x = __builtin_amdgcn_rsqf(s.rstd);
         return s;
     }
-    s.shift = row_exponent<TPR, VPT, F16>(x, spare);
+    s.shift = __builtin_amdgcn_frexp_expf(row_largest<TPR, VPT, F16>(x, spare));
     grad_sums<TPR, VPT, F16, true>(x, dy, w, s.shift, spare + 4, v);
     s.gn = v[1];
     const float eps_s = __builtin_amdgcn_ldexpf(eps, -2 * s.shift);

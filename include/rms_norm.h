@@ -23,8 +23,8 @@
  * Math is fp32; s, y and dx are rounded once, to nearest even; dweight is an
  * fp32 sum in an order that depends on the sizes alone, so results do not
  * change from run to run.  Rows of any finite values are normalised correctly
- * (where the plain sums leave fp32's range they are taken again of x * 2^-e)
- * and get their gradients, as long as the products dy * weight stay in fp32's
+ * (where the plain sums leave fp32's range they are taken again of x * 2^-e, and
+ * products t below it of their mantissas) and get their gradients, as long as the products dy * weight stay in fp32's
  * range.  A row that holds a NaN comes out as NaN; with an infinity, finite
  * elements come out as 0 and infinite ones as NaN, and in 8 bits the scale is
  * NaN either way.
