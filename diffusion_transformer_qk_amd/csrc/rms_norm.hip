@@ -248,7 +248,7 @@ void rms_norm_kernel(const RmsParams p)
     if constexpr (FP8) {
         f = top > 0.0f ? kFp8Max / top : kFp8Max;
         if (t == 0)
-            p.scales[r] = rstd / f;
+            p.scales[r] = rstd > 0.0f ? rstd / f : NAN;       // 0: an infinity, whose products may all be NaN
     }
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {

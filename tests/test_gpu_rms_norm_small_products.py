@@ -93,3 +93,15 @@ def test_rows_of_nan_alone():
         assert bool(torch.isnan(scales[1])) and bool(torch.isfinite(scales[::2]).all())
         assert bool((q[::2].float() == 0).all())
         assert bool(torch.isnan(qkr.rms_norm(x)[1]).all())
+
+
+@pytest.mark.parametrize("hidden", HIDDEN)
+def test_scales_of_infinite_rows(hidden):
+    """NaN, whatever weight an infinity meets: 0 makes its product NaN, which no maximum sees."""
+    x = torch.ones((4, hidden), dtype=torch.bfloat16, device=DEV)
+    x[1, 3], x[2, 3] = math.inf, -math.inf
+    for value in (0.0, -0.0, 1e-38, 1.0, math.nan):
+        w = torch.ones(hidden, device=DEV)
+        w[3] = value
+        scales = qkr.rms_norm_fp8(x, w)[1]
+        assert bool(torch.isnan(scales[1:3]).all()) and bool(torch.isfinite(scales[::3]).all())
