@@ -734,8 +734,9 @@ def attention_packed(q, k, v, offsets, *, kv_offsets=None, causal: bool = False,
     and of k and v unless ``kv_offsets`` (like it) says which.  Each attends to
     its own keys as a sample of ``attention`` does; ``causal``: its last query
     sees its last key.  Rows of no sequence, before the first or behind the
-    last, are neither read nor written; where ``out`` and ``lse`` (float32
-    [heads, tokens]) are both made here, they hold 0 and -inf there.
+    last, count for nothing, whatever they hold, and are left as they are in
+    ``out`` and ``lse`` (float32 [heads, tokens]); where both are made here, they
+    hold 0 and -inf there.
     ``workspace``: at least ``attention_packed_workspace_size`` bytes, allocated
     here on the launch stream when None and one is needed.
     """

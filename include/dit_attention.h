@@ -126,7 +126,8 @@ int dit_attention_backward(const dit_attn_args* args, const dit_attn_tensor* dou
  * clamped to 0 .. the buffer's rows, so none leads out of a buffer, but with
  * decreasing ones the results are undefined.  Rows before the first sequence and
  * behind the last are left as they are in every output, or, with fill_rest, get
- * out = 0, lse = -inf and zero gradients.  Rows of no sequence are not read.
+ * out = 0, lse = -inf and zero gradients.  What rows of no sequence hold changes
+ * nothing (with fill_rest those of q and dout are loaded; the others are not read).
  *
  * Each sequence's own query rows a key head say whether p and ds have a second
  * operand (up to 32), as in a call of its own.  The order of a sequence's sums (tiles,
