@@ -541,6 +541,12 @@ def _attn_tensor(t, name: str) -> AttnTensor:
     return AttnTensor(t.data_ptr(), strides[0], strides[1], strides[2])
 
 
+def _attn_scale(head_dim: int, scale) -> float:
+    if scale is not None:
+        return scale
+    return head_dim ** -0.5 if head_dim else 1.0       # (no head_dim: the library refuses the call)
+
+
 def _attn_args(q, k, v, causal, kv_lengths, scale) -> AttnArgs:
     torch = _torch()
     shape, kv_shape = q.shape, k.shape
@@ -560,7 +566,7 @@ def _attn_args(q, k, v, causal, kv_lengths, scale) -> AttnArgs:
     if kv_lengths is not None and (kv_lengths.dtype != torch.int32 or kv_lengths.shape != (batch,)):
         raise ValueError("kv_lengths must be int32 [batch]")
     return AttnArgs(batch, q_tokens, kv_shape[1], heads, kv_heads, head_dim, 1 if causal else 0,
-                    _x_code(q, "q/k/v"), head_dim ** -0.5 if scale is None else scale,
+                    _x_code(q, "q/k/v"), _attn_scale(head_dim, scale),
                     None if kv_lengths is None else _ptr(kv_lengths))
 
 
@@ -705,7 +711,7 @@ def _packed_args(q, k, v, offsets, kv_offsets, causal, scale, fill) -> AttnPacke
         raise ValueError("kv_offsets must be int32 [sequences + 1], as offsets are")
     return AttnPackedArgs(offsets.numel() - 1, q_tokens, k.shape[0], heads, kv_heads, head_dim,
                           1 if causal else 0, _x_code(q, "q/k/v"),
-                          head_dim ** -0.5 if scale is None else scale, 1 if fill else 0, _ptr(offsets),
+                          _attn_scale(head_dim, scale), 1 if fill else 0, _ptr(offsets),
                           None if kv_offsets is None else _ptr(kv_offsets))
 
 
