@@ -78,11 +78,14 @@ __device__ __forceinline__ void forward_rows(const FwdParams& p, const Work& w, 
 {
     constexpr int BM = NW * 32, BN = tile_keys(D, NW), KB = BN / 32, DB = D / 32;
     constexpr int kTile = BN * D * 2;
-    const int lane = threadIdx.x % 64, n = lane & 31, g = lane >> 5;
+    int lane = threadIdx.x % 64;
+    if constexpr (PACKED)  // nothing that follows from it is shared, and held, with the other form
+        __asm__ volatile("" : "+v"(lane));
+    const int n = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t bh = w.bh;
-    const int64_t b = bh / (uint32_t)p.kv_heads;
-    const int hk = bh % (uint32_t)p.kv_heads;
+    const int64_t b = PACKED ? 0 : bh / (uint32_t)p.kv_heads;
+    const int hk = PACKED ? bh : bh % (uint32_t)p.kv_heads;
     const int split = w.split, mb = w.mb;
     const int q_tokens = w.q_tokens, kv_tokens = w.kv_tokens, rows = w.rows, len = w.len;
     const int64_t q_at = w.q_at, kv_at = w.kv_at;
