@@ -280,7 +280,7 @@ struct Work {
 // cycles, the LDS reads, one fragment a product, and the vector ALU a third each.
 // The four products run at 1141 TFLOP/s on 32760 tokens of 5 heads of 128 and at
 // 1094 on 4608 of 48, launched alone; a large library product, under the same
-// power, reaches 1215 on that card.  Tiles of 64 queries measured 6% faster than
+// power, reaches 1180 to 1600 by how its operands lie.  Tiles of 64 queries measured 6% faster than
 // tiles of 32, and keeping the phases of a block apart 3% more: left to itself
 // the scheduler mixes two blocks and has to spill.
 //

@@ -133,7 +133,7 @@ __device__ __forceinline__ void finish(const FwdParams& p, P& c, int64_t r0, int
 
 // Tiles of kRowsB rows of x and kRowsA / 2 columns of h.  Bound by the matrix cores at
 // the clock that the card's power leaves: 32760 rows of 5120, 13824 columns, gate and
-// up kept, 6.86 ms (1350 TFLOP/s; the library's product of these sizes alone 6.72), and
+// up kept, 6.80 ms (1360 TFLOP/s; the library's product of these sizes alone 6.72), and
 // 4608 rows of 6144 and 16384 columns in 8 bits 0.69 (2690; 0.62).
 template <int T, bool F16, int ACT, int NA, int NB, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB, 2)
@@ -164,8 +164,8 @@ void gated_feed_forward_kernel(const FwdParams p)
 
 // Up to 32 rows of x: the call waits for the weights.  A workgroup takes 32 columns
 // of h, its waves a share of k each, through slots of their own (no barriers), and
-// the first wave adds their sums in order.  One row of 5120 and 13824 columns: 44.6 us,
-// 283 MB of weights at 6.3 TB/s.  Calls of it and of 128 x 128 tiles: one row 53 and 58
+// the first wave adds their sums in order.  One row of 5120 and 13824 columns: 44.0 us,
+// 283 MB of weights at 6.4 TB/s.  Calls of it and of 128 x 128 tiles: one row 53 and 58
 // us, 32 rows 59 and 58; of 1536 and 4096 columns 9.5 and 14.3 us, one row as 32.
 constexpr int kFewRows = 32, kFewColumns = 32, kFewWaves = 2;
 

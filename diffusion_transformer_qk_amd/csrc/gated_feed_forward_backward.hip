@@ -7,7 +7,7 @@
 //   dx = dgate W_gate + dup W_up: one sum over 2 * inner, the weights read down
 //        their rows by transposed reads of LDS;
 //   dw = dgate^T x and dup^T x: sums over the rows, both operands read down.
-// 4608 rows of 6144 and 16384 columns: 122 us, 1.54 ms (1204 TFLOP/s) and 1.44 (1285;
+// 4608 rows of 6144 and 16384 columns: 122 us, 1.53 ms (1215 TFLOP/s) and 1.40 (1326;
 // the library's products 2.05 and 1.61).  The first pass moves 755 MB at 6.2 TB/s.
 //
 // Kept gate and up cost 4 bytes an element and a pass; computing them again would

@@ -30,8 +30,9 @@
  * are kept.  dgate and dup are rounded to the tensors' type before the products
  * that use them (as the sums of 16-bit numbers that they enter would be off by
  * as much); for fp16 they are first scaled by a power of two, by the largest of
- * them, so that small gradients do not sink into fp16's subnormals.  Results do
- * not depend on the order in which workgroups run (no atomic additions).
+ * them, so that small gradients do not sink into fp16's subnormals (one power for
+ * the call: what lies below 2^-28 of the largest is off by up to 2^-39 of it).
+ * Results do not depend on the order in which workgroups run (no atomic additions).
  *
  * All pointers are DEVICE pointers owned by the caller.  The library
  * allocates, frees and synchronises nothing and keeps no state between calls.
