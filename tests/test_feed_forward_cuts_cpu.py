@@ -8,7 +8,7 @@ import subprocess
 
 import pytest
 
-from tests.test_gpu_feed_forward_rounds import BACKWARD, FORWARD
+from tests.test_gpu_feed_forward_large_tiles import BACKWARD, FORWARD
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
