@@ -1275,7 +1275,8 @@ def gated_feed_forward_backward(dh, x, w_gate, w_up, gate, up, *, activation: st
     dtype, written (not added to), and default to new tensors; dx is None
     without ``input_grad``, the other two are without ``weight_grads``.
     ``workspace``: at least ``gated_feed_forward_backward_workspace_size`` bytes
-    (4 bytes an element of dh); allocated here on the launch stream when None.
+    (4 bytes an element of dh, more for few rows); allocated here on the launch
+    stream when None.
     """
     torch = _torch()
     lib = load_library()

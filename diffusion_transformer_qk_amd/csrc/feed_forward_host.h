@@ -61,6 +61,19 @@ inline int check_buffers(const Buffer* in, int ins, const Buffer* out, int outs)
     return QKR_OK;
 }
 
+// The 16-bit terms of dgate and dup in the products that use them.  With one, a gradient
+// is off by 1.41 times its own rounding in the mean, but by up to 1.84 where few numbers
+// are rounded (600 calls of 1 to 20000 rows: above 1.5 with up to 25 rows, or with up
+// to 22000 numbers); with two by its own rounding alone.  Two cost calls of few rows
+// little, as the weights' way bounds them (x of 5120, W of 13824: one row 168 and 171 us,
+// 32 rows 173 and 180; 128 rows 198 and 255), and small ones a launch (32 rows of 96, 264
+// columns: 18.6 and 21.9; 64 of 8192, 512: 26.0 and 31.9).
+inline int terms_of(const dit_ff_args& a)
+{
+    const int64_t small = (int64_t)1 << 15;
+    return a.rows <= 32 || (a.rows * a.inner <= small && a.rows * a.hidden <= 32 * small) ? 2 : 1;
+}
+
 // How a product of rows x columns outputs and `stages` stages of k is cut: tiles of
 // 256 x 256 (a workgroup a CU) or of 128 x 128 (two a CU), and k into splits whose
 // sums are added by a launch of their own.  The cheapest by what a stage of a round

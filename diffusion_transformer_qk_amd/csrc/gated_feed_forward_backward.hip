@@ -10,6 +10,9 @@
 // 4608 rows of 6144 and 16384 columns: 122 us, 1.53 ms (1215 TFLOP/s) and 1.40 (1326;
 // the library's products 2.05 and 1.61).  The first pass moves 755 MB at 6.2 TB/s.
 //
+// Calls of few rows or numbers (terms_of) round dgate and dup in two terms: the
+// remainders are rows beside theirs, so that the weights are read once for both.
+//
 // Kept gate and up cost 4 bytes an element and a pass; computing them again would
 // cost half as many products as the two above.
 //
@@ -31,14 +34,17 @@ using namespace qkr_ff;
 struct BwdParams {
     const uint16_t *dh, *x, *w_gate, *w_up, *gate, *up;
     uint16_t *dx, *dw_gate, *dw_up;
-    uint16_t* d;              // [2][rows][inner]: dgate and dup
+    uint16_t* d;              // [2][terms][rows][inner]: dgate and dup, each with what its rounding left, if terms is 2
+    int32_t terms;
+    uint16_t* x_twice;        // [2][rows][hidden]: x beside itself for the terms' rows in dw, or NULL
     float* largest;           // fp16: [largest_blocks] largest finite |dgate|, |dup|
     uint32_t largest_blocks;
     int64_t rows;
     int32_t hidden, inner;
     uint32_t row_tiles, column_tiles;   // of the grid
     int32_t splits;           // of k
-    float* parts;             // [splits][rows][hidden] of dx, or [splits][2 inner][hidden] of dw, when splits > 1
+    float* parts;             // [splits][terms][rows][hidden] of dx, or [splits][2 inner][hidden] of dw, or NULL where
+                              // the products themselves store dx or dw
 };
 
 constexpr int kThreads = 256;
@@ -94,6 +100,18 @@ void feed_forward_largest_kernel(const BwdParams p)
         p.largest[blockIdx.x] = top;
 }
 
+// What rounding v to `rounded` left (nothing of an infinity or NaN).
+template <bool F16>
+__device__ __forceinline__ u32x4 rest8(const float (&v)[8], u32x4 rounded)
+{
+    float r[8];
+    unpack8<F16>(rounded, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        r[k] = fabsf(r[k]) <= 0x1.fffffep127f ? v[k] - r[k] : 0.0f;
+    return pack8<F16>(r);
+}
+
 template <bool F16, int ACT>
 __global__ __launch_bounds__(kThreads)
 void feed_forward_gradients_kernel(const BwdParams p)
@@ -114,8 +132,23 @@ void feed_forward_gradients_kernel(const BwdParams p)
                 b[k] = __builtin_amdgcn_ldexpf(b[k], -e);
             }
         }
-        store16<false>(p.d + i, pack8<F16>(a));
-        store16<false>(p.d + n + i, pack8<F16>(b));
+        const u32x4 da = pack8<F16>(a), db = pack8<F16>(b);
+        uint16_t* up = p.d + p.terms * n;
+        store16<false>(p.d + i, da);
+        store16<false>(up + i, db);
+        if (p.terms == 2) {
+            store16<false>(p.d + n + i, rest8<F16>(a, da));
+            store16<false>(up + n + i, rest8<F16>(b, db));
+        }
+    }
+    if (!p.x_twice)
+        return;
+    const int64_t of_x = p.rows * p.hidden;
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kVec; i < of_x;
+         i += (int64_t)gridDim.x * kThreads * kVec) {
+        const u32x4 x = load16<false>(p.x + i);
+        store16<false>(p.x_twice + i, x);
+        store16<false>(p.x_twice + of_x + i, x);
     }
 }
 
@@ -151,7 +184,8 @@ __device__ __forceinline__ void store(P& c, uint16_t* out, float* part, int64_t 
     });
 }
 
-// Tiles of kRowsB rows and kRowsA columns of dx.
+// Tiles of kRowsB rows and kRowsA columns of dx, whose terms are rows beside each other
+// here: the weights are read once for both, and the parts are added by the join.
 template <bool F16, int N>
 __global__ __launch_bounds__(128 * N, 2)
 void feed_forward_dx_kernel(const BwdParams p)
@@ -163,7 +197,7 @@ void feed_forward_dx_kernel(const BwdParams p)
     const uint32_t tiles = p.row_tiles * p.column_tiles;
     const TileOf tile(blockIdx.x % tiles, p.row_tiles, p.column_tiles, 4);
     const int split = blockIdx.x / tiles;
-    const int64_t r0 = (int64_t)tile.row * P::kRowsB, rows_left = p.rows - r0;
+    const int64_t all_rows = p.terms * p.rows, r0 = (int64_t)tile.row * P::kRowsB, rows_left = all_rows - r0;
     const int h0 = tile.column * P::kRowsA;
     const int rows = rows_left < P::kRowsB ? (int)rows_left : P::kRowsB;
     const int columns = p.hidden - h0 < P::kRowsA ? p.hidden - h0 : P::kRowsA;
@@ -181,7 +215,7 @@ void feed_forward_dx_kernel(const BwdParams p)
         const int k0 = low * kStageRows, k = (high * kStageRows < p.inner ? high * kStageRows : p.inner) - k0;
         const Matrix w = {reinterpret_cast<const char*>((half ? p.w_up : p.w_gate) + (int64_t)k0 * p.hidden + h0),
                           (int64_t)p.hidden * 2, columns};
-        const Matrix d = {reinterpret_cast<const char*>(p.d + (half * p.rows + r0) * p.inner + k0),
+        const Matrix d = {reinterpret_cast<const char*>(p.d + (half * all_rows + r0) * p.inner + k0),
                           (int64_t)p.inner * 2, rows};
         typename P::LoadA la(w, wave * P::kLoadsA, k, lane);
         typename P::LoadB lb(d, wave * P::kLoadsB, (int64_t)k * 2, lane);
@@ -190,12 +224,13 @@ void feed_forward_dx_kernel(const BwdParams p)
     int e = 0;
     if constexpr (F16)
         e = stored_exponent<64 * P::kWaves>(p, reinterpret_cast<float*>(lds));
-    store<F16>(c, p.dx, p.splits > 1 ? p.parts + split * p.rows * p.hidden : nullptr, r0 + 32 * P::first_b(wave),
-               p.rows, h0 + 32 * P::first_a(wave), p.hidden, e, lane);
+    store<F16>(c, p.dx, p.parts ? p.parts + split * all_rows * p.hidden : nullptr, r0 + 32 * P::first_b(wave),
+               all_rows, h0 + 32 * P::first_a(wave), p.hidden, e, lane);
 }
 
 // Tiles of kRowsB rows (of one weight) and kRowsA columns of dw_gate and dw_up;
-// the first half of the rows of tiles is dw_gate's.
+// the first half of the rows of tiles is dw_gate's.  The sum runs over the rows of all
+// terms.
 template <bool F16, int N>
 __global__ __launch_bounds__(128 * N, 2)
 void feed_forward_dw_kernel(const BwdParams p)
@@ -211,14 +246,16 @@ void feed_forward_dw_kernel(const BwdParams p)
     const int i0 = (tile.row - of_up * per_weight) * P::kRowsB, h0 = tile.column * P::kRowsA;
     const int rows = p.inner - i0 < P::kRowsB ? p.inner - i0 : P::kRowsB;
     const int columns = p.hidden - h0 < P::kRowsA ? p.hidden - h0 : P::kRowsA;
-    const int64_t stages = (p.rows + kStageRows - 1) / kStageRows, each = (stages + p.splits - 1) / p.splits;
+    const int64_t all_rows = p.terms * p.rows;
+    const int64_t stages = (all_rows + kStageRows - 1) / kStageRows, each = (stages + p.splits - 1) / p.splits;
     const int64_t low = split * each, high = low + each < stages ? low + each : stages;
-    const int64_t k0 = low * kStageRows, k = (high * kStageRows < p.rows ? high * kStageRows : p.rows) - k0;
+    const int64_t k0 = low * kStageRows, k = (high * kStageRows < all_rows ? high * kStageRows : all_rows) - k0;
     P c;
     c.clear();
     if (low < high) {
-        const Matrix x = {reinterpret_cast<const char*>(p.x + k0 * p.hidden + h0), (int64_t)p.hidden * 2, columns};
-        const Matrix d = {reinterpret_cast<const char*>(p.d + (of_up * p.rows + k0) * p.inner + i0),
+        const Matrix x = {reinterpret_cast<const char*>((p.x_twice ? p.x_twice : p.x) + k0 * p.hidden + h0),
+                          (int64_t)p.hidden * 2, columns};
+        const Matrix d = {reinterpret_cast<const char*>(p.d + (of_up * all_rows + k0) * p.inner + i0),
                           (int64_t)p.inner * 2, rows};
         typename P::LoadA la(x, wave * P::kLoadsA, k, lane);
         typename P::LoadB lb(d, wave * P::kLoadsB, k, lane);
@@ -227,13 +264,13 @@ void feed_forward_dw_kernel(const BwdParams p)
     int e = 0;
     if constexpr (F16)
         e = p.rows ? stored_exponent<64 * P::kWaves>(p, reinterpret_cast<float*>(lds)) : 0;
-    float* part = p.splits > 1 ? p.parts + ((int64_t)split * 2 + of_up) * p.inner * p.hidden : nullptr;
+    float* part = p.parts ? p.parts + ((int64_t)split * 2 + of_up) * p.inner * p.hidden : nullptr;
     store<F16>(c, of_up ? p.dw_up : p.dw_gate, part, i0 + 32 * P::first_b(wave), p.inner,
                h0 + 32 * P::first_a(wave), p.hidden, e, lane);
 }
 
-// Adds the splits' parts in order: `first` and `second` are the halves of what they
-// are parts of (`elements` each; no second for dx).
+// Adds `splits` parts in order (the splits', and for dx each term's): `first` and
+// `second` are the halves of what they are parts of (`elements` each; no second for dx).
 template <bool F16>
 __global__ __launch_bounds__(kThreads)
 void feed_forward_join_kernel(const BwdParams p, uint16_t* first, uint16_t* second, int64_t elements)
@@ -298,20 +335,23 @@ int64_t element_blocks(int64_t elements)
 // How both products are cut, and where the workspace's parts begin (in bytes).
 struct Shape {
     qkr_ff_host::Cut dx, dw;
-    int64_t largest, parts, bytes;
+    int64_t terms, blocks, x_twice, largest, parts, bytes;
 };
 
 Shape shape_of(const dit_ff_args& a)
 {
     Shape s;
-    s.dx = qkr_ff_host::cut_of(a.rows, a.hidden, 2 * (((int64_t)a.inner + kStageRows - 1) / kStageRows), true);
-    s.dw = qkr_ff_host::cut_of(2 * (int64_t)a.inner, a.hidden, (a.rows + kStageRows - 1) / kStageRows, true);
+    s.terms = qkr_ff_host::terms_of(a);
+    s.dx = qkr_ff_host::cut_of(s.terms * a.rows, a.hidden, 2 * (((int64_t)a.inner + kStageRows - 1) / kStageRows), true);
+    s.dw = qkr_ff_host::cut_of(2 * (int64_t)a.inner, a.hidden, (s.terms * a.rows + kStageRows - 1) / kStageRows, true);
     // tiles of one weight each
     const int64_t side = s.dw.large ? 256 : 128;
     s.dw.row_tiles = 2 * ((a.inner + side - 1) / side);
-    s.largest = 4 * a.rows * a.inner;
-    s.parts = s.largest + (a.dtype == QKR_FP16 ? (element_blocks(a.rows * a.inner) * 4 + 15) / 16 * 16 : 0);
-    const int64_t dx = s.dx.splits > 1 ? s.dx.splits * a.rows * a.hidden * 4 : 0;
+    s.blocks = element_blocks(a.rows * (s.terms == 2 && a.hidden > a.inner ? a.hidden : a.inner));
+    s.x_twice = 4 * s.terms * a.rows * a.inner;
+    s.largest = s.x_twice + (s.terms == 2 ? 4 * a.rows * a.hidden : 0);
+    s.parts = s.largest + (a.dtype == QKR_FP16 ? (s.blocks * 4 + 15) / 16 * 16 : 0);
+    const int64_t dx_parts = s.dx.splits * s.terms, dx = dx_parts > 1 ? dx_parts * a.rows * a.hidden * 4 : 0;
     const int64_t dw = s.dw.splits > 1 ? s.dw.splits * 2 * a.inner * a.hidden * 4 : 0;
     s.bytes = a.rows == 0 ? 0 : s.parts + (dx > dw ? dx : dw);
     return s;
@@ -375,6 +415,9 @@ extern "C" int dit_gated_feed_forward_backward(const dit_ff_args* args, const vo
     p.dw_gate = static_cast<uint16_t*>(dw_gate);
     p.dw_up = static_cast<uint16_t*>(dw_up);
     p.d = static_cast<uint16_t*>(workspace);
+    p.terms = (int32_t)shape.terms;
+    p.x_twice = dw_gate && a.rows && shape.terms == 2
+                    ? reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + shape.x_twice) : nullptr;
     p.largest = reinterpret_cast<float*>(static_cast<char*>(workspace) + shape.largest);
     p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + shape.parts);
     p.rows = a.rows;
@@ -382,24 +425,29 @@ extern "C" int dit_gated_feed_forward_backward(const dit_ff_args* args, const vo
     p.inner = a.inner;
     const bool f16 = a.dtype == QKR_FP16, silu = a.activation == DIT_FF_SILU;
     if (a.rows) {
-        const int64_t blocks = element_blocks(a.rows * a.inner);
+        const int64_t blocks = shape.blocks;
         p.largest_blocks = f16 ? (uint32_t)blocks : 0;
         if (f16)
             rc = launch(silu ? feed_forward_largest_kernel<0> : feed_forward_largest_kernel<1>, blocks, p, stream);
         if (rc == QKR_OK)
             rc = launch(silu ? select_gradients<0>(f16) : select_gradients<1>(f16), blocks, p, stream);
     }
-    const auto product = [&](const Cut& cut, Fn fn, uint16_t* first, uint16_t* second, int64_t elements) {
+    float* const parts = p.parts;
+    // `count` parts of `elements` (first and second together) are to be added
+    const auto product = [&](const Cut& cut, Fn fn, int64_t count, uint16_t* first, uint16_t* second, int64_t elements) {
         p.row_tiles = (uint32_t)cut.row_tiles;
         p.column_tiles = (uint32_t)cut.column_tiles;
         p.splits = (int32_t)cut.splits;
+        p.parts = count > 1 ? parts : nullptr;
         rc = launch(fn, cut.row_tiles * cut.column_tiles * cut.splits, p, stream, cut.large ? 512 : 256);
-        if (rc == QKR_OK && cut.splits > 1 && join(p, first, second, elements, f16, stream) != hipSuccess)
+        p.splits = (int32_t)count;
+        if (rc == QKR_OK && count > 1 && join(p, first, second, elements, f16, stream) != hipSuccess)
             rc = QKR_ERR_HIP;
     };
     if (rc == QKR_OK && dx && a.rows)
-        product(shape.dx, select_dx(f16, shape.dx.large), p.dx, nullptr, a.rows * a.hidden);
+        product(shape.dx, select_dx(f16, shape.dx.large), shape.dx.splits * shape.terms, p.dx, nullptr, a.rows * a.hidden);
     if (rc == QKR_OK && dw_gate)
-        product(shape.dw, select_dw(f16, shape.dw.large), p.dw_gate, p.dw_up, (int64_t)a.inner * a.hidden);
+        product(shape.dw, select_dw(f16, shape.dw.large), shape.dw.splits, p.dw_gate, p.dw_up,
+                (int64_t)a.inner * a.hidden);
     return rc;
 }

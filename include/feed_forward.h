@@ -29,7 +29,9 @@
  * from the fp32 sums and rounded once; gate and up are rounded once where they
  * are kept.  dgate and dup are rounded to the tensors' type before the products
  * that use them (as the sums of 16-bit numbers that they enter would be off by
- * as much); for fp16 they are first scaled by a power of two, by the largest of
+ * as much; for up to 32 rows, and for 2^15 numbers with rows * hidden up to 2^20,
+ * what that leaves is added as a second operand, whose products with an infinity
+ * may be NaN); for fp16 they are first scaled by a power of two, by the largest of
  * them, so that small gradients do not sink into fp16's subnormals (one power for
  * the call: what lies below 2^-28 of the largest is off by up to 2^-39 of it).
  * Results do not depend on the order in which workgroups run (no atomic additions).

@@ -1,7 +1,7 @@
 // How the feed-forward products of a call are cut: compiled by
 // tests/test_feed_forward_cuts_cpu.py and run on the CPU.  Reads lines of rows,
 // hidden, inner and bytes a number; prints for each product (forward, dx, dw) the
-// side of its tiles, their number and the splits of k.
+// side of its tiles, their number and the splits of k, then the terms of dgate and dup.
 #include <stdio.h>
 
 #include "feed_forward_host.h"
@@ -16,9 +16,11 @@ int main()
     long long rows, hidden, inner, size;
     while (scanf("%lld %lld %lld %lld", &rows, &hidden, &inner, &size) == 4) {
         show(qkr_ff_host::cut_of(rows, 2 * inner, (hidden * size + 127) / 128, false));
-        show(qkr_ff_host::cut_of(rows, hidden, 2 * ((inner + 63) / 64), true));
-        show(qkr_ff_host::cut_of(2 * inner, hidden, (rows + 63) / 64, true));
-        printf("\n");
+        const dit_ff_args a = {rows, (int32_t)hidden, (int32_t)inner, DIT_FF_SILU, QKR_BF16, QKR_BF16};
+        const int terms = qkr_ff_host::terms_of(a);
+        show(qkr_ff_host::cut_of(terms * rows, hidden, 2 * ((inner + 63) / 64), true));
+        show(qkr_ff_host::cut_of(2 * inner, hidden, (terms * rows + 63) / 64, true));
+        printf("%d\n", terms);
     }
     return 0;
 }

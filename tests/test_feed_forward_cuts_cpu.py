@@ -23,11 +23,11 @@ def cuts(tmp_path_factory):
                     os.path.join(ROOT, "tests", "c_abi", "cuts_check.cpp"), "-o", exe], check=True)
 
     def of(rows, hidden, inner, size=2):
-        """(side, tiles, splits) of the forward product, dx and dw."""
+        """(side, tiles, splits) of the forward product, dx and dw, and the terms of dgate and dup."""
         out = subprocess.run([exe], input="%d %d %d %d\n" % (rows, hidden, inner, size), capture_output=True, text=True,
                              check=True, timeout=60).stdout
         v = [int(n) for n in out.split()]
-        return [tuple(v[i:i + 3]) for i in (0, 3, 6)]
+        return [tuple(v[i:i + 3]) for i in (0, 3, 6)] + [v[9]]
 
     return of
 
@@ -66,3 +66,12 @@ def test_sizes_of_other_tests(cuts, size, forward, dx, dw):
         if want:
             assert got[0] == want[0]
             assert got[2] > 1 if want[1] is True else got[2] == want[1]
+
+
+def test_terms(cuts):
+    """Two for up to 32 rows, and for 2^15 numbers of up to 2^20 of x."""
+    for size in ((1, 5120, 13824), (32, 8192, 16384), (33, 8, 992), (128, 8192, 256), (4096, 256, 8)):
+        assert cuts(*size)[3] == 2, size
+    for size in ((33, 5120, 13824), (33, 8, 1000), (129, 8192, 248), (4096, 264, 8), (4104, 8, 8), (32760, 40, 8),
+                 (4608, 6144, 16384)):
+        assert cuts(*size)[3] == 1, size
